@@ -35,7 +35,9 @@ typedef enum {
     QGEMV_E_K256 = 5,      /* I is not a multiple of 256 (MQ4-v2, FWHT-256)   */
     QGEMV_E_IDS = 6,       /* expert strides too small for one expert         */
     QGEMV_E_WORKSPACE = 7, /* workspace NULL or smaller than required         */
-    QGEMV_E_HIP = 8        /* the HIP runtime reported an error at launch     */
+    QGEMV_E_HIP = 8,       /* the HIP runtime reported an error at launch     */
+    QGEMV_E_ARG = 9        /* unknown type or activation, or an epilogue term
+                              that this call does not take                    */
 } qgemv_status;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -254,6 +256,132 @@ int qgemv_moe_topk_noalloc(const void *w, const float *scales, long long w_strid
                            long long s_stride, int E, const int32_t *ids, const float *gates,
                            int T, int K, const float *x, float *y, int I, int O, int gs,
                            void *stream);
+
+/*
+ * Products with an epilogue, for any number of rows (tokens).
+ *
+ * Type of x, bias, residual and y of one call; sums are f32 (of exact
+ * products of the decoded integer or fp8 values with x, the scales applied to
+ * each scale group's f32 sum) and y is rounded once.
+ */
+typedef enum { QGEMV_F32 = 0, QGEMV_BF16 = 1 } qgemv_dtype;
+
+/* v = act(a): silu a / (1 + e^-a); gelu a/2 (1 + erf(a / sqrt 2)); gelu_tanh
+ * a/2 (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))). */
+typedef enum {
+    QGEMV_ACT_NONE = 0,
+    QGEMV_ACT_RELU = 1,
+    QGEMV_ACT_SILU = 2,
+    QGEMV_ACT_GELU = 3,
+    QGEMV_ACT_GELU_TANH = 4
+} qgemv_act;
+
+/*
+ * What follows the product a = x . W^T of a call, W of O rows:
+ *     a += bias;  y = act(a) + residual                          (O columns)
+ * or, gated (O even; the first O/2 rows of W are the gate projection, the
+ * last O/2 the up projection):
+ *     a += bias;  y = act(a[:, :O/2]) * a[:, O/2:] + residual    (O/2 columns)
+ * A NULL qgemv_epilogue is the plain product.  The struct itself is host
+ * memory, read during the call; its pointers are device pointers.
+ *   bias      [O] (grouped products: [E][O]), or NULL
+ *   residual  one row per row of y, ld_residual elements apart, or NULL; it
+ *             may be y itself (same pointer and stride)
+ */
+typedef struct {
+    int act;                 /* qgemv_act                                      */
+    int gated;               /* 0 or 1                                         */
+    const void *bias;
+    const void *residual;
+    long long ld_residual;   /* elements; at least the columns of y            */
+} qgemv_epilogue;
+
+/*
+ * y = epilogue(x . W^T) with grouped-int4 W (layout as qgemv_i4g) for S >= 0
+ * rows of x (S = 0 launches nothing and accepts any pointers).
+ *   x  dtype [S] rows of I, ldx >= I elements apart;  y dtype [S] rows of O
+ *   (gated: O/2), ldy elements apart; nothing between or behind the rows is
+ *   read or written.  y must not overlap x, the weights or the bias.
+ *   x, y, bias and residual are aligned to their element, w to a byte.
+ *   workspace  device scratch of qgemv_linear_workspace bytes, 256-byte
+ *              aligned, overwritten; calls that may overlap in time (two
+ *              streams, two captured graphs) need one each.
+ * Any I >= 1 and any even gs.  gs % 32 == 0 with I % 32 == 0 and 16-byte
+ * aligned w takes the fast kernels; every other valid shape a slower general
+ * kernel with the same result definition.
+ * A row of x that holds an infinity or NaN gives a row of y without finite
+ * sums (infinities may come out as NaN); other rows are not affected.
+ */
+size_t qgemv_linear_workspace(int S, int I, int O, int dtype);
+int qgemv_i4g_linear(const void *w, const float *scales, const void *x, long long ldx, void *y,
+                     long long ldy, int S, int I, int O, int gs, int dtype,
+                     const qgemv_epilogue *epilogue, void *workspace, size_t ws_bytes,
+                     void *stream);
+
+/*
+ * The same with fp8-e4m3 W and 128x128 f32 block scales (layout as
+ * qgemv_fp8b128; blocks are counted over all O rows, gated or not).  Fast
+ * kernels: I % 32 == 0 and 16-byte aligned w.  A NaN code makes its column of
+ * y NaN.
+ */
+int qgemv_fp8b128_linear(const void *w, const float *scale_inv, const void *x, long long ldx,
+                         void *y, long long ldy, int S, int I, int O, int dtype,
+                         const qgemv_epilogue *epilogue, void *workspace, size_t ws_bytes,
+                         void *stream);
+
+/*
+ * Routed slots sorted by expert: the plan of the grouped product below, from
+ * the ids that qgemv_router_topk gives.  Slot (t, k) of expert ids[t][k] = e
+ * gets a row r in offsets[e] <= r < offsets[e + 1], rows of one expert in
+ * slot order (stable; the result does not depend on timing).
+ *   ids      int32 [T][K]; an id outside [0, E) gets no row
+ *   offsets  int32 [E + 1], offsets[0] = 0
+ *   tokens   int32 [T * K]: the token t of each row; -1 at and behind
+ *            offsets[E]
+ *   pos      int32 [T][K]: the row of each slot, -1 for an id out of range
+ *   1 <= E <= 1024, K >= 1, T * K <= 2^24; T = 0 gives all-zero offsets
+ *   workspace  qgemv_moe_group_workspace bytes (may be 0: then it may be
+ *              NULL), 4-byte aligned, overwritten
+ */
+size_t qgemv_moe_group_workspace(int T, int K, int E);
+int qgemv_moe_group(const int32_t *ids, int T, int K, int E, int32_t *offsets, int32_t *tokens,
+                    int32_t *pos, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Grouped product: rows offsets[e] .. offsets[e + 1] - 1 of y are
+ *     y[r] = epilogue(x[rows[r]] . W_e^T)       (x[r] where rows is NULL)
+ * with expert e's grouped-int4 W_e (strides as qgemv_moe_topk) and bias[e].
+ *   offsets  int32 [E + 1] device array, non-decreasing, within 0..R; other
+ *            values are clamped (nothing outside the buffers is touched)
+ *   rows     int32 [R] device array or NULL; an index outside [0, T) makes
+ *            its row of y NaN
+ *   x [T] rows (T >= R where rows is NULL);  y [R] rows; rows of y before
+ *   offsets[0] and from offsets[E] on are left as they were
+ *   1 <= E <= 1024; R = 0 launches nothing; the epilogue's residual must be
+ *   NULL
+ *   workspace  qgemv_grouped_workspace bytes, 256-byte aligned
+ * Row counts per expert stay on the device.
+ */
+size_t qgemv_grouped_workspace(int T, int R, int E, int I, int O, int dtype);
+int qgemv_i4g_grouped(const void *w, const float *scales, long long w_stride, long long s_stride,
+                      int E, const int32_t *offsets, const int32_t *rows, const void *x,
+                      long long ldx, int T, void *y, long long ldy, int R, int I, int O, int gs,
+                      int dtype, const qgemv_epilogue *epilogue, void *workspace,
+                      size_t ws_bytes, void *stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *     y[t] = sum_k gates[t][k] * h[pos[t][k]]  (+ residual[t])
+ * summed in f32 over k in ascending order (no atomics), rounded once.
+ *   h        dtype [R] rows of O, ldh elements apart
+ *   pos      int32 [T][K] as qgemv_moe_group gives; an index outside [0, R)
+ *            makes row t of y NaN (it is never dereferenced)
+ *   gates    f32 [T][K];  residual dtype rows ldr apart, or NULL (may be y)
+ *   T = 0 launches nothing; 1 <= K <= 64
+ */
+int qgemv_moe_combine(const void *h, long long ldh, int R, const int32_t *pos,
+                      const float *gates, int T, int K, int O, const void *residual,
+                      long long ldr, void *y, long long ldy, int dtype, void *stream);
 
 /*
  * Decode-only entry points: write the decoded f32 weights W[O][I], each the

@@ -7,8 +7,9 @@ library is missing or a call is refused, an exception is raised.
 Two layers:
 * ``qgemv_*`` -- the C ABI under the same names, taking raw device pointers
   (ints), sizes and a stream handle, returning the status code;
-* ``i4g``, ``fp8b128``, ``mq4v2``, ``fwht256``, ``moe_topk``, ``dequant_*`` --
-  take torch tensors on the current CUDA (HIP) device, allocate the output
+* ``i4g``, ``fp8b128``, ``mq4v2``, ``fwht256``, ``moe_topk``, ``dequant_*``,
+  ``i4g_linear``, ``fp8b128_linear``, ``moe_group``, ``i4g_grouped``,
+  ``moe_combine`` -- take torch tensors on the current CUDA (HIP) device, allocate the output
   with ``torch.empty``, launch on ``torch.cuda.current_stream()`` and raise
   ``QgemvError`` on a refusal.
 """
@@ -21,6 +22,16 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libqgemv.so")
 
 QGEMV_MAX_S = 8
+
+# qgemv_act
+ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+class Epilogue(C.Structure):
+    """qgemv_epilogue (host struct of device pointers)."""
+    _fields_ = [("act", C.c_int), ("gated", C.c_int), ("bias", C.c_void_p),
+                ("residual", C.c_void_p), ("ld_residual", C.c_longlong)]
+
 
 # every entry point declared in include/qgemv.h
 _SIGS = {
@@ -57,6 +68,25 @@ _SIGS = {
                                          C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_int,
                                          C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
                                          C.c_void_p]),
+    "qgemv_linear_workspace": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
+    "qgemv_i4g_linear": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_longlong, C.c_void_p,
+                                   C.c_longlong, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,
+                                   C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qgemv_fp8b128_linear": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_longlong,
+                                       C.c_void_p, C.c_longlong, C.c_int, C.c_int, C.c_int,
+                                       C.c_int, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qgemv_moe_group_workspace": (C.c_size_t, [C.c_int, C.c_int, C.c_int]),
+    "qgemv_moe_group": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
+                                  C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qgemv_grouped_workspace": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,
+                                             C.c_int]),
+    "qgemv_i4g_grouped": (C.c_int, [C.c_void_p, C.c_void_p, C.c_longlong, C.c_longlong, C.c_int,
+                                    C.c_void_p, C.c_void_p, C.c_void_p, C.c_longlong, C.c_int,
+                                    C.c_void_p, C.c_longlong, C.c_int, C.c_int, C.c_int, C.c_int,
+                                    C.c_int, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qgemv_moe_combine": (C.c_int, [C.c_void_p, C.c_longlong, C.c_int, C.c_void_p, C.c_void_p,
+                                    C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_longlong,
+                                    C.c_void_p, C.c_longlong, C.c_int, C.c_void_p]),
     "qgemv_dequant_i4g": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p,
                                     C.c_int, C.c_int, C.c_int, C.c_void_p]),
     "qgemv_dequant_fp8b128": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p,
@@ -178,6 +208,45 @@ def qgemv_moe_topk_noalloc(w, scales, w_stride, s_stride, E, ids, gates, T, K, x
                            stream):
     return lib().qgemv_moe_topk_noalloc(w, scales, w_stride, s_stride, E, ids, gates, T, K, x, y,
                                         I, O, gs, stream)
+
+
+def qgemv_linear_workspace(S, I, O, dtype):
+    return lib().qgemv_linear_workspace(S, I, O, dtype)
+
+
+def qgemv_i4g_linear(w, scales, x, ldx, y, ldy, S, I, O, gs, dtype, epilogue, workspace, ws_bytes,
+                     stream):
+    return lib().qgemv_i4g_linear(w, scales, x, ldx, y, ldy, S, I, O, gs, dtype, epilogue,
+                                  workspace, ws_bytes, stream)
+
+
+def qgemv_fp8b128_linear(w, scale_inv, x, ldx, y, ldy, S, I, O, dtype, epilogue, workspace,
+                         ws_bytes, stream):
+    return lib().qgemv_fp8b128_linear(w, scale_inv, x, ldx, y, ldy, S, I, O, dtype, epilogue,
+                                      workspace, ws_bytes, stream)
+
+
+def qgemv_moe_group_workspace(T, K, E):
+    return lib().qgemv_moe_group_workspace(T, K, E)
+
+
+def qgemv_moe_group(ids, T, K, E, offsets, tokens, pos, workspace, ws_bytes, stream):
+    return lib().qgemv_moe_group(ids, T, K, E, offsets, tokens, pos, workspace, ws_bytes, stream)
+
+
+def qgemv_grouped_workspace(T, R, E, I, O, dtype):
+    return lib().qgemv_grouped_workspace(T, R, E, I, O, dtype)
+
+
+def qgemv_i4g_grouped(w, scales, w_stride, s_stride, E, offsets, rows, x, ldx, T, y, ldy, R, I, O,
+                      gs, dtype, epilogue, workspace, ws_bytes, stream):
+    return lib().qgemv_i4g_grouped(w, scales, w_stride, s_stride, E, offsets, rows, x, ldx, T, y,
+                                   ldy, R, I, O, gs, dtype, epilogue, workspace, ws_bytes, stream)
+
+
+def qgemv_moe_combine(h, ldh, R, pos, gates, T, K, O, residual, ldr, y, ldy, dtype, stream):
+    return lib().qgemv_moe_combine(h, ldh, R, pos, gates, T, K, O, residual, ldr, y, ldy, dtype,
+                                   stream)
 
 
 def qgemv_dequant_i4g(w, scales, W, I, O, gs, stream):
@@ -466,6 +535,213 @@ def moe_topk_error(workspace):
     flag = C.c_int(0)
     _call("qgemv_moe_topk_error", _dev(workspace, "workspace"), C.byref(flag), _stream())
     return flag.value
+
+
+# -- products with an epilogue, routed slots -------------------------------
+# x, bias, residual and y of one call share a type, float32 or bfloat16.
+# x, residual, h and a caller's out may be row-strided views (columns
+# contiguous); everything else is contiguous.  The launch goes to the device
+# of the tensors, on its current stream.
+def _dtype_code(t, name):
+    torch = _torch()
+    if isinstance(t, torch.Tensor):
+        if t.dtype == torch.float32:
+            return 0
+        if t.dtype == torch.bfloat16:
+            return 1
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+
+
+def _rows(t, name, dtype, shape=None):
+    """(pointer, row stride in elements) of a 2-D tensor with contiguous rows."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if shape is not None:
+        _shape(t, name, shape)
+    n, width = t.shape
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if n <= 1:
+        return t.data_ptr(), max(t.stride(0), width)
+    if t.stride(0) < width:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return t.data_ptr(), t.stride(0)
+
+
+def _epilogue(dtype, O, bias, act, gated, residual, rows, E=None):
+    """(Epilogue or None, columns of y); E: bias is [E][O]."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(k for k in ACTIVATIONS if k)} or None")
+    if gated and O % 2:
+        raise ValueError("a gated product needs an even number of rows in w")
+    oc = O // 2 if gated else O
+    if bias is None and act is None and not gated and residual is None:
+        return None, oc
+    e = Epilogue(ACTIVATIONS[act], int(bool(gated)), None, None, 0)
+    if bias is not None:
+        e.bias = _dev(bias, "bias", dtype)
+        _shape(bias, "bias", (O,) if E is None else (E, O))
+    if residual is not None:
+        e.residual, e.ld_residual = _rows(residual, "residual", dtype, (rows, oc))
+    return e, oc
+
+
+def _ref(e):
+    return C.addressof(e) if e is not None else None
+
+
+def _scratch(workspace, need, device):
+    """The caller's workspace (checked) or a new one; (tensor, pointer)."""
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(max(int(need), 1), dtype=torch.uint8, device=device)
+    elif workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    return workspace, _dev(workspace, "workspace", torch.uint8)
+
+
+def _linear(fn, w, scales, x, gs, bias, act, gated, residual, workspace, out):
+    torch = _torch()
+    code = _dtype_code(x, "x")
+    one = x.dim() == 1
+    if one:
+        x = x.unsqueeze(0)
+        residual = residual.unsqueeze(0) if residual is not None and residual.dim() == 1 \
+            else residual
+        out = out.unsqueeze(0) if out is not None and out.dim() == 1 else out
+    if x.dim() != 2:
+        raise ValueError("x must be [I] or [S, I]")
+    S, I = x.shape
+    O = _i4g_check(w, scales, x, gs, S, I) if gs is not None else _fp8_check(w, scales, I,
+                                                                             "scale_inv")
+    _one_device(w, scales, x, bias, residual, workspace, out)
+    xp, ldx = _rows(x, "x", x.dtype)
+    epi, oc = _epilogue(x.dtype, O, bias, act, gated, residual, S)
+    y = out if out is not None else torch.empty((S, oc), dtype=x.dtype, device=x.device)
+    yp, ldy = _rows(y, "out", x.dtype, (S, oc))
+    wp, sp = _dev(w, "w", torch.uint8), _dev(scales, "scales", torch.float32)
+    with torch.cuda.device(x.device):
+        ws, wsp = _scratch(workspace, qgemv_linear_workspace(S, I, O, code), x.device)
+        args = (wp, sp, xp, ldx, yp, ldy, S, I, O) + ((gs,) if gs is not None else ())
+        _call(fn, *args, code, _ref(epi), wsp, ws.numel(), _stream())
+    return y[0] if one else y
+
+
+def linear_workspace(S, I, O, dtype, device):
+    """Scratch for one i4g_linear or fp8b128_linear call of these sizes."""
+    torch = _torch()
+    code = _dtype_code(torch.empty(0, dtype=dtype), "dtype")
+    return torch.empty(max(int(qgemv_linear_workspace(S, I, O, code)), 1), dtype=torch.uint8,
+                       device=device)
+
+
+def i4g_linear(w, scales, x, gs, bias=None, act=None, gated=False, residual=None, workspace=None,
+               out=None):
+    """y = act(x W^T + bias) + residual with grouped-int4 W, any number of rows.
+
+    w u8 [O][(I+1)//2], scales f32 [O][ng], x [S][I] (or [I]) f32 or bf16, bias
+    [O], residual and y [S][O] of x's type.  gated: w holds the gate rows, then
+    the up rows, y = act(gate) * up (+ residual) has O/2 columns.  act: None,
+    "relu", "silu", "gelu" or "gelu_tanh".
+    """
+    return _linear("qgemv_i4g_linear", w, scales, x, _gs(gs), bias, act, gated, residual,
+                   workspace, out)
+
+
+def fp8b128_linear(w, scale_inv, x, bias=None, act=None, gated=False, residual=None,
+                   workspace=None, out=None):
+    """i4g_linear's product with fp8-e4m3 W [O][I] and 128x128 block scales."""
+    return _linear("qgemv_fp8b128_linear", w, scale_inv, x, None, bias, act, gated, residual,
+                   workspace, out)
+
+
+def moe_group(ids, E, workspace=None):
+    """Routed slots sorted by expert: ids int32 [T][K] -> (offsets int32 [E+1],
+    tokens int32 [T*K], pos int32 [T][K]); see qgemv_moe_group."""
+    torch = _torch()
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, K]")
+    T, K = ids.shape
+    _one_device(ids, workspace)
+    ip = _dev(ids, "ids", torch.int32)
+    offsets = torch.empty(min(max(int(E), 0), 1024) + 1, dtype=torch.int32, device=ids.device)
+    tokens = torch.empty(T * K, dtype=torch.int32, device=ids.device)
+    pos = torch.empty((T, K), dtype=torch.int32, device=ids.device)
+    with torch.cuda.device(ids.device):
+        ws, wsp = _scratch(workspace, qgemv_moe_group_workspace(T, K, E), ids.device)
+        _call("qgemv_moe_group", ip, T, K, E, _dev(offsets, "offsets"), _dev(tokens, "tokens"),
+              _dev(pos, "pos"), wsp, ws.numel(), _stream())
+    return offsets, tokens, pos
+
+
+def grouped_workspace(T, R, E, I, O, dtype, device):
+    """Scratch for one i4g_grouped call of these sizes."""
+    torch = _torch()
+    code = _dtype_code(torch.empty(0, dtype=dtype), "dtype")
+    return torch.empty(max(int(qgemv_grouped_workspace(T, R, E, I, O, code)), 1),
+                       dtype=torch.uint8, device=device)
+
+
+def i4g_grouped(w, scales, x, offsets, gs, rows=None, bias=None, act=None, gated=False,
+                workspace=None, out=None):
+    """Each expert's rows times its grouped-int4 matrix, with i4g_linear's bias,
+    activation and gate: w u8 [E][O][rb], scales f32 [E][O][ng], offsets int32
+    [E+1], bias [E][O].  Row r of y belongs to the expert e with offsets[e] <=
+    r < offsets[e+1] and reads x[rows[r]] (x[r] without rows); rows of no
+    expert are left as they are in ``out``."""
+    torch = _torch()
+    code = _dtype_code(x, "x")
+    gs = _gs(gs)
+    if w.dim() != 3 or x.dim() != 2:
+        raise ValueError("w must be [E, O, (I + 1) // 2] and x [T, I]")
+    E, O = w.shape[0], w.shape[1]
+    T, I = x.shape
+    R = T if rows is None else rows.numel()
+    _shape(w, "w", (E, O, (I + 1) // 2))
+    _shape(scales, "scales", (E, O, (I + gs - 1) // gs))
+    _shape(offsets, "offsets", (E + 1,))
+    if rows is not None:
+        _shape(rows, "rows", (R,))
+    _one_device(w, scales, x, offsets, rows, bias, workspace, out)
+    xp, ldx = _rows(x, "x", x.dtype)
+    epi, oc = _epilogue(x.dtype, O, bias, act, gated, None, R, E)
+    y = out if out is not None else torch.empty((R, oc), dtype=x.dtype, device=x.device)
+    yp, ldy = _rows(y, "out", x.dtype, (R, oc))
+    wp, sp = _dev(w, "w", torch.uint8), _dev(scales, "scales", torch.float32)
+    op = _dev(offsets, "offsets", torch.int32)
+    rp = _dev(rows, "rows", torch.int32) if rows is not None else None
+    with torch.cuda.device(x.device):
+        ws, wsp = _scratch(workspace, qgemv_grouped_workspace(T, R, E, I, O, code), x.device)
+        _call("qgemv_i4g_grouped", wp, sp, O * w.shape[2], O * scales.shape[2], E, op, rp, xp,
+              ldx, T, yp, ldy, R, I, O, gs, code, _ref(epi), wsp, ws.numel(), _stream())
+    return y
+
+
+def moe_combine(h, pos, gates, residual=None, out=None):
+    """y[t] = sum_k gates[t][k] h[pos[t][k]] (+ residual[t]): h [R][O] f32 or
+    bf16, pos int32 [T][K], gates f32 [T][K], residual and y [T][O]."""
+    torch = _torch()
+    code = _dtype_code(h, "h")
+    if pos.dim() != 2 or h.dim() != 2:
+        raise ValueError("h must be [R, O] and pos [T, K]")
+    T, K = pos.shape
+    R, O = h.shape
+    _shape(gates, "gates", (T, K))
+    _one_device(h, pos, gates, residual, out)
+    hp, ldh = _rows(h, "h", h.dtype)
+    rp, ldr = _rows(residual, "residual", h.dtype, (T, O)) if residual is not None else (None, 0)
+    y = out if out is not None else torch.empty((T, O), dtype=h.dtype, device=h.device)
+    yp, ldy = _rows(y, "out", h.dtype, (T, O))
+    with torch.cuda.device(h.device):
+        _call("qgemv_moe_combine", hp, ldh, R, _dev(pos, "pos", torch.int32),
+              _dev(gates, "gates", torch.float32), T, K, O, rp, ldr, yp, ldy, code, _stream())
+    return y
 
 
 def dequant_i4g(w, scales, I, gs):

@@ -1,0 +1,202 @@
+// abi_linear.hip -- the extern "C" entry points of the products with an
+// epilogue and of the routed slots: argument validation, then launch.
+//
+// As in abi.hip, validation looks at pointer values, dimensions and sizes
+// only, so a refused call is safe with any pointers.
+#include "qg_linear.h"
+
+namespace {
+
+constexpr int MAX_DIM = 1 << 24;
+constexpr int MAX_EXPERTS = 1024;
+
+bool misaligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) != 0; }
+
+int launched(hipError_t e) { return e == hipSuccess ? QGEMV_OK : QGEMV_E_HIP; }
+
+bool bad_dtype(int dtype) { return dtype != QGEMV_F32 && dtype != QGEMV_BF16; }
+
+int element(int dtype) { return dtype == QGEMV_BF16 ? 2 : 4; }
+
+bool bad_sizes(int rows, int I, int O)
+{
+    return rows < 0 || rows > MAX_DIM || I < 1 || O < 1 || I > MAX_DIM || O > MAX_DIM;
+}
+
+// 64 x 64 tiles of y, the smallest of all kernels, must fit a launch
+bool too_many_tiles(long long row_tiles, int oc)
+{
+    return row_tiles * ((oc + 15) / 16) > 0x7FFFFFFFLL;
+}
+
+// Fills a's type, strides and epilogue from the arguments and checks them.
+int take(qg::LinearArgs &a, const qgemv_epilogue *e, bool with_residual)
+{
+    if (bad_dtype(a.dtype)) return QGEMV_E_ARG;
+    a.act = e ? e->act : QGEMV_ACT_NONE;
+    a.gated = e ? e->gated : 0;
+    a.bias = e ? e->bias : nullptr;
+    a.residual = e ? e->residual : nullptr;
+    a.ldr = a.residual ? e->ld_residual : 0;
+    if (a.act < QGEMV_ACT_NONE || a.act > QGEMV_ACT_GELU_TANH || (a.gated != 0 && a.gated != 1))
+        return QGEMV_E_ARG;
+    if (a.residual && !with_residual) return QGEMV_E_ARG;
+    if (a.gated && (a.O & 1)) return QGEMV_E_DIMS;
+    const int oc = a.gated ? a.O / 2 : a.O;
+    if (a.ldx < a.I || a.ldy < oc || (a.residual && a.ldr < oc)) return QGEMV_E_DIMS;
+    const uintptr_t el = element(a.dtype);
+    if (misaligned(a.scales, 4) || misaligned(a.x, el) || misaligned(a.y, el) ||
+        misaligned(a.bias, el) || misaligned(a.residual, el))
+        return QGEMV_E_ALIGN;
+    return QGEMV_OK;
+}
+
+int dense(qg::WeightFormat fmt, const void *w, const float *scales, const void *x, long long ldx,
+          void *y, long long ldy, int S, int I, int O, int gs, int dtype,
+          const qgemv_epilogue *epilogue, void *workspace, size_t ws_bytes, void *stream)
+{
+    if (bad_sizes(S, I, O)) return QGEMV_E_DIMS;
+    if (gs < 2 || (gs & 1) || gs > MAX_DIM) return QGEMV_E_GS;
+    if (S > 0 && (!w || !scales || !x || !y)) return QGEMV_E_NULL;
+    qg::LinearArgs a{};
+    a.w = static_cast<const uint8_t *>(w);
+    a.scales = scales;
+    a.x = x;
+    a.y = y;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.T = a.R = S;
+    a.E = 1;
+    a.I = I;
+    a.O = O;
+    a.gs = gs;
+    a.ng = (I + gs - 1) / gs;
+    a.dtype = dtype;
+    if (int e = take(a, epilogue, true)) return e;
+    if (S == 0) return QGEMV_OK;
+    if (too_many_tiles((S + 15) / 16, O)) return QGEMV_E_DIMS;
+    if (!workspace || misaligned(workspace, 256) ||
+        ws_bytes < qg::linear_workspace(S, S, 0, I, O, dtype))
+        return QGEMV_E_WORKSPACE;
+    return launched(qg::launch_linear(fmt, a, workspace, (hipStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qgemv_linear_workspace(int S, int I, int O, int dtype)
+{
+    if (bad_sizes(S, I, O) || bad_dtype(dtype)) return 0;
+    return qg::linear_workspace(S, S, 0, I, O, dtype);
+}
+
+int qgemv_i4g_linear(const void *w, const float *scales, const void *x, long long ldx, void *y,
+                     long long ldy, int S, int I, int O, int gs, int dtype,
+                     const qgemv_epilogue *epilogue, void *workspace, size_t ws_bytes,
+                     void *stream)
+{
+    return dense(qg::FMT_I4G, w, scales, x, ldx, y, ldy, S, I, O, gs, dtype, epilogue, workspace,
+                 ws_bytes, stream);
+}
+
+int qgemv_fp8b128_linear(const void *w, const float *scale_inv, const void *x, long long ldx,
+                         void *y, long long ldy, int S, int I, int O, int dtype,
+                         const qgemv_epilogue *epilogue, void *workspace, size_t ws_bytes,
+                         void *stream)
+{
+    return dense(qg::FMT_FP8, w, scale_inv, x, ldx, y, ldy, S, I, O, 128, dtype, epilogue,
+                 workspace, ws_bytes, stream);
+}
+
+size_t qgemv_grouped_workspace(int T, int R, int E, int I, int O, int dtype)
+{
+    if (bad_sizes(R, I, O) || T < 0 || T > MAX_DIM || E < 1 || E > MAX_EXPERTS ||
+        bad_dtype(dtype))
+        return 0;
+    return qg::linear_workspace(T, R, E, I, O, dtype);
+}
+
+int qgemv_i4g_grouped(const void *w, const float *scales, long long w_stride, long long s_stride,
+                      int E, const int32_t *offsets, const int32_t *rows, const void *x,
+                      long long ldx, int T, void *y, long long ldy, int R, int I, int O, int gs,
+                      int dtype, const qgemv_epilogue *epilogue, void *workspace,
+                      size_t ws_bytes, void *stream)
+{
+    if (bad_sizes(R, I, O) || E < 1 || E > MAX_EXPERTS || T < 0 || T > MAX_DIM)
+        return QGEMV_E_DIMS;
+    if (R > 0 && (rows ? T < 1 : T < R)) return QGEMV_E_DIMS;
+    if (gs < 2 || (gs & 1) || gs > MAX_DIM) return QGEMV_E_GS;
+    if (R > 0 && (!w || !scales || !offsets || !x || !y)) return QGEMV_E_NULL;
+    if (misaligned(offsets, 4) || misaligned(rows, 4)) return QGEMV_E_ALIGN;
+    const long long rb = ((long long)I + 1) / 2, ng = ((long long)I + gs - 1) / gs;
+    if (w_stride < (long long)O * rb || s_stride < (long long)O * ng) return QGEMV_E_IDS;
+    qg::LinearArgs a{};
+    a.w = static_cast<const uint8_t *>(w);
+    a.scales = scales;
+    a.w_stride = w_stride;
+    a.s_stride = s_stride;
+    a.x = x;
+    a.y = y;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.rows = rows;
+    a.offsets = offsets;
+    a.T = T;
+    a.R = R;
+    a.E = E;
+    a.I = I;
+    a.O = O;
+    a.gs = gs;
+    a.ng = (int)ng;
+    a.dtype = dtype;
+    if (int e = take(a, epilogue, false)) return e;
+    if (R == 0) return QGEMV_OK;
+    if (too_many_tiles((long long)R / 16 + (E < R ? E : R), O)) return QGEMV_E_DIMS;
+    if (!workspace || misaligned(workspace, 256) ||
+        ws_bytes < qg::linear_workspace(T, R, E, I, O, dtype))
+        return QGEMV_E_WORKSPACE;
+    return launched(qg::launch_linear(qg::FMT_I4G, a, workspace, (hipStream_t)stream));
+}
+
+size_t qgemv_moe_group_workspace(int T, int K, int E)
+{
+    if (T < 0 || K < 1 || E < 1 || E > MAX_EXPERTS || (long long)T * K > MAX_DIM) return 0;
+    return qg::moe_group_workspace(T, K, E);
+}
+
+int qgemv_moe_group(const int32_t *ids, int T, int K, int E, int32_t *offsets, int32_t *tokens,
+                    int32_t *pos, void *workspace, size_t ws_bytes, void *stream)
+{
+    if (T < 0 || K < 1 || E < 1 || E > MAX_EXPERTS || (long long)T * K > MAX_DIM)
+        return QGEMV_E_DIMS;
+    if (!offsets || (T > 0 && (!ids || !tokens || !pos))) return QGEMV_E_NULL;
+    if (misaligned(ids, 4) || misaligned(offsets, 4) || misaligned(tokens, 4) ||
+        misaligned(pos, 4))
+        return QGEMV_E_ALIGN;
+    const size_t need = qg::moe_group_workspace(T, K, E);
+    if (need > 0 && (!workspace || misaligned(workspace, 4) || ws_bytes < need))
+        return QGEMV_E_WORKSPACE;
+    return launched(qg::launch_moe_group(ids, T, K, E, offsets, tokens, pos, workspace,
+                                         (hipStream_t)stream));
+}
+
+int qgemv_moe_combine(const void *h, long long ldh, int R, const int32_t *pos,
+                      const float *gates, int T, int K, int O, const void *residual,
+                      long long ldr, void *y, long long ldy, int dtype, void *stream)
+{
+    if (T < 0 || T > MAX_DIM || R < 0 || R > MAX_DIM || K < 1 || K > 64 || O < 1 || O > MAX_DIM)
+        return QGEMV_E_DIMS;
+    if (bad_dtype(dtype)) return QGEMV_E_ARG;
+    if (T > 0 && (!pos || !gates || !y || (R > 0 && !h))) return QGEMV_E_NULL;
+    if (ldh < O || ldy < O || (residual && ldr < O)) return QGEMV_E_DIMS;
+    const uintptr_t el = element(dtype);
+    if (misaligned(h, el) || misaligned(y, el) || misaligned(residual, el) ||
+        misaligned(pos, 4) || misaligned(gates, 4))
+        return QGEMV_E_ALIGN;
+    if (T == 0) return QGEMV_OK;
+    return launched(qg::launch_moe_combine(h, ldh, R, pos, gates, T, K, O, residual, ldr, y, ldy,
+                                           dtype, (hipStream_t)stream));
+}
+
+}  // extern "C"

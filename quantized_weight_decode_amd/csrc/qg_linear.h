@@ -1,0 +1,113 @@
+// qg_linear.h -- launchers and device helpers of the many-token products with
+// an epilogue (dense and grouped by expert) and of the routed slots.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "qgemv.h"
+
+namespace qg {
+
+enum WeightFormat { FMT_I4G = 0, FMT_FP8 = 1 };
+
+// One product Y = epilogue(X . W^T), dense (tiles == nullptr) or grouped.
+struct LinearArgs {
+    const uint8_t *w;
+    const float *scales;
+    long long w_stride, s_stride;   // from one expert to the next (bytes, floats)
+    const void *x;                  // [T][ldx], type dtype
+    void *y;                        // [R][ldy], type dtype
+    long long ldx, ldy, ldr;        // row strides in elements
+    const void *bias;               // [O] per expert, or nullptr
+    const void *residual;           // [R][ldr], or nullptr
+    const int32_t *rows;            // grouped: row of x for each row of y, or nullptr
+    const int32_t *offsets;         // grouped: [E + 1] device array, else nullptr
+    int T, R, E;                    // rows of x, rows of y, experts (dense: T == R, E == 1)
+    int I, O, gs, ng;               // ng: scales per row of W (i4g) or of blocks (fp8)
+    int dtype, act, gated;
+};
+
+// Workspace bytes of a product (an upper bound over its kernels; a function
+// of these sizes only).  E = 0: dense.
+size_t linear_workspace(int T, int R, int E, int I, int O, int dtype);
+hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStream_t st);
+
+// routed slots: sort by expert, and the gate-weighted return
+size_t moe_group_workspace(int T, int K, int E);
+hipError_t launch_moe_group(const int32_t *ids, int T, int K, int E, int32_t *offsets,
+                            int32_t *tokens, int32_t *pos, void *ws, hipStream_t st);
+hipError_t launch_moe_combine(const void *h, long long ldh, int R, const int32_t *pos,
+                              const float *gates, int T, int K, int O, const void *residual,
+                              long long ldr, void *y, long long ldy, int dtype, hipStream_t st);
+
+}  // namespace qg
+
+namespace qg {
+
+// -- element types -----------------------------------------------------------
+struct F32 {
+    typedef float raw;
+    static __device__ __forceinline__ float get(raw v) { return v; }
+    static __device__ __forceinline__ raw put(float v) { return v; }
+};
+struct BF16 {
+    typedef uint16_t raw;
+    static __device__ __forceinline__ float get(raw v)
+    {
+        return __builtin_bit_cast(float, (uint32_t)v << 16);
+    }
+    // round to nearest even (the type's one rounding of a result)
+    static __device__ __forceinline__ raw put(float v)
+    {
+        return __builtin_bit_cast(uint16_t, (__bf16)v);
+    }
+};
+
+// -- epilogue ----------------------------------------------------------------
+// act(a) in f32.  silu a / (1 + e^-a); gelu a/2 (1 + erf(a / sqrt 2)), written
+// with erfc for negative a, where 1 + erf cancels; gelu_tanh the tanh form,
+// a * sigmoid(2u).
+__device__ __forceinline__ float activate(float a, int act)
+{
+    switch (act) {
+    case QGEMV_ACT_RELU: return a < 0.0f ? 0.0f : a;             // NaN stays NaN
+    case QGEMV_ACT_SILU: return a / (1.0f + expf(-a));
+    case QGEMV_ACT_GELU: {
+        const float z = a * 0.70710678118654752f;
+        return a * (z < 0.0f ? 0.5f * erfcf(-z) : 0.5f + 0.5f * erff(z));
+    }
+    case QGEMV_ACT_GELU_TANH: {
+        const float u = 0.79788456080286536f * (a + 0.044715f * a * a * a);
+        return a / (1.0f + expf(-2.0f * u));
+    }
+    default: return a;
+    }
+}
+
+// The end of one output: bias and activation (and gate), residual, store.
+// c is the output column, row the row of y; up only where gated.
+template <typename XT>
+__device__ __forceinline__ void finish(const LinearArgs &a, int expert, int row, int c,
+                                       float acc, float up)
+{
+    typedef typename XT::raw raw;
+    if (a.bias) {
+        const raw *b = static_cast<const raw *>(a.bias) + (size_t)expert * a.O;
+        acc += XT::get(b[c]);
+        if (a.gated) up += XT::get(b[a.O / 2 + c]);
+    }
+    float v = activate(acc, a.act);
+    if (a.gated) v *= up;
+    if (a.residual)
+        v += XT::get(static_cast<const raw *>(a.residual)[(size_t)row * a.ldr + c]);
+    static_cast<raw *>(a.y)[(size_t)row * a.ldy + c] = XT::put(v);
+}
+
+// One tile of rows: rows [row0, row0 + n) of y, all of one expert.
+struct RowTile {
+    int expert, row0, n, pad;
+};
+
+}  // namespace qg

@@ -1,0 +1,242 @@
+"""Products with an epilogue (i4g_linear, fp8b128_linear) on the GPU against
+64-bit references, elementwise within the bound derived in linear_util."""
+import numpy as np
+import pytest
+import torch
+
+import linear_util as L
+from gpu_util import dev, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+DT = [torch.float32, torch.bfloat16]
+# (S, I, O, gs): one row to several tiles, both sides of 16, 32, 64 and 128
+# rows; odd and tiny I and O; group sizes in and out of whole 32 columns
+SHAPES = [(1, 512, 256, 64), (1, 1, 1, 2), (2, 6144, 130, 64), (3, 64, 7, 32), (5, 3, 18, 2),
+          (15, 160, 66, 32), (16, 4096, 48, 128), (17, 33, 65, 2), (31, 96, 129, 96),
+          (33, 2048, 258, 64), (64, 416, 514, 32), (65, 100, 64, 48), (96, 1024, 300, 64),
+          (128, 640, 255, 128), (130, 1001, 257, 100), (257, 1536, 1026, 64),
+          (300, 2080, 70, 256), (520, 256, 1000, 64)]
+
+
+@pytest.fixture(scope="module")
+def q():
+    torch_cuda()
+    import quantized_weight_decode_amd as q
+    return q
+
+
+def _run(q, fmt, S, I, O, gs, dtype, seed=0, **k):
+    if fmt == "i4g":
+        w, s = L.int4((O,), I, gs, seed)
+        W = L.decode_int4(w, s, I, gs)
+    else:
+        w, s = L.fp8(O, I, seed)
+        W = L.decode_fp8(w, s)
+    x = L.acts(S, I, dtype, seed + 1)
+    gated = k.get("gated", False)
+    oc = O // 2 if gated else O
+    bias = L.acts(1, O, dtype, seed + 2)[0] if k.get("bias") else None
+    res = L.acts(S, oc, dtype, seed + 3) if k.get("residual") else None
+    kw = {"act": k.get("act"), "gated": gated}
+    dv = {"bias": bias.cuda() if bias is not None else None,
+          "residual": res.cuda() if res is not None else None}
+    if fmt == "i4g":
+        y = q.i4g_linear(dev(w), dev(s), x.cuda(), gs, **kw, **dv)
+    else:
+        y = q.fp8b128_linear(dev(w), dev(s), x.cuda(), **kw, **dv)
+    ref, bound = L.reference(W, x, dtype, bias=bias, residual=res, **kw)
+    return y, ref, bound
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("S,I,O,gs", SHAPES)
+def test_i4g_product(q, S, I, O, gs, dtype):
+    y, ref, bound = _run(q, "i4g", S, I, O, gs, dtype, seed=S + I)
+    L.assert_within(y, ref, bound)
+    if dtype == torch.float32:
+        assert L.rel_l2(y, ref) <= 1e-5
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("S,I,O", [(s, i, o) for s, i, o, _ in SHAPES])
+def test_fp8_product(q, S, I, O, dtype):
+    y, ref, bound = _run(q, "fp8", S, I, O, 128, dtype, seed=S + I)
+    L.assert_within(y, ref, bound)
+    if dtype == torch.float32:
+        assert L.rel_l2(y, ref) <= 1e-5
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("fmt", ["i4g", "fp8"])
+@pytest.mark.parametrize("S,I,O,gs", [(1, 512, 250, 64), (7, 129, 34, 2), (40, 768, 132, 32),
+                                      (140, 512, 516, 64)])
+@pytest.mark.parametrize("act,gated,bias,residual",
+                         [("relu", False, True, False), ("silu", False, False, True),
+                          ("gelu", False, True, True), ("gelu_tanh", False, False, False),
+                          (None, False, True, True), ("silu", True, False, False),
+                          ("gelu", True, True, True), (None, True, False, True),
+                          ("gelu_tanh", True, True, False), ("relu", True, False, False)])
+def test_epilogue(q, fmt, S, I, O, gs, act, gated, bias, residual, dtype):
+    y, ref, bound = _run(q, fmt, S, I, O, gs, dtype, act=act, gated=gated, bias=bias,
+                         residual=residual)
+    L.assert_within(y, ref, bound)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("S", [1, 6, 50, 200])
+def test_strided_rows_and_untouched_gaps(q, S, dtype):
+    """x, residual and out as column slices of wider tensors; the columns
+    beside out and the rows behind it keep their values; odd offsets leave the
+    rows on element alignment only."""
+    I, O, gs = 320, 90, 64
+    w, s = L.int4((O,), I, gs, 3)
+    xb = L.acts(S + 2, I + 37, dtype, 4).cuda()
+    rb = L.acts(S + 2, O + 11, dtype, 5).cuda()
+    ob = torch.full((S + 2, O + 23), 7.5, dtype=dtype, device="cuda")
+    x, r, out = xb[1:S + 1, 5:5 + I], rb[1:S + 1, 3:3 + O], ob[1:S + 1, 7:7 + O]
+    y = q.i4g_linear(dev(w), dev(s), x, gs, residual=r, out=out)
+    assert y.data_ptr() == out.data_ptr()
+    ref, bound = L.reference(L.decode_int4(w, s, I, gs), x, dtype, residual=r)
+    L.assert_within(out, ref, bound)
+    keep = ob.clone()
+    keep[1:S + 1, 7:7 + O] = 7.5
+    assert bool((keep == 7.5).all())
+
+
+@pytest.mark.parametrize("S", [1, 20, 150])
+def test_residual_in_place_and_vector_form(q, S):
+    I, O, gs = 256, 192, 64
+    w, s = L.int4((O,), I, gs, 6)
+    x = L.acts(S, I, torch.bfloat16, 7)
+    h = L.acts(S, O, torch.bfloat16, 8)
+    y = h.cuda()
+    q.i4g_linear(dev(w), dev(s), x.cuda(), gs, residual=y, out=y)
+    ref, bound = L.reference(L.decode_int4(w, s, I, gs), x, torch.bfloat16, residual=h)
+    L.assert_within(y, ref, bound)
+    v = q.i4g_linear(dev(w), dev(s), x[0].cuda(), gs, residual=h[0].cuda())
+    assert v.shape == (O,)
+    L.assert_within(v[None], ref[:1], bound[:1])
+
+
+@pytest.mark.parametrize("fmt", ["i4g", "fp8"])
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("S", [4, 40, 140])
+def test_wide_range_and_non_finite_rows(q, fmt, S, dtype):
+    """Rows of very different scale, an outlier on one column, a row of zeros;
+    a row with an infinity or NaN comes out without finite sums and leaves the
+    others alone."""
+    I, O, gs = 512, 130, 64
+    w, s = L.int4((O,), I, gs, 9) if fmt == "i4g" else L.fp8(O, I, 9)
+    W = L.decode_int4(w, s, I, gs) if fmt == "i4g" else L.decode_fp8(w, s)
+    x = L.acts(S, I, dtype, 10)
+    x[0] *= 1e-30
+    x[1] *= 1e25
+    x[2, 77] = 3e4
+    x[3] = 0.0
+    call = (lambda v: q.i4g_linear(dev(w), dev(s), v.cuda(), gs)) if fmt == "i4g" else \
+        (lambda v: q.fp8b128_linear(dev(w), dev(s), v.cuda()))
+    ref, bound = L.reference(W, x, dtype)
+    L.assert_within(call(x), ref, bound)
+    bad = x.clone()
+    bad[1, 5], bad[2, 500] = float("nan"), float("inf")
+    y = call(bad)
+    assert not bool(torch.isfinite(y[1]).any()) and not bool(torch.isfinite(y[2]).any())
+    rest = [i for i in range(S) if i not in (1, 2)]
+    L.assert_within(y[rest], ref[rest], bound[rest])
+
+
+@pytest.mark.parametrize("S", [2, 100])
+def test_nan_weight_code_poisons_its_column_only(q, S):
+    I, O = 256, 140
+    w, s = L.fp8(O, I, 11)
+    w[77, 33] = 0x7F
+    x = L.acts(S, I, torch.bfloat16, 12)
+    y = q.fp8b128_linear(dev(w), dev(s), x.cuda())
+    assert bool(torch.isnan(y[:, 77]).all())
+    assert bool(torch.isfinite(y[:, [c for c in range(O) if c != 77]]).all())
+
+
+def test_single_and_many_rows_agree_with_the_gemv(q):
+    """The plain f32 product next to the library's GEMV of the same weights."""
+    I, O, gs = 2048, 512, 64
+    w, s = L.int4((O,), I, gs, 13)
+    x = L.acts(4, I, torch.float32, 14).cuda()
+    a = q.i4g_linear(dev(w), dev(s), x, gs)
+    b = q.i4g(dev(w), dev(s), x, gs)
+    assert L.rel_l2(a, b.cpu().double()) <= 1e-5
+
+
+@pytest.mark.parametrize("S", [0, 1, 3, 70, 300])
+def test_results_do_not_change_between_calls(q, S):
+    I, O, gs = 1024, 400, 64
+    w, s = (dev(t) for t in L.int4((O,), I, gs, 15))
+    x = L.acts(S, I, torch.bfloat16, 16).cuda()
+    y = [q.i4g_linear(w, s, x, gs, act="silu", gated=True) for _ in range(3)]
+    assert y[0].shape == (S, O // 2)
+    assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
+
+
+@pytest.mark.parametrize("S", [1, 40, 200])
+def test_side_stream_and_replayed_graphs(q, S):
+    """Work goes to the current stream; two captured calls with a workspace
+    each replay several times, with eager calls and new inputs between."""
+    I, O, gs = 768, 300, 64
+    w, s = (dev(t) for t in L.int4((O,), I, gs, 17))
+    x = L.acts(S, I, torch.bfloat16, 18).cuda()
+    want = q.i4g_linear(w, s, x, gs, act="silu")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = q.i4g_linear(w, s, x, gs, act="silu")
+    side.synchronize()
+    assert torch.equal(got, want)
+    graphs = []
+    for _ in range(2):
+        xin, out = x.clone(), torch.zeros_like(want)
+        ws = q.linear_workspace(S, I, O, x.dtype, "cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            q.i4g_linear(w, s, xin, gs, act="silu", workspace=ws, out=out)
+        graphs.append((g, xin, out))
+    for i in range(4):
+        for j, (g, xin, out) in enumerate(graphs):
+            xin.copy_(x * (1 + i + 2 * j))
+            out.zero_()
+            g.replay()
+        want = [q.i4g_linear(w, s, xin, gs, act="silu") for _, xin, _ in graphs]
+        torch.cuda.synchronize()
+        for (_, _, out), v in zip(graphs, want):
+            assert torch.equal(out, v)
+
+
+@pytest.mark.parametrize("S", [3, 140])
+def test_rows_beyond_32_bit_offsets(q, S):
+    """y rows 2^30 bytes apart or so: the last row starts past 4 GiB."""
+    I, O, gs = 64, 40, 32
+    w, s = L.int4((O,), I, gs, 19)
+    x = L.acts(S, I, torch.bfloat16, 20)
+    ld = (5 << 30) // 2 // (S - 1)
+    buf = torch.empty((S - 1) * ld + I, dtype=torch.bfloat16, device="cuda")
+    out = buf.as_strided((S, O), (ld, 1))
+    q.i4g_linear(dev(w), dev(s), x.cuda(), gs, out=out)
+    ref, bound = L.reference(L.decode_int4(w, s, I, gs), x, torch.bfloat16)
+    L.assert_within(out, ref, bound)
+    xs = buf.as_strided((S, I), (ld, 1))
+    xs.copy_(x)
+    y = q.i4g_linear(dev(w), dev(s), xs, gs)
+    L.assert_within(y, ref, bound)
+
+
+def test_misaligned_weights(q):
+    """w one byte off any alignment: the general kernel's result."""
+    I, O, gs = 256, 60, 64
+    w, s = L.int4((O,), I, gs, 21)
+    buf = torch.zeros(w.size + 64, dtype=torch.uint8, device="cuda")
+    for off in (1, 4, 8):
+        v = buf[off:off + w.size].view(O, I // 2)
+        v.copy_(dev(w))
+        for S in (2, 90):
+            x = L.acts(S, I, torch.bfloat16, 22)
+            ref, bound = L.reference(L.decode_int4(w, s, I, gs), x, torch.bfloat16)
+            L.assert_within(q.i4g_linear(v, dev(s), x.cuda(), gs), ref, bound)
