@@ -191,8 +191,6 @@ __global__ __launch_bounds__(1024) void plan_tiles(const int32_t *__restrict__ o
     }
 }
 
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-
 // tiles that R rows of E experts can need
 long long max_tiles(int R, int E, int bm)
 {
@@ -213,23 +211,32 @@ void run_general(const LinearArgs &a, const RowTile *tiles, unsigned grid, hipSt
 
 size_t linear_workspace(int T, int R, int E, int I, int O, int dtype)
 {
-    (void)T; (void)I; (void)O; (void)dtype;
-    return E > 0 ? align256((size_t)max_tiles(R, E, 16) * sizeof(RowTile)) : 256;
+    (void)O;
+    return (E > 0 ? align256((size_t)max_tiles(R, E, 16) * sizeof(RowTile)) : 0) +
+           tile_workspace(T, I, dtype);
 }
 
 hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStream_t st)
 {
     const int oc = a.gated ? a.O / 2 : a.O;
+    const bool fits = tile_fits(fmt, a);
+    int bm = GM;
+    if (fits) {
+        const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
+        bm = rows > 64 && a.dtype == QGEMV_BF16 ? 128 : rows > 32 ? 64 : 32;
+    }
     RowTile *tiles = nullptr;
-    long long mt = (a.R + GM - 1) / GM;
+    long long mt = (a.R + bm - 1) / bm;
     if (a.offsets) {
         tiles = static_cast<RowTile *>(ws);
-        mt = max_tiles(a.R, a.E, GM);
-        hipLaunchKernelGGL(plan_tiles, dim3(1), dim3(1024), 0, st, a.offsets, a.E, a.R, GM, tiles,
+        mt = max_tiles(a.R, a.E, bm);
+        hipLaunchKernelGGL(plan_tiles, dim3(1), dim3(1024), 0, st, a.offsets, a.E, a.R, bm, tiles,
                            (int)mt);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
+        ws = static_cast<char *>(ws) + align256((size_t)max_tiles(a.R, a.E, 16) * sizeof(RowTile));
     }
+    if (fits) return launch_tile(fmt, a, bm, tiles, (int)mt, ws, st);
     const long long grid = mt * ((oc + GN - 1) / GN);
     if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     if (fmt == FMT_I4G) {

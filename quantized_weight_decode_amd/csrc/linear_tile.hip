@@ -1,0 +1,452 @@
+// linear_tile.hip -- many rows of x times packed weights on the f16 matrix
+// cores, dense or grouped by expert, with the epilogue.
+#include "qg_device.h"
+#include "qg_linear.h"
+
+namespace qg {
+
+namespace {
+
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// ---------------------------------------------------------------------------
+// Packed activations.
+//
+// Each row of x is scaled by a power of two, x' = x 2^(15 - E) with max|x| in
+// [2^(E-1), 2^E) over its finite values, so that 2^14 <= max|x'| < 2^15, and
+// stored as f16: bf16 values exactly down to 2^-28 of the maximum (below it
+// to 2^-39 of the maximum); f32 values as two planes, hi = f16(x') and lo =
+// f16(x' - hi), together within 2^-22 of themselves (2^-40 of the maximum
+// where lo is subnormal), the size of f32's own rounding of a product.
+// The exponent E - 15 is undone on the f32 sum.  int4 weights unpack in the
+// column order 0 4 1 5 2 6 3 7 of each eight; x is stored in that order.
+// Rows are padded with zeros to whole K steps.  Bound by HBM: x read once, 2
+// or 4 bytes per element written.
+// ---------------------------------------------------------------------------
+template <typename XT, int FMT>
+__global__ __launch_bounds__(256) void pack_rows(const typename XT::raw *__restrict__ x,
+                                                 long long ldx, int I, int Ip,
+                                                 _Float16 *__restrict__ hi,
+                                                 _Float16 *__restrict__ lo,
+                                                 int *__restrict__ rexp)
+{
+    __shared__ uint32_t wmax[4];
+    const int tid = threadIdx.x;
+    const long long t = blockIdx.x;
+    const typename XT::raw *src = x + (size_t)t * ldx;
+    // largest finite |x| by its bits
+    uint32_t m = 0;
+    for (int c = tid; c < I; c += 256) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, XT::get(src[c])) & 0x7FFFFFFFu;
+        m = b < 0x7F800000u && b > m ? b : m;
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)m, d);
+        m = o > m ? o : m;
+    }
+    if ((tid & 63) == 0) wmax[tid >> 6] = m;
+    __syncthreads();
+    m = 0;
+    for (int i = 0; i < 4; i++) m = wmax[i] > m ? wmax[i] : m;
+    int E = 0;
+    if (m) frexpf(__builtin_bit_cast(float, m), &E);
+    if (tid == 0) rexp[t] = E - 15;
+    for (int c = tid * 8; c < Ip; c += 256 * 8) {
+        f16x8 h, l;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int from = FMT == FMT_I4G ? (j >> 1) + 4 * (j & 1) : j;
+            const float v = c + from < I ? ldexpf(XT::get(src[c + from]), 15 - E) : 0.0f;
+            h[j] = (_Float16)v;
+            if (lo) l[j] = (_Float16)(v - (float)h[j]);
+        }
+        *reinterpret_cast<f16x8 *>(hi + (size_t)t * Ip + c) = h;
+        if (lo) *reinterpret_cast<f16x8 *>(lo + (size_t)t * Ip + c) = l;
+    }
+}
+
+// Eight nibbles of a dword as q - 8 in f16, exactly, in the column order 0 4
+// 1 5 2 6 3 7: 0x6400 | q is 1024 + q, and 0x6400 | 16 q is 1024 + 16 q =
+// 16 (q - 8) + 1152.
+__device__ __forceinline__ f16x8 nib8_f16(uint32_t w)
+{
+    const f16x2 one = {(_Float16)1.0f, (_Float16)1.0f};
+    const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const f16x2 c0 = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+    const f16x2 c1 = {(_Float16)-72.0f, (_Float16)-72.0f};
+    const uint32_t w8 = w >> 8;
+    const f16x2 a = __builtin_bit_cast(f16x2, (w & 0x000F000Fu) | 0x64006400u);
+    const f16x2 b = __builtin_bit_cast(f16x2, (w & 0x00F000F0u) | 0x64006400u);
+    const f16x2 c = __builtin_bit_cast(f16x2, (w8 & 0x000F000Fu) | 0x64006400u);
+    const f16x2 d = __builtin_bit_cast(f16x2, (w8 & 0x00F000F0u) | 0x64006400u);
+    const f16x2 r0 = a * one + c0, r1 = b * sixteenth + c1;
+    const f16x2 r2 = c * one + c0, r3 = d * sixteenth + c1;
+    return f16x8{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
+}
+
+// Eight E4M3 codes (two dwords, byte order = column order) in f16, exactly.
+__device__ __forceinline__ f16x8 fp8x8_f16(uint32_t a, uint32_t b)
+{
+    const f16x2 r0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)a, 1.0f, false);
+    const f16x2 r1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)a, 1.0f, true);
+    const f16x2 r2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)b, 1.0f, false);
+    const f16x2 r3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)b, 1.0f, true);
+    return f16x8{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
+}
+
+constexpr int TK = 64;          // columns per K step
+constexpr int TN = 256;         // rows of W per workgroup tile
+
+struct TileArgs {
+    LinearArgs a;
+    const _Float16 *hi, *lo;
+    const int *rexp;
+    const RowTile *tiles;
+    int Ip, ntm, ntn;
+};
+
+// Tile kernel.  A workgroup of 4 waves makes 16 MF rows of y x 256 rows of W;
+// each wave all 16 MF rows x 64 rows of W, so a weight is unpacked once per
+// workgroup, from registers, and never passes LDS, while the waves share the
+// packed activations through LDS (two buffers, 16-byte chunks XOR-swizzled by
+// row).  v_mfma_f32_16x16x32_f16, lane l: A row l % 16, B column l % 16, eight
+// k from the lane group l / 16; D rows 4 (l / 16) + i, column l % 16.  The k
+// order inside a K step is free as long as A and B agree: with one scale per
+// 64 columns a lane group owns 16 consecutive columns (one 8-byte load of
+// int4), with one per 32 it owns eight of each 32.
+// Integer (or fp8) products are summed exactly-scaled per scale group: the
+// group's sum starts at zero and is added to the total as acc += s * sum, one
+// FMA per output and group, beside two matrix instructions.
+template <int FMT, typename XT, int NP, int MF, bool GATED, int FG>
+__global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
+{
+    constexpr int BM = 16 * MF;
+    constexpr int CH = BM * 8;                           // 16-byte chunks of a plane
+    constexpr int PT = CH / 256;                         // per thread
+    static_assert(CH % 256 == 0, "whole chunks per thread");
+    constexpr int LDO = TN + 4;                          // epilogue row stride, floats
+    constexpr size_t XS = 2 * NP * CH * sizeof(f16x8), OS = 16 * LDO * sizeof(float);
+    __shared__ __align__(16) char smem[XS > OS ? XS : OS];
+    __shared__ int rx[BM];
+    f16x8 (*const xs)[NP][CH] = reinterpret_cast<f16x8 (*)[NP][CH]>(smem);
+    const LinearArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int li = lane & 15, lg = lane >> 4;
+    const int oc = GATED ? a.O / 2 : a.O;
+
+    // consecutive tiles go to one XCD (workgroups are dealt to the 8 in turn)
+    const int nb = gridDim.x, q8 = nb / 8, r8 = nb % 8;
+    const int xcd = blockIdx.x % 8, in = blockIdx.x / 8;
+    const int b = xcd * q8 + min(xcd, r8) + in;
+    int mt, nt;
+    RowTile t;
+    if (p.tiles) {                                       // an expert's columns together
+        mt = b / p.ntn;
+        nt = b % p.ntn;
+        t = p.tiles[mt];
+        if (t.n <= 0) return;
+    } else {                                             // a column block's rows together
+        nt = b / p.ntm;
+        mt = b % p.ntm;
+        t = RowTile{0, mt * BM, min(BM, a.R - mt * BM), 0};
+    }
+
+    // row exponents; a bad row index is marked and reads row 0
+    constexpr int BAD_ROW = -0x7FFFFFFF;
+    if (tid < BM) {
+        int e = 0;
+        if (tid < t.n) {
+            int r = t.row0 + tid;
+            if (a.rows) r = a.rows[r];
+            e = r < 0 || r >= a.T ? BAD_ROW : p.rexp[r];
+        }
+        rx[tid] = e;
+    }
+
+    // activation chunks of this thread: row c / 8, swizzled chunk c % 8
+    const _Float16 *asrc[PT];
+#pragma unroll
+    for (int i = 0; i < PT; i++) {
+        const int c = tid + 256 * i;
+        const int row = c >> 3;
+        int r = t.row0 + (row < t.n ? row : 0);
+        if (a.rows) {
+            r = a.rows[r];
+            r = r < 0 || r >= a.T ? 0 : r;
+        }
+        asrc[i] = p.hi + (size_t)r * p.Ip + ((c & 7) ^ (row & 7)) * 8;
+    }
+    const long long lo_off = NP == 2 ? p.lo - p.hi : 0;
+
+    // weight rows of this lane
+    const size_t rb = FMT == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
+    const uint8_t *wbase = a.w + (size_t)t.expert * a.w_stride;
+    const float *sbase = a.scales + (size_t)t.expert * a.s_stride;
+    constexpr int CW = GATED ? 32 : 64;                  // columns of y per wave
+    const int c0 = nt * (4 * CW) + wave * CW + li;
+    uint32_t woff[4];
+    uint32_t soff[4];
+#pragma unroll
+    for (int n = 0; n < 4; n++) {
+        const int c = c0 + (GATED ? n & 1 : n) * 16;
+        const int row = (c < oc ? c : oc - 1) + (GATED && n >= 2 ? oc : 0);
+        woff[n] = (uint32_t)(row * rb);
+        soff[n] = (uint32_t)(FMT == FMT_I4G ? row : row >> 7) * (uint32_t)a.ng;
+    }
+
+    f32x4v acc[MF][4];
+#pragma unroll
+    for (int m = 0; m < MF; m++)
+#pragma unroll
+        for (int n = 0; n < 4; n++) acc[m][n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+
+    constexpr int WD = FMT == FMT_FP8 ? 4 : 2;           // raw dwords per lane, row and step
+    constexpr int NS = TK / FG;                          // scales per row and step
+    f16x8 av[NP][PT];
+    uint32_t wv[4][WD];
+    float sv[4][NS];
+    const int gs = FMT == FMT_FP8 ? 128 : a.gs;
+    const uint32_t lane_b = FMT == FMT_FP8 ? lg * 16 : FG == 64 ? lg * 8 : lg * 4;
+    uint32_t group = 0;                                  // scale group of the next load
+    int done = 0;                                        // its columns already loaded
+
+    // The loop's body has no branches: loads past the last step repeat it, and
+    // in a last half step (I % 64 == 32) the lanes behind the row's end read
+    // its last bytes again, which meet zeros of x.
+    auto load_a = [&](int k0) {
+#pragma unroll
+        for (int q = 0; q < NP; q++)
+#pragma unroll
+            for (int i = 0; i < PT; i++)
+                av[q][i] = *reinterpret_cast<const f16x8 *>(asrc[i] + q * lo_off + k0);
+    };
+    auto store_a = [&](int buf) {
+#pragma unroll
+        for (int q = 0; q < NP; q++)
+#pragma unroll
+            for (int i = 0; i < PT; i++) xs[buf][q][tid + 256 * i] = av[q][i];
+    };
+    auto load_w = [&](int k0) {
+        const uint32_t kb = (FMT == FMT_I4G ? k0 / 2 : k0) + lane_b;
+        const uint32_t end = (uint32_t)rb - WD * 4;
+#pragma unroll
+        for (int n = 0; n < 4; n++) {
+            const uint8_t *src = wbase + woff[n];
+            if (FMT == FMT_FP8) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(src + min(kb, end));
+                wv[n][0] = v.x; wv[n][1] = v.y; wv[n][WD - 2] = v.z; wv[n][WD - 1] = v.w;
+            } else if (FG == 64) {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(src + min(kb, end));
+                wv[n][0] = v.x; wv[n][1] = v.y;
+            } else {
+                wv[n][0] = *reinterpret_cast<const uint32_t *>(src + kb);
+                wv[n][1] = *reinterpret_cast<const uint32_t *>(src + min(kb + 16, end + 4));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NS; j++) {
+            const uint32_t gj = min(group, (uint32_t)a.ng - 1);
+#pragma unroll
+            for (int n = 0; n < 4; n++) sv[n][j] = sbase[soff[n] + gj];
+            done += FG;
+            group += done == gs;
+            done = done == gs ? 0 : done;
+        }
+    };
+
+    load_a(0);
+    load_w(0);
+    store_a(0);
+    __syncthreads();
+    int buf = 0;
+    for (int k0 = 0; k0 < p.Ip; k0 += TK) {
+        // unpack this step's weights, then ask for the next step's data
+        f16x8 bv[4][2];
+        float sc[4][NS];
+#pragma unroll
+        for (int n = 0; n < 4; n++) {
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                bv[n][h] = FMT == FMT_FP8 ? fp8x8_f16(wv[n][(2 * h) % WD], wv[n][(2 * h + 1) % WD])
+                                          : nib8_f16(wv[n][h]);
+#pragma unroll
+            for (int j = 0; j < NS; j++) sc[n][j] = sv[n][j];
+        }
+        const int next = min(k0 + TK, p.Ip - TK);
+        load_a(next);
+        load_w(next);
+        // Steps of two 16 x 16 blocks (n, n + 1) of one row block m and scale
+        // group j: a step's sums are added to the totals while the next
+        // step's matrix instructions run.  The scheduling barrier keeps the
+        // compiler from running ahead and holding many steps' values.
+        f16x8 am[2][NP][2];
+        f32x4v g[2][2];
+        auto read_a = [&](int m) {
+#pragma unroll
+            for (int q = 0; q < NP; q++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int ch = FG == 64 ? 2 * lg + h : 4 * h + lg;
+                    am[m & 1][q][h] = xs[buf][q][(m * 16 + li) * 8 + (ch ^ (li & 7))];
+                }
+        };
+        auto flush = [&](int s) {
+            const int m = s / (2 * NS), j = (s / 2) % NS, n = (s & 1) * 2;
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+                    acc[m][n + i][r] = fmaf(sc[n + i][j], g[s & 1][i][r], acc[m][n + i][r]);
+        };
+        read_a(0);
+#pragma unroll
+        for (int s = 0; s < 2 * NS * MF; s++) {
+            const int m = s / (2 * NS), j = (s / 2) % NS, n = (s & 1) * 2;
+            if (s % (2 * NS) == 0 && m + 1 < MF) read_a(m + 1);
+            f32x4v t0 = {0.0f, 0.0f, 0.0f, 0.0f}, t1 = t0;
+#pragma unroll
+            for (int h = j * (2 / NS); h < (j + 1) * (2 / NS); h++)
+#pragma unroll
+                for (int q = NP - 1; q >= 0; q--) {      // small parts first
+                    t0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(am[m & 1][q][h], bv[n][h], t0, 0,
+                                                                0, 0);
+                    t1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(am[m & 1][q][h], bv[n + 1][h], t1,
+                                                                0, 0, 0);
+                }
+            g[s & 1][0] = t0;
+            g[s & 1][1] = t1;
+            if (s > 0) flush(s - 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        flush(2 * NS * MF - 1);
+        store_a(buf ^ 1);
+        __syncthreads();
+        buf ^= 1;
+    }
+
+    // Epilogue, 16 rows at a time through LDS: whole rows are stored, and the
+    // end of an output is one piece of code.  (The last K step ended with a
+    // barrier, so the activations' LDS is free.)
+    float *os = reinterpret_cast<float *>(smem);
+    constexpr int YC = 4 * CW;                           // columns of y
+    const int ec = tid % YC, er = tid / YC;
+    const int yc = nt * YC + ec;
+    const int oi = GATED ? (ec / 32) * 64 + ec % 32 : ec;
+#pragma unroll
+    for (int m = 0; m < MF; m++) {
+        if (m * 16 >= t.n) break;                        // uniform over the workgroup
+        if (m > 0) __syncthreads();
+#pragma unroll
+        for (int n = 0; n < 4; n++)
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                os[(4 * lg + r) * LDO + wave * 64 + n * 16 + li] = acc[m][n][r];
+        __syncthreads();
+        if (yc < oc)
+#pragma unroll 1
+            for (int r = er; r < 16; r += 256 / YC) {
+                const int row = m * 16 + r;
+                if (row >= t.n) break;
+                const int e = rx[row];
+                float v = ldexpf(os[r * LDO + oi], e);
+                float up = GATED ? ldexpf(os[r * LDO + oi + 32], e) : 0.0f;
+                if (e == BAD_ROW) v = up = __builtin_nanf("");
+                finish<XT>(a, t.expert, t.row0 + row, yc, v, up);
+            }
+    }
+}
+
+#define QG_RUN(FG)                                                                          \
+    do {                                                                                    \
+        if (p.a.gated)                                                                      \
+            hipLaunchKernelGGL((linear_tile<FMT, XT, NP, MF, true, FG>), dim3(grid), dim3(256), 0, \
+                               st, p);                                                      \
+        else                                                                                \
+            hipLaunchKernelGGL((linear_tile<FMT, XT, NP, MF, false, FG>), dim3(grid), dim3(256), 0, \
+                               st, p);                                                      \
+    } while (0)
+
+template <int FMT, typename XT, int MF>
+hipError_t run_tile(const TileArgs &p, unsigned grid, hipStream_t st)
+{
+    constexpr int NP = sizeof(typename XT::raw) == 4 ? 2 : 1;
+    if constexpr (FMT == FMT_FP8) {
+        QG_RUN(64);
+    } else {
+        if (p.a.gs % 64 == 0) QG_RUN(64);
+        else QG_RUN(32);
+    }
+    return hipGetLastError();
+}
+int padded(int I) { return (I + TK - 1) / TK * TK; }
+
+}  // namespace
+
+size_t tile_workspace(int T, int I, int dtype)
+{
+    return align256((size_t)T * sizeof(int)) +
+           align256((size_t)T * padded(I) * 2) * (dtype == QGEMV_BF16 ? 1 : 2);
+}
+
+bool tile_fits(WeightFormat fmt, const LinearArgs &a)
+{
+    const size_t rb = fmt == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
+    return a.I % 32 == 0 && (fmt == FMT_FP8 || a.gs % 32 == 0) && ((uintptr_t)a.w & 15) == 0 &&
+           (!a.offsets || a.w_stride % 16 == 0) && rb * a.O < (1ull << 32) &&
+           (size_t)a.ng * a.O < (1ull << 32);
+}
+
+hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, int bm, const RowTile *tiles,
+                       int ntm, void *ws, hipStream_t st)
+{
+    TileArgs p{};
+    p.a = a;
+    p.Ip = padded(a.I);
+    char *at = static_cast<char *>(ws);
+    int *rexp = reinterpret_cast<int *>(at);
+    at += align256((size_t)a.T * sizeof(int));
+    _Float16 *hi = reinterpret_cast<_Float16 *>(at);
+    at += align256((size_t)a.T * p.Ip * 2);
+    _Float16 *lo = a.dtype == QGEMV_BF16 ? nullptr : reinterpret_cast<_Float16 *>(at);
+    p.hi = hi;
+    p.lo = lo;
+    p.rexp = rexp;
+    p.tiles = tiles;
+    p.ntm = ntm;
+    const int cols = a.gated ? TN / 2 : TN, oc = a.gated ? a.O / 2 : a.O;
+    p.ntn = (oc + cols - 1) / cols;
+    const long long grid = (long long)ntm * p.ntn;
+    if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+#define QG_PACK(XT, F)                                                                      \
+    hipLaunchKernelGGL((pack_rows<XT, F>), dim3(a.T), dim3(256), 0, st,                     \
+                       static_cast<const XT::raw *>(a.x), a.ldx, a.I, p.Ip, hi, lo, rexp)
+    if (fmt == FMT_I4G) {
+        if (a.dtype == QGEMV_BF16) QG_PACK(BF16, FMT_I4G);
+        else QG_PACK(F32, FMT_I4G);
+    } else {
+        if (a.dtype == QGEMV_BF16) QG_PACK(BF16, FMT_FP8);
+        else QG_PACK(F32, FMT_FP8);
+    }
+#undef QG_PACK
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+#define QG_TILE(MF)                                                                         \
+    (fmt == FMT_I4G                                                                         \
+         ? (a.dtype == QGEMV_BF16 ? run_tile<FMT_I4G, BF16, MF>(p, (unsigned)grid, st)      \
+                                  : run_tile<FMT_I4G, F32, MF>(p, (unsigned)grid, st))      \
+         : (a.dtype == QGEMV_BF16 ? run_tile<FMT_FP8, BF16, MF>(p, (unsigned)grid, st)      \
+                                  : run_tile<FMT_FP8, F32, MF>(p, (unsigned)grid, st)))
+    switch (bm) {
+    case 128:                                            // bf16 only
+        return fmt == FMT_I4G ? run_tile<FMT_I4G, BF16, 8>(p, (unsigned)grid, st)
+                              : run_tile<FMT_FP8, BF16, 8>(p, (unsigned)grid, st);
+    case 64: return QG_TILE(4);
+    default: return QG_TILE(2);
+    }
+#undef QG_TILE
+}
+
+}  // namespace qg

@@ -34,6 +34,16 @@ struct LinearArgs {
 size_t linear_workspace(int T, int R, int E, int I, int O, int dtype);
 hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStream_t st);
 
+// The f16 tile kernels (linear_tile.hip): shapes they take, workspace, launch
+// with row tiles of bm in {32, 64, 128}; tiles == nullptr: dense.
+struct RowTile;
+bool tile_fits(WeightFormat fmt, const LinearArgs &a);
+size_t tile_workspace(int T, int I, int dtype);
+hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, int bm, const RowTile *tiles,
+                       int ntm, void *ws, hipStream_t st);
+
+inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
 // routed slots: sort by expert, and the gate-weighted return
 size_t moe_group_workspace(int T, int K, int E);
 hipError_t launch_moe_group(const int32_t *ids, int T, int K, int E, int32_t *offsets,
