@@ -220,9 +220,12 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStr
 {
     const int oc = a.gated ? a.O / 2 : a.O;
     const bool fits = tile_fits(fmt, a);
+    const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
+    const bool stream = rows <= 16 && stream_fits(fmt, a);
     int bm = GM;
-    if (fits) {
-        const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
+    if (stream) {
+        bm = 16;
+    } else if (fits) {
         bm = rows > 64 && a.dtype == QGEMV_BF16 ? 128 : rows > 32 ? 64 : 32;
     }
     RowTile *tiles = nullptr;
@@ -236,6 +239,7 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStr
         if (e != hipSuccess) return e;
         ws = static_cast<char *>(ws) + align256((size_t)max_tiles(a.R, a.E, 16) * sizeof(RowTile));
     }
+    if (stream) return launch_stream(fmt, a, tiles, (int)mt, st);
     if (fits) return launch_tile(fmt, a, bm, tiles, (int)mt, ws, st);
     const long long grid = mt * ((oc + GN - 1) / GN);
     if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;

@@ -42,6 +42,11 @@ size_t tile_workspace(int T, int I, int dtype);
 hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, int bm, const RowTile *tiles,
                        int ntm, void *ws, hipStream_t st);
 
+// The stream kernels (linear_stream.hip): row tiles of 16.
+bool stream_fits(WeightFormat fmt, const LinearArgs &a);
+hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, const RowTile *tiles, int ntm,
+                         hipStream_t st);
+
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // routed slots: sort by expert, and the gate-weighted return
