@@ -128,8 +128,11 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     constexpr int PT = CH / 256;                         // per thread
     static_assert(CH % 256 == 0, "whole chunks per thread");
     constexpr int LDO = TN + 4;                          // epilogue row stride, floats
-    constexpr size_t XS = 2 * NP * CH * sizeof(f16x8), OS = 16 * LDO * sizeof(float);
-    __shared__ __align__(16) char smem[XS > OS ? XS : OS];
+    constexpr int WB = FMT == FMT_FP8 ? 64 : 32;         // bytes of a row and step
+    constexpr int WD = WB / 16;                          // 16-byte pieces per lane and step
+    constexpr size_t XS = 2 * NP * CH * sizeof(f16x8), WS = (size_t)TN * WB;
+    constexpr size_t OS = 16 * LDO * sizeof(float);
+    __shared__ __align__(16) char smem[XS + WS > OS ? XS + WS : OS];
     __shared__ int rx[BM];
     f16x8 (*const xs)[NP][CH] = reinterpret_cast<f16x8 (*)[NP][CH]>(smem);
     const LinearArgs &a = p.a;
@@ -177,7 +180,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
             r = a.rows[r];
             r = r < 0 || r >= a.T ? 0 : r;
         }
-        asrc[i] = p.hi + (size_t)r * p.Ip + ((c & 7) ^ (row & 7)) * 8;
+        asrc[i] = p.hi + (size_t)r * p.Ip + ((c & 7) ^ ((row >> 1) & 7)) * 8;
     }
     const long long lo_off = NP == 2 ? p.lo - p.hi : 0;
 
@@ -186,16 +189,25 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     const uint8_t *wbase = a.w + (size_t)t.expert * a.w_stride;
     const float *sbase = a.scales + (size_t)t.expert * a.s_stride;
     constexpr int CW = GATED ? 32 : 64;                  // columns of y per wave
-    const int c0 = nt * (4 * CW) + wave * CW + li;
-    uint32_t woff[4];
-    uint32_t soff[4];
+    constexpr int NS = TK / FG;                          // scales per row and step
+    // row i of the wave's 64 (block i / 16 of n)
+    auto weight_row = [&](int i) {
+        const int n = i >> 4;
+        const int c = nt * (4 * CW) + wave * CW + (GATED ? n & 1 : n) * 16 + (i & 15);
+        return (c < oc ? c : oc - 1) + (GATED && n >= 2 ? oc : 0);
+    };
+    uint32_t woff[WD];                                   // lanes of a row next to each other
 #pragma unroll
-    for (int n = 0; n < 4; n++) {
-        const int c = c0 + (GATED ? n & 1 : n) * 16;
-        const int row = (c < oc ? c : oc - 1) + (GATED && n >= 2 ? oc : 0);
-        woff[n] = (uint32_t)(row * rb);
-        soff[n] = (uint32_t)(FMT == FMT_I4G ? row : row >> 7) * (uint32_t)a.ng;
+    for (int i = 0; i < WD; i++)
+        woff[i] = (uint32_t)(weight_row((lane + 64 * i) / WD) * rb);
+    const uint32_t lane_b = (lane % WD) * 16;
+    uint32_t soff[NS];
+#pragma unroll
+    for (int j = 0; j < NS; j++) {
+        const int row = weight_row((lane + 64 * j) / NS);
+        soff[j] = (uint32_t)(FMT == FMT_I4G ? row : row >> 7) * (uint32_t)a.ng;
     }
+    char *const wl = smem + XS + wave * (64 * WB);       // the wave's own weights in LDS
 
     f32x4v acc[MF][4];
 #pragma unroll
@@ -203,13 +215,10 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
 #pragma unroll
         for (int n = 0; n < 4; n++) acc[m][n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 
-    constexpr int WD = FMT == FMT_FP8 ? 4 : 2;           // raw dwords per lane, row and step
-    constexpr int NS = TK / FG;                          // scales per row and step
     f16x8 av[NP][PT];
-    uint32_t wv[4][WD];
-    float sv[4][NS];
+    u32x4 wv[WD];
+    float sv[NS];
     const int gs = FMT == FMT_FP8 ? 128 : a.gs;
-    const uint32_t lane_b = FMT == FMT_FP8 ? lg * 16 : FG == 64 ? lg * 8 : lg * 4;
     uint32_t group = 0;                                  // scale group of the next load
     int done = 0;                                        // its columns already loaded
 
@@ -230,50 +239,61 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
             for (int i = 0; i < PT; i++) xs[buf][q][tid + 256 * i] = av[q][i];
     };
     auto load_w = [&](int k0) {
-        const uint32_t kb = (FMT == FMT_I4G ? k0 / 2 : k0) + lane_b;
-        const uint32_t end = (uint32_t)rb - WD * 4;
+        const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? k0 / 2 : k0) + lane_b,
+                                (uint32_t)rb - 16);
 #pragma unroll
-        for (int n = 0; n < 4; n++) {
-            const uint8_t *src = wbase + woff[n];
-            if (FMT == FMT_FP8) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(src + min(kb, end));
-                wv[n][0] = v.x; wv[n][1] = v.y; wv[n][WD - 2] = v.z; wv[n][WD - 1] = v.w;
-            } else if (FG == 64) {
-                const u32x2 v = *reinterpret_cast<const u32x2 *>(src + min(kb, end));
-                wv[n][0] = v.x; wv[n][1] = v.y;
-            } else {
-                wv[n][0] = *reinterpret_cast<const uint32_t *>(src + kb);
-                wv[n][1] = *reinterpret_cast<const uint32_t *>(src + min(kb + 16, end + 4));
-            }
-        }
+        for (int i = 0; i < WD; i++)
+            wv[i] = *reinterpret_cast<const u32x4 *>(wbase + (woff[i] + kb));
+        // lane: row (lane + 64 j) / NS of the wave's, group lane % NS
+        uint32_t gl = 0;
 #pragma unroll
         for (int j = 0; j < NS; j++) {
-            const uint32_t gj = min(group, (uint32_t)a.ng - 1);
-#pragma unroll
-            for (int n = 0; n < 4; n++) sv[n][j] = sbase[soff[n] + gj];
+            gl = j == 0 || (lane & 1) ? group : gl;
             done += FG;
             group += done == gs;
             done = done == gs ? 0 : done;
         }
+        gl = min(gl, (uint32_t)a.ng - 1);
+#pragma unroll
+        for (int j = 0; j < NS; j++) sv[j] = sbase[soff[j] + gl];
+    };
+    auto store_w = [&]() {
+#pragma unroll
+        for (int i = 0; i < WD; i++) reinterpret_cast<u32x4 *>(wl)[lane + 64 * i] = wv[i];
     };
 
     load_a(0);
     load_w(0);
     store_a(0);
+    store_w();
     __syncthreads();
     int buf = 0;
     for (int k0 = 0; k0 < p.Ip; k0 += TK) {
-        // unpack this step's weights, then ask for the next step's data
+        // unpack this step's weights, ask for the next step's data
         f16x8 bv[4][2];
         float sc[4][NS];
 #pragma unroll
         for (int n = 0; n < 4; n++) {
+            const char *wr = wl + (n * 16 + li) * WB;
+            if constexpr (FMT == FMT_FP8) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(wr + lg * 16);
+                bv[n][0] = fp8x8_f16(v.x, v.y);
+                bv[n][1] = fp8x8_f16(v.z, v.w);
+            } else if constexpr (FG == 64) {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(wr + lg * 8);
+                bv[n][0] = nib8_f16(v.x);
+                bv[n][1] = nib8_f16(v.y);
+            } else {
+                bv[n][0] = nib8_f16(*reinterpret_cast<const uint32_t *>(wr + lg * 4));
+                bv[n][1] = nib8_f16(*reinterpret_cast<const uint32_t *>(wr + 16 + lg * 4));
+            }
 #pragma unroll
-            for (int h = 0; h < 2; h++)
-                bv[n][h] = FMT == FMT_FP8 ? fp8x8_f16(wv[n][(2 * h) % WD], wv[n][(2 * h + 1) % WD])
-                                          : nib8_f16(wv[n][h]);
-#pragma unroll
-            for (int j = 0; j < NS; j++) sc[n][j] = sv[n][j];
+            for (int j = 0; j < NS; j++) {
+                const int from = (n * 16 * NS) % 64 + li * NS + j;
+                sc[n][j] = __builtin_bit_cast(
+                    float, __builtin_amdgcn_ds_bpermute(
+                               from * 4, __builtin_bit_cast(int, sv[n * NS / 4])));
+            }
         }
         const int next = min(k0 + TK, p.Ip - TK);
         load_a(next);
@@ -290,7 +310,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     const int ch = FG == 64 ? 2 * lg + h : 4 * h + lg;
-                    am[m & 1][q][h] = xs[buf][q][(m * 16 + li) * 8 + (ch ^ (li & 7))];
+                    am[m & 1][q][h] = xs[buf][q][(m * 16 + li) * 8 + (ch ^ (li >> 1))];
                 }
         };
         auto flush = [&](int s) {
@@ -323,6 +343,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
         }
         flush(2 * NS * MF - 1);
         store_a(buf ^ 1);
+        store_w();
         __syncthreads();
         buf ^= 1;
     }
