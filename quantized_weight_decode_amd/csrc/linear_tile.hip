@@ -68,6 +68,15 @@ __global__ __launch_bounds__(256) void pack_rows(const typename XT::raw *__restr
     }
 }
 
+// (w & mask) | bits in one instruction: an instruction takes one scalar
+// operand and no literal here, which the compiler splits into two.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits)
+{
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(w), "s"(mask), "v"(bits));
+    return r;
+}
+
 // Eight nibbles of a dword as q - 8 in f16, exactly, in the column order 0 4
 // 1 5 2 6 3 7: 0x6400 | q is 1024 + q, and 0x6400 | 16 q is 1024 + 16 q =
 // 16 (q - 8) + 1152.
@@ -78,10 +87,10 @@ __device__ __forceinline__ f16x8 nib8_f16(uint32_t w)
     const f16x2 c0 = {(_Float16)-1032.0f, (_Float16)-1032.0f};
     const f16x2 c1 = {(_Float16)-72.0f, (_Float16)-72.0f};
     const uint32_t w8 = w >> 8;
-    const f16x2 a = __builtin_bit_cast(f16x2, (w & 0x000F000Fu) | 0x64006400u);
-    const f16x2 b = __builtin_bit_cast(f16x2, (w & 0x00F000F0u) | 0x64006400u);
-    const f16x2 c = __builtin_bit_cast(f16x2, (w8 & 0x000F000Fu) | 0x64006400u);
-    const f16x2 d = __builtin_bit_cast(f16x2, (w8 & 0x00F000F0u) | 0x64006400u);
+    const f16x2 a = __builtin_bit_cast(f16x2, and_or(w, 0x000F000Fu, 0x64006400u));
+    const f16x2 b = __builtin_bit_cast(f16x2, and_or(w, 0x00F000F0u, 0x64006400u));
+    const f16x2 c = __builtin_bit_cast(f16x2, and_or(w8, 0x000F000Fu, 0x64006400u));
+    const f16x2 d = __builtin_bit_cast(f16x2, and_or(w8, 0x00F000F0u, 0x64006400u));
     const f16x2 r0 = a * one + c0, r1 = b * sixteenth + c1;
     const f16x2 r2 = c * one + c0, r3 = d * sixteenth + c1;
     return f16x8{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
@@ -99,6 +108,18 @@ __device__ __forceinline__ f16x8 fp8x8_f16(uint32_t a, uint32_t b)
 
 constexpr int TK = 64;          // columns per K step
 constexpr int TN = 256;         // rows of W per workgroup tile
+
+// Where a row's 16-byte chunk c of a K step sits in its 128 bytes: c ^
+// swizzle(row).  A 16-byte LDS read of a wave is served in four passes, lanes
+// 0-3, 12-15, 20-27, then 4-11, 16-19, 28-31, then the same of the upper half;
+// with this key the 16 lanes of each pass touch all 64 banks once, for both
+// column orders (bank conflicts measured: none; with row % 8 or row / 2 % 8
+// as key each read took twice as long).
+__device__ __forceinline__ int swizzle(int row)
+{
+    const int j = row >> 1;
+    return (j & 1) | ((j >> 1) & 2) | ((j ^ (j >> 1)) & 2) << 1;
+}
 
 struct TileArgs {
     LinearArgs a;
@@ -180,7 +201,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
             r = a.rows[r];
             r = r < 0 || r >= a.T ? 0 : r;
         }
-        asrc[i] = p.hi + (size_t)r * p.Ip + ((c & 7) ^ ((row >> 1) & 7)) * 8;
+        asrc[i] = p.hi + (size_t)r * p.Ip + ((c & 7) ^ swizzle(row)) * 8;
     }
     const long long lo_off = NP == 2 ? p.lo - p.hi : 0;
 
@@ -310,7 +331,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     const int ch = FG == 64 ? 2 * lg + h : 4 * h + lg;
-                    am[m & 1][q][h] = xs[buf][q][(m * 16 + li) * 8 + (ch ^ (li >> 1))];
+                    am[m & 1][q][h] = xs[buf][q][(m * 16 + li) * 8 + (ch ^ swizzle(li))];
                 }
         };
         auto flush = [&](int s) {
@@ -339,6 +360,13 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
             g[s & 1][0] = t0;
             g[s & 1][1] = t1;
             if (s > 0) flush(s - 1);
+#ifndef NOSGB
+#pragma unroll
+            for (int i = 0; i < 4 * NP / NS; i++) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 2 * NS, 0);
+            }
+#endif
             __builtin_amdgcn_sched_barrier(0);
         }
         flush(2 * NS * MF - 1);
