@@ -106,6 +106,27 @@ __device__ __forceinline__ f16x8 fp8x8_f16(uint32_t a, uint32_t b)
     return f16x8{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
 }
 
+// Memory to LDS without registers: lane i's 16 (4) bytes from base + off go to
+// LDS bytes lds + 16 i (4 i); lds is uniform over the wave.  The compiler does
+// not count these loads: the K loop waits for them itself (wait_loads), and
+// holds no other vector-memory loads.
+__device__ __forceinline__ void load_lds16(const void *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(lds), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds4(const void *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 :: "s"(lds), "v"(off), "s"(base) : "memory");
+}
+// All but the wave's last n loads have arrived, for every wave of the group.
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "i"(N) : "memory");
+}
+
 constexpr int TK = 64;          // columns per K step
 constexpr int TN = 256;         // rows of W per workgroup tile
 
@@ -151,13 +172,16 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     constexpr int LDO = TN + 4;                          // epilogue row stride, floats
     constexpr int WB = FMT == FMT_FP8 ? 64 : 32;         // bytes of a row and step
     constexpr int WD = WB / 16;                          // 16-byte pieces per lane and step
-    constexpr size_t XS = 2 * NP * CH * sizeof(f16x8), WS = (size_t)TN * WB;
-    constexpr size_t OS = 16 * LDO * sizeof(float);
-    __shared__ __align__(16) char smem[XS + WS > OS ? XS + WS : OS];
+    constexpr int NS = TK / FG;                          // scales per row and step
+    // a stage of LDS: activations, weights, scales of one K step
+    constexpr uint32_t XB = NP * CH * 16, WO = XB, SO = WO + TN * WB, STAGE = SO + TN * NS * 4;
+    constexpr int ST = 3;                                // stages: two steps of loads in flight
+    constexpr uint32_t OS = 16 * LDO * sizeof(float);
+    __shared__ __align__(16) char smem[ST * STAGE > OS ? ST * STAGE : OS];
     __shared__ int rx[BM];
-    f16x8 (*const xs)[NP][CH] = reinterpret_cast<f16x8 (*)[NP][CH]>(smem);
     const LinearArgs &a = p.a;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, lg = lane >> 4;
     const int oc = GATED ? a.O / 2 : a.O;
 
@@ -171,6 +195,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
         mt = b / p.ntn;
         nt = b % p.ntn;
         t = p.tiles[mt];
+        t.expert = __builtin_amdgcn_readfirstlane(t.expert);
         if (t.n <= 0) return;
     } else {                                             // a column block's rows together
         nt = b / p.ntm;
@@ -191,7 +216,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     }
 
     // activation chunks of this thread: row c / 8, swizzled chunk c % 8
-    const _Float16 *asrc[PT];
+    uint32_t aoff[PT];
 #pragma unroll
     for (int i = 0; i < PT; i++) {
         const int c = tid + 256 * i;
@@ -201,16 +226,14 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
             r = a.rows[r];
             r = r < 0 || r >= a.T ? 0 : r;
         }
-        asrc[i] = p.hi + (size_t)r * p.Ip + ((c & 7) ^ swizzle(row)) * 8;
+        aoff[i] = ((uint32_t)r * (uint32_t)p.Ip + ((c & 7) ^ swizzle(row)) * 8) * 2;
     }
-    const long long lo_off = NP == 2 ? p.lo - p.hi : 0;
 
     // weight rows of this lane
     const size_t rb = FMT == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
-    const uint8_t *wbase = a.w + (size_t)t.expert * a.w_stride;
-    const float *sbase = a.scales + (size_t)t.expert * a.s_stride;
+    const uint8_t *const wbase = a.w + (size_t)t.expert * a.w_stride;
+    const float *const sbase = a.scales + (size_t)t.expert * a.s_stride;
     constexpr int CW = GATED ? 32 : 64;                  // columns of y per wave
-    constexpr int NS = TK / FG;                          // scales per row and step
     // row i of the wave's 64 (block i / 16 of n)
     auto weight_row = [&](int i) {
         const int n = i >> 4;
@@ -228,7 +251,6 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
         const int row = weight_row((lane + 64 * j) / NS);
         soff[j] = (uint32_t)(FMT == FMT_I4G ? row : row >> 7) * (uint32_t)a.ng;
     }
-    char *const wl = smem + XS + wave * (64 * WB);       // the wave's own weights in LDS
 
     f32x4v acc[MF][4];
 #pragma unroll
@@ -236,35 +258,30 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
 #pragma unroll
         for (int n = 0; n < 4; n++) acc[m][n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 
-    f16x8 av[NP][PT];
-    u32x4 wv[WD];
-    float sv[NS];
     const int gs = FMT == FMT_FP8 ? 128 : a.gs;
     uint32_t group = 0;                                  // scale group of the next load
     int done = 0;                                        // its columns already loaded
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem);
 
-    // The loop's body has no branches: loads past the last step repeat it, and
-    // in a last half step (I % 64 == 32) the lanes behind the row's end read
-    // its last bytes again, which meet zeros of x.
-    auto load_a = [&](int k0) {
+    // Loads of one step into a stage.  Past the last step they repeat it; in a
+    // last half step (I % 64 == 32) the lanes behind the row's end read its
+    // last bytes again, which meet zeros of x.
+    constexpr int LOADS = NP * PT + WD + NS;             // per wave
+    auto load = [&](int k0, int stage) {
+        k0 = min(k0, p.Ip - TK);
+        const uint32_t at = lds0 + stage * STAGE;
 #pragma unroll
         for (int q = 0; q < NP; q++)
 #pragma unroll
             for (int i = 0; i < PT; i++)
-                av[q][i] = *reinterpret_cast<const f16x8 *>(asrc[i] + q * lo_off + k0);
-    };
-    auto store_a = [&](int buf) {
-#pragma unroll
-        for (int q = 0; q < NP; q++)
-#pragma unroll
-            for (int i = 0; i < PT; i++) xs[buf][q][tid + 256 * i] = av[q][i];
-    };
-    auto load_w = [&](int k0) {
+                load_lds16((q ? p.lo : p.hi) + k0, aoff[i],
+                           at + (q * CH + wave * 64 + 256 * i) * 16);
         const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? k0 / 2 : k0) + lane_b,
                                 (uint32_t)rb - 16);
 #pragma unroll
         for (int i = 0; i < WD; i++)
-            wv[i] = *reinterpret_cast<const u32x4 *>(wbase + (woff[i] + kb));
+            load_lds16(wbase, woff[i] + kb, at + WO + wave * (64 * WB) + 1024 * i);
         // lane: row (lane + 64 j) / NS of the wave's, group lane % NS
         uint32_t gl = 0;
 #pragma unroll
@@ -276,21 +293,22 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
         }
         gl = min(gl, (uint32_t)a.ng - 1);
 #pragma unroll
-        for (int j = 0; j < NS; j++) sv[j] = sbase[soff[j] + gl];
-    };
-    auto store_w = [&]() {
-#pragma unroll
-        for (int i = 0; i < WD; i++) reinterpret_cast<u32x4 *>(wl)[lane + 64 * i] = wv[i];
+        for (int j = 0; j < NS; j++)
+            load_lds4(sbase, (soff[j] + gl) * 4, at + SO + wave * (256 * NS) + 256 * j);
     };
 
-    load_a(0);
-    load_w(0);
-    store_a(0);
-    store_w();
-    __syncthreads();
-    int buf = 0;
+    __syncthreads();                                     // rx; earlier loads are done
+    load(0, 0);
+    load(TK, 1);
+    int stage = 0;
     for (int k0 = 0; k0 < p.Ip; k0 += TK) {
-        // unpack this step's weights, ask for the next step's data
+        // this step's stage is there; the one that the last step read is free
+        wait_loads<LOADS>();
+        load(k0 + 2 * TK, stage == 0 ? 2 : stage - 1);
+        const char *const sm = smem + stage * STAGE;
+        const char *const wl = sm + WO + wave * (64 * WB);
+        const float *const sl = reinterpret_cast<const float *>(sm + SO) + wave * (64 * NS);
+        const f16x8 (*const xs)[CH] = reinterpret_cast<const f16x8 (*)[CH]>(sm);
         f16x8 bv[4][2];
         float sc[4][NS];
 #pragma unroll
@@ -309,16 +327,8 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
                 bv[n][1] = nib8_f16(*reinterpret_cast<const uint32_t *>(wr + 16 + lg * 4));
             }
 #pragma unroll
-            for (int j = 0; j < NS; j++) {
-                const int from = (n * 16 * NS) % 64 + li * NS + j;
-                sc[n][j] = __builtin_bit_cast(
-                    float, __builtin_amdgcn_ds_bpermute(
-                               from * 4, __builtin_bit_cast(int, sv[n * NS / 4])));
-            }
+            for (int j = 0; j < NS; j++) sc[n][j] = sl[(n * 16 + li) * NS + j];
         }
-        const int next = min(k0 + TK, p.Ip - TK);
-        load_a(next);
-        load_w(next);
         // Steps of two 16 x 16 blocks (n, n + 1) of one row block m and scale
         // group j: a step's sums are added to the totals while the next
         // step's matrix instructions run.  The scheduling barrier keeps the
@@ -331,7 +341,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     const int ch = FG == 64 ? 2 * lg + h : 4 * h + lg;
-                    am[m & 1][q][h] = xs[buf][q][(m * 16 + li) * 8 + (ch ^ swizzle(li))];
+                    am[m & 1][q][h] = xs[q][(m * 16 + li) * 8 + (ch ^ swizzle(li))];
                 }
         };
         auto flush = [&](int s) {
@@ -370,15 +380,13 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
             __builtin_amdgcn_sched_barrier(0);
         }
         flush(2 * NS * MF - 1);
-        store_a(buf ^ 1);
-        store_w();
-        __syncthreads();
-        buf ^= 1;
+        stage = stage == ST - 1 ? 0 : stage + 1;
     }
+    // loads past the last step still write LDS
+    wait_loads<0>();
 
     // Epilogue, 16 rows at a time through LDS: whole rows are stored, and the
-    // end of an output is one piece of code.  (The last K step ended with a
-    // barrier, so the activations' LDS is free.)
+    // end of an output is one piece of code.
     float *os = reinterpret_cast<float *>(smem);
     constexpr int YC = 4 * CW;                           // columns of y
     const int ec = tid % YC, er = tid / YC;
@@ -445,7 +453,7 @@ bool tile_fits(WeightFormat fmt, const LinearArgs &a)
     const size_t rb = fmt == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
     return a.I % 32 == 0 && (fmt == FMT_FP8 || a.gs % 32 == 0) && ((uintptr_t)a.w & 15) == 0 &&
            (!a.offsets || a.w_stride % 16 == 0) && rb * a.O < (1ull << 32) &&
-           (size_t)a.ng * a.O < (1ull << 32);
+           (size_t)a.ng * a.O * 4 < (1ull << 32) && (size_t)a.T * padded(a.I) * 2 < (1ull << 32);
 }
 
 hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, int bm, const RowTile *tiles,
