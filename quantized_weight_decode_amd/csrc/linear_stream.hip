@@ -88,20 +88,16 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b)
     return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
-// Eight activations of a lane as bf16 parts, in the weights' column order.
+// Eight activations of a lane, read from LDS as they are in memory, as NP bf16
+// parts in the weights' column order.
 template <typename XT, int FMT>
 struct XFrag;
 template <int FMT>
 struct XFrag<BF16, FMT> {
     static constexpr int NP = 1;
-    u32x4 v;
-    __device__ __forceinline__ void load(const uint16_t *p, bool ok)
+    static __device__ __forceinline__ void parts(const char *p, bf16x8 out[1])
     {
-        v = u32x4{0, 0, 0, 0};
-        if (ok) v = *reinterpret_cast<const u32x4 *>(p);
-    }
-    __device__ __forceinline__ void parts(bf16x8 out[1]) const
-    {
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
         u32x4 o = v;
         if (FMT == FMT_I4G) {
             o.x = low_halves(v.x, v.y);
@@ -117,17 +113,10 @@ struct XFrag<BF16, FMT> {
 template <int FMT>
 struct XFrag<F32, FMT> {
     static constexpr int NP = 3;
-    f32x4 a, b;
-    __device__ __forceinline__ void load(const float *p, bool ok)
+    static __device__ __forceinline__ void parts(const char *p, bf16x8 out[3])
     {
-        a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (ok) {
-            a = *reinterpret_cast<const f32x4 *>(p);
-            b = *reinterpret_cast<const f32x4 *>(p + 4);
-        }
-    }
-    __device__ __forceinline__ void parts(bf16x8 out[3]) const
-    {
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(p);
+        const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 16);
         uint32_t h[3][8];
 #pragma unroll
         for (int j = 0; j < 8; j++) {
@@ -168,7 +157,13 @@ struct StreamArgs {
 // together they read 512 bytes of a row at a time, and their sums are joined
 // through LDS in a fixed order.  v_mfma_f32_16x16x32_bf16, lane l: A row of x
 // l % 16, B row of W l % 16, eight columns from the lane group l / 16.
-// Weights and activations of D chunks are in flight per wave.
+//
+// Lanes next to each other load 16-byte pieces of one row (a load of 64 lanes
+// in 64 different rows takes the vector cache 64 cycles, whatever its width:
+// measured 23 us so and 2x less this way for one row at 6144 x 12288); each
+// wave passes its chunk through its own part of LDS to get the fragments'
+// order, and scales by lane permutes.  The loads of D chunks are in flight per
+// wave.
 //
 // bf16 activations multiply the nibbles q themselves, and the group's sum
 // starts from -8 sum(x), one more matrix instruction per group: |error| <=
@@ -185,69 +180,93 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     constexpr bool OFFSET = FMT == FMT_I4G && NP == 1;
     constexpr int NG = SC / FG;                          // scale groups of a chunk
     constexpr int TPG = 4 / NG;                          // 32-column steps of a group
-    constexpr int WL = FMT == FMT_FP8 ? 2 : 1;           // 16-byte loads per row and chunk
+    constexpr int WP = FMT == FMT_FP8 ? 8 : 4;           // 16-byte pieces of a row and chunk
+    constexpr int WL = NB * 16 * WP / 64;                // weight loads of a lane and chunk
+    constexpr int SL = (NB * 16 * NG + 63) / 64;         // scale loads
+    constexpr int XP = SC * sizeof(raw) / 16;            // 16-byte pieces of a row of x
+    constexpr int XR = 64 / XP;                          // rows of x per load
+    constexpr int XL = 16 / XR;                          // loads of x for 16 rows
+    constexpr int XROW = SC * sizeof(raw) + 16;          // LDS row stride, bytes
     constexpr int YC = GATED ? NB * 8 : NB * 16;         // columns of y
     constexpr int LDR = NB * 16 + 4;
-    __shared__ float red[SW][16][LDR];
+    constexpr int WB = WL * 1024, WAVE_LDS = WB + 16 * XROW;
+    constexpr int RED = SW * 16 * LDR * 4;
+    __shared__ __align__(16) char smem[SW * WAVE_LDS > RED ? SW * WAVE_LDS : RED];
     const LinearArgs &a = p.a;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, lg = lane >> 4;
     const int oc = GATED ? a.O / 2 : a.O;
     const int nt = (int)(blockIdx.x % p.ntn), mt = (int)(blockIdx.x / p.ntn);
     RowTile t;
     if (p.tiles) t = p.tiles[mt];
     else t = RowTile{0, mt * 16, min(16, a.R - mt * 16), 0};
+    t.n = __builtin_amdgcn_readfirstlane(t.n);
+    t.expert = __builtin_amdgcn_readfirstlane(t.expert);
     if (t.n <= 0) return;                                // uniform over the workgroup
 
-    const bool xok = li < t.n;
-    int xrow = t.row0 + (xok ? li : 0);
-    if (a.rows) {
-        xrow = a.rows[xrow];
-        if (xrow < 0 || xrow >= a.T) xrow = 0;           // marked in the epilogue
+    // x: lane's piece lane % XP of row lane / XP + XR i of the tile
+    const raw *xp[XL];
+#pragma unroll
+    for (int i = 0; i < XL; i++) {
+        int r = lane / XP + XR * i;
+        r = t.row0 + (r < t.n ? r : 0);
+        if (a.rows) {
+            r = a.rows[r];
+            if (r < 0 || r >= a.T) r = 0;                // marked in the epilogue
+        }
+        xp[i] = static_cast<const raw *>(a.x) + (size_t)r * a.ldx +
+                (lane % XP) * (16 / sizeof(raw));
     }
-    const raw *xp = static_cast<const raw *>(a.x) + (size_t)xrow * a.ldx;
 
     const size_t rb = FMT == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
-    const uint8_t *wbase = a.w + (size_t)t.expert * a.w_stride;
-    const float *sbase = a.scales + (size_t)t.expert * a.s_stride;
-    uint32_t woff[NB], soff[NB];
-#pragma unroll
-    for (int n = 0; n < NB; n++) {
+    const uint8_t *const wbase = a.w + (size_t)t.expert * a.w_stride;
+    const float *const sbase = a.scales + (size_t)t.expert * a.s_stride;
+    // row i of the workgroup's 16 NB
+    auto weight_row = [&](int i) {
+        const int n = i >> 4;
         const int half = GATED ? n / (NB / 2) : 0;
-        const int c = nt * YC + (GATED ? n % (NB / 2) : n) * 16 + li;
-        const int row = (c < oc ? c : oc - 1) + half * oc;
-        woff[n] = (uint32_t)(row * rb);
-        soff[n] = (uint32_t)(FMT == FMT_I4G ? row : row >> 7) * (uint32_t)a.ng;
+        const int c = nt * YC + (GATED ? n % (NB / 2) : n) * 16 + (i & 15);
+        return (c < oc ? c : oc - 1) + half * oc;
+    };
+    uint32_t woff[WL], soff[SL];
+#pragma unroll
+    for (int i = 0; i < WL; i++)
+        woff[i] = (uint32_t)(weight_row((lane + 64 * i) / WP) * rb);
+#pragma unroll
+    for (int i = 0; i < SL; i++) {
+        const int row = weight_row(min((lane + 64 * i) / NG, NB * 16 - 1));
+        soff[i] = (uint32_t)(FMT == FMT_I4G ? row : row >> 7) * (uint32_t)a.ng;
     }
+    const int lane_k = (lane % WP) * (FMT == FMT_FP8 ? 16 : 32);
 
-    u32x4 wr[D][NB][WL];
-    float sr[D][NB][NG];
-    Frag xr[D][4];
+    // the wave's LDS: weights, then 16 rows of x; rows past the tile's stay zero
+    char *const wl = smem + wave * WAVE_LDS;
+    char *const xl = wl + WB;
+    for (int i = lane; i < 16 * XROW / 16; i += 64)
+        reinterpret_cast<u32x4 *>(xl)[i] = u32x4{0, 0, 0, 0};
+
+    u32x4 wr[D][WL], xr[D][XL];
+    float sr[D][SL];
     const int chunks = (a.I + SC - 1) / SC;
     const int gs = FMT == FMT_FP8 ? 128 : a.gs;
     auto load = [&](int d, int c) {
-        const int k0 = (c < chunks ? c : chunks - 1) * SC;
+        const int k0 = min(c, chunks - 1) * SC;
+        // a lane behind the row's end reads the row's last bytes, which meet
+        // zeros of x
+        const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? (k0 + lane_k) / 2 : k0 + lane_k),
+                                (uint32_t)rb - 16);
 #pragma unroll
-        for (int u = 0; u < WL; u++) {
-            const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? k0 / 2 + 16 * lg
-                                                              : k0 + 64 * u + 16 * lg),
-                                    (uint32_t)rb - 16);
+        for (int i = 0; i < WL; i++)
+            wr[d][i] = ld_stream(reinterpret_cast<const u32x4 *>(wbase + (woff[i] + kb)));
+        const uint32_t gi = (uint32_t)min(k0 + (lane % NG) * FG, a.I - 1) / (uint32_t)gs;
 #pragma unroll
-            for (int n = 0; n < NB; n++)
-                wr[d][n][u] = ld_stream(reinterpret_cast<const u32x4 *>(wbase + woff[n] + kb));
-        }
+        for (int i = 0; i < SL; i++) sr[d][i] = sbase[soff[i] + gi];
+        const bool kok = k0 + (lane % XP) * (int)(16 / sizeof(raw)) < a.I && c < chunks;
 #pragma unroll
-        for (int g = 0; g < NG; g++) {
-            const int k = min(k0 + g * FG, a.I - 1);
-            const uint32_t gi = (uint32_t)(k / gs);
-#pragma unroll
-            for (int n = 0; n < NB; n++) sr[d][n][g] = sbase[soff[n] + gi];
-        }
-#pragma unroll
-        for (int s = 0; s < 4; s++) {
-            const int k = FMT == FMT_I4G ? k0 + 32 * s + 8 * lg
-                                         : k0 + 64 * (s >> 1) + 16 * lg + 8 * (s & 1);
-            xr[d][s].load(xp + k, xok && k < a.I && c < chunks);
+        for (int i = 0; i < XL; i++) {
+            xr[d][i] = u32x4{0, 0, 0, 0};
+            if (i * XR < t.n && kok) xr[d][i] = *reinterpret_cast<const u32x4 *>(xp[i] + k0);
         }
     };
 
@@ -256,20 +275,37 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     for (int n = 0; n < NB; n++) acc[n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 
     auto multiply = [&](int d) {
-        uint32_t wd[NB][4 * WL];
+        // to LDS and back in fragment order; only this wave uses this part,
+        // and its LDS operations complete in order
+#pragma unroll
+        for (int i = 0; i < WL; i++) reinterpret_cast<u32x4 *>(wl)[lane + 64 * i] = wr[d][i];
+#pragma unroll
+        for (int i = 0; i < XL; i++)
+            if (i * XR < t.n && lane / XP + XR * i < t.n)
+                *reinterpret_cast<u32x4 *>(xl + (lane / XP + XR * i) * XROW + (lane % XP) * 16) =
+                    xr[d][i];
+        uint32_t wd[NB][WP];
 #pragma unroll
         for (int n = 0; n < NB; n++) {
+            const char *row = wl + (n * 16 + li) * (WP * 16);
 #pragma unroll
-            for (int u = 0; u < WL; u++)
+            for (int u = 0; u < WP / 4; u++) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(row + 64 * u + 16 * lg);
 #pragma unroll
-                for (int j = 0; j < 4; j++) wd[n][4 * u + j] = wr[d][n][u][j];
+                for (int j = 0; j < 4; j++) wd[n][4 * u + j] = v[j];
+            }
             if (FMT == FMT_I4G) transpose4(wd[n]);
         }
 #pragma unroll
         for (int g = 0; g < NG; g++) {
             bf16x8 xv[TPG][NP];
 #pragma unroll
-            for (int s = 0; s < TPG; s++) xr[d][g * TPG + s].parts(xv[s]);
+            for (int s = 0; s < TPG; s++) {
+                const int st = g * TPG + s;
+                const int k = FMT == FMT_I4G ? 32 * st + 8 * lg
+                                             : 64 * (st >> 1) + 16 * lg + 8 * (st & 1);
+                Frag::parts(xl + li * XROW + k * sizeof(raw), xv[s]);
+            }
             f32x4v z = {0.0f, 0.0f, 0.0f, 0.0f};
             if (OFFSET) {
                 const u32x4 m8 = {0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u};
@@ -288,17 +324,22 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
                     if (FMT == FMT_I4G) {
                         wv = OFFSET ? nib8_bf16(wd[n][st]) : nib8_bf16_signed(wd[n][st]);
                     } else {
-                        const uint32_t p0 = wd[n][(2 * st) % (4 * WL)];
-                        const uint32_t p1 = wd[n][(2 * st + 1) % (4 * WL)];
+                        const uint32_t p0 = wd[n][(2 * st) % WP];
+                        const uint32_t p1 = wd[n][(2 * st + 1) % WP];
                         wv = join(cvt_lo<0>(p0), cvt_hi<0>(p0), cvt_lo<0>(p1), cvt_hi<0>(p1));
                     }
 #pragma unroll
                     for (int q = NP - 1; q >= 0; q--)    // small parts first
                         sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[s][q], wv, sum, 0, 0, 0);
                 }
+                const int from = (n * 16 * NG) % 64 + li * NG + g;
+                const float sc = __builtin_bit_cast(
+                    float, __builtin_amdgcn_ds_bpermute(
+                               from * 4, __builtin_bit_cast(int, sr[d][n * NG / 4])));
 #pragma unroll
-                for (int r = 0; r < 4; r++) acc[n][r] = fmaf(sr[d][n][g], sum[r], acc[n][r]);
+                for (int r = 0; r < 4; r++) acc[n][r] = fmaf(sc, sum[r], acc[n][r]);
             }
+            if (NG == 4) __builtin_amdgcn_sched_barrier(0);    // keeps registers down
         }
     };
 
@@ -314,6 +355,8 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
         }
     }
 
+    __syncthreads();
+    float (*const red)[16][LDR] = reinterpret_cast<float (*)[16][LDR]>(smem);
 #pragma unroll
     for (int n = 0; n < NB; n++)
 #pragma unroll
