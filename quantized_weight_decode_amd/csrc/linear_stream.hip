@@ -55,15 +55,29 @@ __device__ __forceinline__ bf16x2 cvt_hi(uint32_t w)
     return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, (float)(1 << E), true);
 }
 
-// Eight nibbles in the column order 0 2 4 6 1 3 5 7, in bf16.  Read as E4M3
-// codes, 0..15 are n 2^-9, so bytes of one nibble each convert two at a time.
-// Plain: the nibbles q.
+// (w & mask) | bits in one instruction: it takes one scalar operand and no
+// literal here, so the constants are shown to the compiler as values in a
+// scalar and a vector register.  (The instruction itself stays the compiler's,
+// which keeps its distance to a matrix instruction that reads the result.)
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits)
+{
+    asm("" : "+s"(mask));
+    asm("" : "+v"(bits));
+    return (w & mask) | bits;
+}
+
+// Eight nibbles as 16 + q in bf16 (0x4180 | 8 q), in the column order 0 4 1 5
+// 2 6 3 7.
 __device__ __forceinline__ bf16x8 nib8_bf16(uint32_t w)
 {
-    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
-    return join(cvt_lo<9>(lo), cvt_hi<9>(lo), cvt_lo<9>(hi), cvt_hi<9>(hi));
+    constexpr uint32_t M = 0x00780078u, B = 0x41804180u;
+    const u32x4 o = {and_or(w << 3, M, B), and_or(w >> 1, M, B), and_or(w >> 5, M, B),
+                     and_or(w >> 9, M, B)};
+    return __builtin_bit_cast(bf16x8, o);
 }
-// Signed: q - 8.  t = the two's complement nibble; its code is t for t < 8,
+// Eight nibbles as q - 8, in the column order 0 2 4 6 1 3 5 7.  Read as E4M3
+// codes, 0..15 are n 2^-9, so bytes of one nibble each convert two at a time.
+// t = the two's complement nibble; its code is t for t < 8,
 // else 0x90 - t (sign bit and 16 - t) = (t ^ 0x8F) + 1.
 __device__ __forceinline__ uint32_t signed_codes(uint32_t t)
 {
@@ -100,10 +114,10 @@ struct XFrag<BF16, FMT> {
         const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
         u32x4 o = v;
         if (FMT == FMT_I4G) {
-            o.x = low_halves(v.x, v.y);
-            o.y = low_halves(v.z, v.w);
-            o.z = high_halves(v.x, v.y);
-            o.w = high_halves(v.z, v.w);
+            o.x = low_halves(v.x, v.z);
+            o.y = high_halves(v.x, v.z);
+            o.z = low_halves(v.y, v.w);
+            o.w = high_halves(v.y, v.w);
         }
         out[0] = __builtin_bit_cast(bf16x8, o);
     }
@@ -250,10 +264,20 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     float sr[D][SL];
     const int chunks = (a.I + SC - 1) / SC;
     const int gs = FMT == FMT_FP8 ? 128 : a.gs;
+    const int nx = (t.n + XR - 1) / XR;                  // loads of x that hold rows
+    auto x_inside = [&](int c) {                         // this lane's columns exist
+        return c * SC + (lane % XP) * (int)(16 / sizeof(raw)) < a.I;
+    };
+    // Past the last chunk, and for a lane behind the row's end, loads repeat
+    // valid data, which multiply() meets with zeros of x.  x goes first: how
+    // many of its loads there are varies, and the wait for a slot then also
+    // waits for as many of the next slot's first loads.
     auto load = [&](int d, int c) {
         const int k0 = min(c, chunks - 1) * SC;
-        // a lane behind the row's end reads the row's last bytes, which meet
-        // zeros of x
+        const int kx = x_inside(c) ? k0 : 0;
+#pragma unroll
+        for (int i = 0; i < XL; i++)
+            if (i < nx) xr[d][i] = *reinterpret_cast<const u32x4 *>(xp[i] + kx);
         const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? (k0 + lane_k) / 2 : k0 + lane_k),
                                 (uint32_t)rb - 16);
 #pragma unroll
@@ -262,28 +286,24 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
         const uint32_t gi = (uint32_t)min(k0 + (lane % NG) * FG, a.I - 1) / (uint32_t)gs;
 #pragma unroll
         for (int i = 0; i < SL; i++) sr[d][i] = sbase[soff[i] + gi];
-        const bool kok = k0 + (lane % XP) * (int)(16 / sizeof(raw)) < a.I && c < chunks;
-#pragma unroll
-        for (int i = 0; i < XL; i++) {
-            xr[d][i] = u32x4{0, 0, 0, 0};
-            if (i * XR < t.n && kok) xr[d][i] = *reinterpret_cast<const u32x4 *>(xp[i] + k0);
-        }
     };
 
     f32x4v acc[NB];
 #pragma unroll
     for (int n = 0; n < NB; n++) acc[n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto multiply = [&](int d) {
+    auto multiply = [&](int d, int c) {
         // to LDS and back in fragment order; only this wave uses this part,
         // and its LDS operations complete in order
 #pragma unroll
         for (int i = 0; i < WL; i++) reinterpret_cast<u32x4 *>(wl)[lane + 64 * i] = wr[d][i];
 #pragma unroll
-        for (int i = 0; i < XL; i++)
-            if (i * XR < t.n && lane / XP + XR * i < t.n)
+        for (int i = 0; i < XL; i++) {
+            const u32x4 v = x_inside(c) ? xr[d][i] : u32x4{0, 0, 0, 0};
+            if (i < nx && lane / XP + XR * i < t.n)
                 *reinterpret_cast<u32x4 *>(xl + (lane / XP + XR * i) * XROW + (lane % XP) * 16) =
-                    xr[d][i];
+                    v;
+        }
         uint32_t wd[NB][WP];
 #pragma unroll
         for (int n = 0; n < NB; n++) {
@@ -308,11 +328,11 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
             }
             f32x4v z = {0.0f, 0.0f, 0.0f, 0.0f};
             if (OFFSET) {
-                const u32x4 m8 = {0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u};
+                const u32x4 m24 = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
 #pragma unroll
                 for (int s = 0; s < TPG; s++)
                     z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        xv[s][0], __builtin_bit_cast(bf16x8, m8), z, 0, 0, 0);
+                        xv[s][0], __builtin_bit_cast(bf16x8, m24), z, 0, 0, 0);
             }
 #pragma unroll
             for (int n = 0; n < NB; n++) {
@@ -347,8 +367,8 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     for (int d = 0; d < D; d++) load(d, wave + d * SW);
     for (int c = wave; c < chunks; c += D * SW) {
 #pragma unroll
-        for (int d = 0; d < D; d++) {                    // slots past the end hold zeros of x
-            multiply(d);
+        for (int d = 0; d < D; d++) {
+            multiply(d, c + d * SW);
             __builtin_amdgcn_sched_barrier(0);
             load(d, c + (d + D) * SW);
             __builtin_amdgcn_sched_barrier(0);

@@ -68,13 +68,15 @@ __global__ __launch_bounds__(256) void pack_rows(const typename XT::raw *__restr
     }
 }
 
-// (w & mask) | bits in one instruction: an instruction takes one scalar
-// operand and no literal here, which the compiler splits into two.
+// (w & mask) | bits in one instruction: it takes one scalar operand and no
+// literal here, so the constants are shown to the compiler as values in a
+// scalar and a vector register.  (The instruction itself stays the compiler's,
+// which keeps its distance to a matrix instruction that reads the result.)
 __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits)
 {
-    uint32_t r;
-    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(w), "s"(mask), "v"(bits));
-    return r;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(bits));
+    return (w & mask) | bits;
 }
 
 // Eight nibbles of a dword as q - 8 in f16, exactly, in the column order 0 4
