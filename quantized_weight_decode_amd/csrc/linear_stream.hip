@@ -167,17 +167,15 @@ struct StreamArgs {
 };
 
 // Stream kernel.  A workgroup of 8 waves makes up to 16 rows of y x 16 NB
-// rows of W; the waves take the chunks of 128 columns in turn, so that
-// together they read 512 bytes of a row at a time, and their sums are joined
-// through LDS in a fixed order.  v_mfma_f32_16x16x32_bf16, lane l: A row of x
+// rows of W; the waves take blocks of P chunks of 128 columns in turn, and
+// their sums are joined through LDS in a fixed order.  v_mfma_f32_16x16x32_bf16, lane l: A row of x
 // l % 16, B row of W l % 16, eight columns from the lane group l / 16.
 //
 // Lanes next to each other load 16-byte pieces of one row (a load of 64 lanes
-// in 64 different rows takes the vector cache 64 cycles, whatever its width:
-// measured 23 us so and 2x less this way for one row at 6144 x 12288); each
-// wave passes its chunk through its own part of LDS to get the fragments'
-// order, and scales by lane permutes.  The loads of D chunks are in flight per
-// wave.
+// in 64 different rows takes the vector cache 64 cycles, whatever its width),
+// whole 128-byte lines at a time.  Each wave passes its block through its own
+// part of LDS to get the fragments' order, and as soon as the weights are in
+// LDS asks for its next block, so that one block per wave is always in flight.
 //
 // bf16 activations multiply the nibbles q themselves, and the group's sum
 // starts from -8 sum(x), one more matrix instruction per group: |error| <=
@@ -185,7 +183,7 @@ struct StreamArgs {
 // activations multiply q - 8, whose unpacking costs 2.5 instead of 0.9
 // instructions per weight: an outlier of x at a zero weight must not cost the
 // small elements their bits.
-template <int FMT, typename XT, int NB, bool GATED, int FG, int D>
+template <int FMT, typename XT, int NB, bool GATED, int FG, int P>
 __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
 {
     typedef typename XT::raw raw;
@@ -194,16 +192,20 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     constexpr bool OFFSET = FMT == FMT_I4G && NP == 1;
     constexpr int NG = SC / FG;                          // scale groups of a chunk
     constexpr int TPG = 4 / NG;                          // 32-column steps of a group
-    constexpr int WP = FMT == FMT_FP8 ? 8 : 4;           // 16-byte pieces of a row and chunk
-    constexpr int WL = NB * 16 * WP / 64;                // weight loads of a lane and chunk
-    constexpr int SL = (NB * 16 * NG + 63) / 64;         // scale loads
-    constexpr int XP = SC * sizeof(raw) / 16;            // 16-byte pieces of a row of x
+    constexpr int WC = FMT == FMT_FP8 ? 8 : 4;           // 16-byte pieces of a row and chunk
+    constexpr int WP = P * WC;                           // and block
+    constexpr int WL = NB * 16 * WP / 64;                // weight loads of a lane and block
+    constexpr int WROW = WP * 16 + 16;                   // LDS row stride, bytes
+    constexpr int NGB = P * NG;                          // scale groups of a block
+    constexpr int SL = (NB * 16 * NGB + 63) / 64;        // scale loads
+    constexpr int XP = SC * sizeof(raw) / 16;            // 16-byte pieces of a row and chunk of x
     constexpr int XR = 64 / XP;                          // rows of x per load
     constexpr int XL = 16 / XR;                          // loads of x for 16 rows
     constexpr int XROW = SC * sizeof(raw) + 16;          // LDS row stride, bytes
     constexpr int YC = GATED ? NB * 8 : NB * 16;         // columns of y
     constexpr int LDR = NB * 16 + 4;
-    constexpr int WB = WL * 1024, WAVE_LDS = WB + 16 * XROW;
+    constexpr int WB = NB * 16 * WROW, SB = SL * 256;
+    constexpr int WAVE_LDS = WB + SB + 16 * XROW;
     constexpr int RED = SW * 16 * LDR * 4;
     __shared__ __align__(16) char smem[SW * WAVE_LDS > RED ? SW * WAVE_LDS : RED];
     const LinearArgs &a = p.a;
@@ -249,67 +251,80 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
         woff[i] = (uint32_t)(weight_row((lane + 64 * i) / WP) * rb);
 #pragma unroll
     for (int i = 0; i < SL; i++) {
-        const int row = weight_row(min((lane + 64 * i) / NG, NB * 16 - 1));
+        const int row = weight_row(min((lane + 64 * i) / NGB, NB * 16 - 1));
         soff[i] = (uint32_t)(FMT == FMT_I4G ? row : row >> 7) * (uint32_t)a.ng;
     }
     const int lane_k = (lane % WP) * (FMT == FMT_FP8 ? 16 : 32);
 
-    // the wave's LDS: weights, then 16 rows of x; rows past the tile's stay zero
+    // the wave's LDS: weights, scales, 16 rows of x; rows past the tile's stay
+    // zero
     char *const wl = smem + wave * WAVE_LDS;
-    char *const xl = wl + WB;
+    float *const sl = reinterpret_cast<float *>(wl + WB);
+    char *const xl = wl + WB + SB;
     for (int i = lane; i < 16 * XROW / 16; i += 64)
         reinterpret_cast<u32x4 *>(xl)[i] = u32x4{0, 0, 0, 0};
 
-    u32x4 wr[D][WL], xr[D][XL];
-    float sr[D][SL];
-    const int chunks = (a.I + SC - 1) / SC;
+    u32x4 wr[WL], xr[P][XL];
+    float sr[SL];
+    const int blocks = (a.I + P * SC - 1) / (P * SC);
     const int gs = FMT == FMT_FP8 ? 128 : a.gs;
     const int nx = (t.n + XR - 1) / XR;                  // loads of x that hold rows
-    auto x_inside = [&](int c) {                         // this lane's columns exist
-        return c * SC + (lane % XP) * (int)(16 / sizeof(raw)) < a.I;
-    };
-    // Past the last chunk, and for a lane behind the row's end, loads repeat
-    // valid data, which multiply() meets with zeros of x.  x goes first: how
-    // many of its loads there are varies, and the wait for a slot then also
-    // waits for as many of the next slot's first loads.
-    auto load = [&](int d, int c) {
-        const int k0 = min(c, chunks - 1) * SC;
-        const int kx = x_inside(c) ? k0 : 0;
-#pragma unroll
-        for (int i = 0; i < XL; i++)
-            if (i < nx) xr[d][i] = *reinterpret_cast<const u32x4 *>(xp[i] + kx);
+    // Past the last block, and for a lane behind the row's end, loads repeat
+    // valid data, which meets zeros of x.
+    auto load_w = [&](int c) {
+        const int k0 = min(c, blocks - 1) * (P * SC);
         const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? (k0 + lane_k) / 2 : k0 + lane_k),
                                 (uint32_t)rb - 16);
 #pragma unroll
         for (int i = 0; i < WL; i++)
-            wr[d][i] = ld_stream(reinterpret_cast<const u32x4 *>(wbase + (woff[i] + kb)));
-        const uint32_t gi = (uint32_t)min(k0 + (lane % NG) * FG, a.I - 1) / (uint32_t)gs;
+            wr[i] = ld_stream(reinterpret_cast<const u32x4 *>(wbase + (woff[i] + kb)));
+        const uint32_t gi = (uint32_t)min(k0 + (lane % NGB) * FG, a.I - 1) / (uint32_t)gs;
 #pragma unroll
-        for (int i = 0; i < SL; i++) sr[d][i] = sbase[soff[i] + gi];
+        for (int i = 0; i < SL; i++) sr[i] = sbase[soff[i] + gi];
+    };
+    auto x_inside = [&](int c, int q) {                  // this lane's columns exist
+        return (c * P + q) * SC + (lane % XP) * (int)(16 / sizeof(raw)) < a.I;
+    };
+    auto load_x = [&](int c) {
+#pragma unroll
+        for (int q = 0; q < P; q++) {
+            const int kx = x_inside(c, q) ? (c * P + q) * SC : 0;
+#pragma unroll
+            for (int i = 0; i < XL; i++)
+                if (i < nx) xr[q][i] = *reinterpret_cast<const u32x4 *>(xp[i] + kx);
+        }
+    };
+    // to LDS; only this wave uses this part, and its LDS operations complete in
+    // order
+    auto store_w = [&]() {
+#pragma unroll
+        for (int i = 0; i < WL; i++)
+            *reinterpret_cast<u32x4 *>(wl + ((lane + 64 * i) / WP) * WROW + (lane % WP) * 16) =
+                wr[i];
+#pragma unroll
+        for (int i = 0; i < SL; i++) sl[lane + 64 * i] = sr[i];
+    };
+    auto store_x = [&](int c, int q) {
+#pragma unroll
+        for (int i = 0; i < XL; i++) {
+            const u32x4 v = x_inside(c, q) ? xr[q][i] : u32x4{0, 0, 0, 0};
+            if (i < nx && lane / XP + XR * i < t.n)
+                *reinterpret_cast<u32x4 *>(xl + (lane / XP + XR * i) * XROW + (lane % XP) * 16) =
+                    v;
+        }
     };
 
     f32x4v acc[NB];
 #pragma unroll
     for (int n = 0; n < NB; n++) acc[n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto multiply = [&](int d, int c) {
-        // to LDS and back in fragment order; only this wave uses this part,
-        // and its LDS operations complete in order
-#pragma unroll
-        for (int i = 0; i < WL; i++) reinterpret_cast<u32x4 *>(wl)[lane + 64 * i] = wr[d][i];
-#pragma unroll
-        for (int i = 0; i < XL; i++) {
-            const u32x4 v = x_inside(c) ? xr[d][i] : u32x4{0, 0, 0, 0};
-            if (i < nx && lane / XP + XR * i < t.n)
-                *reinterpret_cast<u32x4 *>(xl + (lane / XP + XR * i) * XROW + (lane % XP) * 16) =
-                    v;
-        }
-        uint32_t wd[NB][WP];
+    auto multiply = [&](int q) {                         // chunk q of the block
+        uint32_t wd[NB][WC];
 #pragma unroll
         for (int n = 0; n < NB; n++) {
-            const char *row = wl + (n * 16 + li) * (WP * 16);
+            const char *row = wl + (n * 16 + li) * WROW + q * (WC * 16);
 #pragma unroll
-            for (int u = 0; u < WP / 4; u++) {
+            for (int u = 0; u < WC / 4; u++) {
                 const u32x4 v = *reinterpret_cast<const u32x4 *>(row + 64 * u + 16 * lg);
 #pragma unroll
                 for (int j = 0; j < 4; j++) wd[n][4 * u + j] = v[j];
@@ -336,6 +351,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
             }
 #pragma unroll
             for (int n = 0; n < NB; n++) {
+                const float sc = sl[(n * 16 + li) * NGB + q * NG + g];
                 f32x4v sum = z;
 #pragma unroll
                 for (int s = 0; s < TPG; s++) {
@@ -344,18 +360,14 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
                     if (FMT == FMT_I4G) {
                         wv = OFFSET ? nib8_bf16(wd[n][st]) : nib8_bf16_signed(wd[n][st]);
                     } else {
-                        const uint32_t p0 = wd[n][(2 * st) % WP];
-                        const uint32_t p1 = wd[n][(2 * st + 1) % WP];
+                        const uint32_t p0 = wd[n][(2 * st) % WC];
+                        const uint32_t p1 = wd[n][(2 * st + 1) % WC];
                         wv = join(cvt_lo<0>(p0), cvt_hi<0>(p0), cvt_lo<0>(p1), cvt_hi<0>(p1));
                     }
 #pragma unroll
                     for (int q = NP - 1; q >= 0; q--)    // small parts first
                         sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[s][q], wv, sum, 0, 0, 0);
                 }
-                const int from = (n * 16 * NG) % 64 + li * NG + g;
-                const float sc = __builtin_bit_cast(
-                    float, __builtin_amdgcn_ds_bpermute(
-                               from * 4, __builtin_bit_cast(int, sr[d][n * NG / 4])));
 #pragma unroll
                 for (int r = 0; r < 4; r++) acc[n][r] = fmaf(sc, sum[r], acc[n][r]);
             }
@@ -363,14 +375,19 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
         }
     };
 
+    load_x(wave);
+    load_w(wave);
+    for (int c = wave; c < blocks; c += SW) {
+        store_w();
+        store_x(c, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        load_w(c + SW);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int d = 0; d < D; d++) load(d, wave + d * SW);
-    for (int c = wave; c < chunks; c += D * SW) {
-#pragma unroll
-        for (int d = 0; d < D; d++) {
-            multiply(d, c + d * SW);
-            __builtin_amdgcn_sched_barrier(0);
-            load(d, c + (d + D) * SW);
+        for (int q = 0; q < P; q++) {
+            if (q > 0) store_x(c, q);
+            if (q == P - 1) load_x(c + SW);
+            multiply(q);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -404,9 +421,9 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
 template <int FMT, typename XT, int NB, bool GATED>
 void run_nb(const StreamArgs &p, unsigned grid, hipStream_t st)
 {
-    constexpr int D = 2;
+    constexpr int P = FMT == FMT_I4G || NB <= 2 ? 2 : 1;
 #define QG_RUN(FG)                                                                          \
-    hipLaunchKernelGGL((linear_stream<FMT, XT, NB, GATED, FG, D>), dim3(grid), dim3(SW * 64), 0, \
+    hipLaunchKernelGGL((linear_stream<FMT, XT, NB, GATED, FG, P>), dim3(grid), dim3(SW * 64), 0, \
                        st, p)
     if constexpr (FMT == FMT_FP8) {
         QG_RUN(128);
