@@ -226,7 +226,9 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStr
     if (stream) {
         bm = 16;
     } else if (fits) {
-        bm = rows > 64 && a.dtype == QGEMV_BF16 ? 128 : rows > 32 ? 64 : 32;
+        // the largest that the rows fill; grouped tiles skip what they lack
+        bm = a.dtype == QGEMV_BF16 ? 128 : 64;
+        if (!a.offsets && rows <= 64) bm = rows > 32 ? 64 : 32;
     }
     RowTile *tiles = nullptr;
     long long mt = (a.R + bm - 1) / bm;
