@@ -3,6 +3,7 @@
 //
 // Y = epilogue(X . W^T), W grouped int4 or fp8-e4m3 with block scales.
 #include "qg_device.h"
+#include "qg_launch.h"
 #include "qg_linear.h"
 
 namespace qg {
@@ -223,12 +224,18 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStr
     const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
     const bool stream = rows <= 16 && stream_fits(fmt, a);
     int bm = GM;
+    bool narrow = false;
     if (stream) {
         bm = 16;
     } else if (fits) {
         // the largest that the rows fill; grouped tiles skip what they lack
         bm = a.dtype == QGEMV_BF16 ? 128 : 64;
-        if (!a.offsets && rows <= 64) bm = rows > 32 ? 64 : 32;
+        const int wide = a.gated ? 128 : 256;            // columns of y of a tile
+        const long long t = (long long)(a.offsets ? (a.R + bm - 1) / bm + a.E / 2
+                                                  : (a.R + bm - 1) / bm) *
+                            ((oc + wide - 1) / wide);
+        narrow = 2 * t <= cu_count();
+        if (narrow) bm = rows > 32 && a.dtype == QGEMV_BF16 ? 64 : 32;
     }
     RowTile *tiles = nullptr;
     long long mt = (a.R + bm - 1) / bm;
@@ -242,7 +249,7 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStr
         ws = static_cast<char *>(ws) + align256((size_t)max_tiles(a.R, a.E, 16) * sizeof(RowTile));
     }
     if (stream) return launch_stream(fmt, a, tiles, (int)mt, st);
-    if (fits) return launch_tile(fmt, a, bm, tiles, (int)mt, ws, st);
+    if (fits) return launch_tile(fmt, a, narrow, bm, tiles, (int)mt, ws, st);
     const long long grid = mt * ((oc + GN - 1) / GN);
     if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     if (fmt == FMT_I4G) {

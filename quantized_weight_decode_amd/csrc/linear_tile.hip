@@ -129,6 +129,27 @@ __device__ __forceinline__ void wait_loads()
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "i"(N) : "memory");
 }
 
+// A lane's two fragments (h = 0, 1) of one weight row and K step from the
+// row's bytes in LDS.
+template <int FMT, int FG>
+__device__ __forceinline__ void unpack(const char *row, int lg, f16x8 out[2])
+{
+    if constexpr (FMT == FMT_FP8) {
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(row + lg * 16);
+        out[0] = fp8x8_f16(v.x, v.y);
+        out[1] = fp8x8_f16(v.z, v.w);
+    } else if constexpr (FG == 64) {
+        const u32x2 v = *reinterpret_cast<const u32x2 *>(row + lg * 8);
+        out[0] = nib8_f16(v.x);
+        out[1] = nib8_f16(v.y);
+    } else {
+        out[0] = nib8_f16(*reinterpret_cast<const uint32_t *>(row + lg * 4));
+        out[1] = nib8_f16(*reinterpret_cast<const uint32_t *>(row + 16 + lg * 4));
+    }
+}
+
+constexpr int BAD_ROW = -0x7FFFFFFF;     // exponent of a row of y without a row of x
+
 constexpr int TK = 64;          // columns per K step
 constexpr int TN = 256;         // rows of W per workgroup tile
 
@@ -151,6 +172,78 @@ struct TileArgs {
     const RowTile *tiles;
     int Ip, ntm, ntn;
 };
+
+// One K step of a wave: 16 MF rows of x (packed in LDS at sm, NP planes of 8
+// MF rows x 128 bytes) times its unpacked weights, added to acc.
+//
+// Steps of two 16 x 16 blocks (n, n + 1) of one row block m and scale group j:
+// a step's sums are added to the totals while the next step's matrix
+// instructions run.  The scheduling barrier keeps the compiler from running
+// ahead and holding many steps' values.  RAGGED: only mf row blocks.
+template <int NP, int MF, int NB, int FG, bool RAGGED>
+__device__ __forceinline__ void multiply_step(f32x4v (&acc)[MF][NB], const f16x8 (&bv)[NB][2],
+                                              const float (&sc)[NB][TK / FG], const char *sm,
+                                              int lane, int mf)
+{
+    constexpr int NS = TK / FG, NH = NB / 2, SPM = NH * NS;   // steps of a row block
+    constexpr int CH = MF * 16 * 8;
+    const int li = lane & 15, lg = lane >> 4;
+    const f16x8 *const xs = reinterpret_cast<const f16x8 *>(sm);
+    f16x8 am[2][NP][2];
+    f32x4v g[2][2];
+    auto read_a = [&](int m) {
+#pragma unroll
+        for (int q = 0; q < NP; q++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int ch = FG == 64 ? 2 * lg + h : 4 * h + lg;
+                am[m & 1][q][h] = xs[q * CH + (m * 16 + li) * 8 + (ch ^ swizzle(li))];
+            }
+    };
+    auto flush = [&](int s) {
+        const int m = s / SPM, j = (s / NH) % NS, n = (s % NH) * 2;
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                acc[m][n + i][r] = fmaf(sc[n + i][j], g[s & 1][i][r], acc[m][n + i][r]);
+        // (not to be moved past the branches below)
+        asm volatile("" : "+v"(acc[m][n]), "+v"(acc[m][n + 1]));
+    };
+    read_a(0);
+#pragma unroll
+    for (int m = 0; m < MF; m++) {
+        if (!RAGGED || m < mf) {                         // uniform over the workgroup
+            if (m + 1 < MF) read_a(m + 1);
+#pragma unroll
+            for (int s = m * SPM; s < (m + 1) * SPM; s++) {
+                const int j = (s / NH) % NS, n = (s % NH) * 2;
+                f32x4v t0 = {0.0f, 0.0f, 0.0f, 0.0f}, t1 = t0;
+#pragma unroll
+                for (int h = j * (2 / NS); h < (j + 1) * (2 / NS); h++)
+#pragma unroll
+                    for (int q = NP - 1; q >= 0; q--) {  // small parts first
+                        t0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(am[m & 1][q][h], bv[n][h], t0,
+                                                                    0, 0, 0);
+                        t1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(am[m & 1][q][h],
+                                                                    bv[n + 1][h], t1, 0, 0, 0);
+                    }
+                g[s & 1][0] = t0;
+                g[s & 1][1] = t1;
+                if (s > 0) flush(s - 1);
+#pragma unroll
+                for (int i = 0; i < 4 * NP / NS; i++) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 2 * NS, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else if (m == mf) {                            // the tile's last sums
+            flush(m * SPM - 1);
+        }
+    }
+    if (!RAGGED || mf == MF) flush(MF * SPM - 1);
+}
 
 // Tile kernel.  A workgroup of 4 waves makes 16 MF rows of y x 256 rows of W;
 // each wave all 16 MF rows x 64 rows of W, so a weight is unpacked once per
@@ -208,7 +301,6 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     }
 
     // row exponents; a bad row index is marked and reads row 0
-    constexpr int BAD_ROW = -0x7FFFFFFF;
     if (tid < BM) {
         int e = 0;
         if (tid < t.n) {
@@ -320,86 +412,15 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
         const char *const sm = smem + stage * STAGE;
         const char *const wl = sm + WO + wave * (64 * WB);
         const float *const sl = reinterpret_cast<const float *>(sm + SO) + wave * (64 * NS);
-        const f16x8 (*const xs)[CH] = reinterpret_cast<const f16x8 (*)[CH]>(sm);
         f16x8 bv[4][2];
         float sc[4][NS];
 #pragma unroll
         for (int n = 0; n < 4; n++) {
-            const char *wr = wl + (n * 16 + li) * WB;
-            if constexpr (FMT == FMT_FP8) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(wr + lg * 16);
-                bv[n][0] = fp8x8_f16(v.x, v.y);
-                bv[n][1] = fp8x8_f16(v.z, v.w);
-            } else if constexpr (FG == 64) {
-                const u32x2 v = *reinterpret_cast<const u32x2 *>(wr + lg * 8);
-                bv[n][0] = nib8_f16(v.x);
-                bv[n][1] = nib8_f16(v.y);
-            } else {
-                bv[n][0] = nib8_f16(*reinterpret_cast<const uint32_t *>(wr + lg * 4));
-                bv[n][1] = nib8_f16(*reinterpret_cast<const uint32_t *>(wr + 16 + lg * 4));
-            }
+            unpack<FMT, FG>(wl + (n * 16 + li) * WB, lg, bv[n]);
 #pragma unroll
             for (int j = 0; j < NS; j++) sc[n][j] = sl[(n * 16 + li) * NS + j];
         }
-        // Steps of two 16 x 16 blocks (n, n + 1) of one row block m and scale
-        // group j: a step's sums are added to the totals while the next
-        // step's matrix instructions run.  The scheduling barrier keeps the
-        // compiler from running ahead and holding many steps' values.
-        f16x8 am[2][NP][2];
-        f32x4v g[2][2];
-        auto read_a = [&](int m) {
-#pragma unroll
-            for (int q = 0; q < NP; q++)
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const int ch = FG == 64 ? 2 * lg + h : 4 * h + lg;
-                    am[m & 1][q][h] = xs[q][(m * 16 + li) * 8 + (ch ^ swizzle(li))];
-                }
-        };
-        auto flush = [&](int s) {
-            const int m = s / (2 * NS), j = (s / 2) % NS, n = (s & 1) * 2;
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-#pragma unroll
-                for (int r = 0; r < 4; r++)
-                    acc[m][n + i][r] = fmaf(sc[n + i][j], g[s & 1][i][r], acc[m][n + i][r]);
-            // (not to be moved past the branches below)
-            asm volatile("" : "+v"(acc[m][n]), "+v"(acc[m][n + 1]));
-        };
-        read_a(0);
-        constexpr int SPM = 2 * NS;                      // steps of a row block
-#pragma unroll
-        for (int m = 0; m < MF; m++) {
-            if (!RAGGED || m < mf) {                     // uniform over the workgroup
-                if (m + 1 < MF) read_a(m + 1);
-#pragma unroll
-                for (int s = m * SPM; s < (m + 1) * SPM; s++) {
-                    const int j = (s / 2) % NS, n = (s & 1) * 2;
-                    f32x4v t0 = {0.0f, 0.0f, 0.0f, 0.0f}, t1 = t0;
-#pragma unroll
-                    for (int h = j * (2 / NS); h < (j + 1) * (2 / NS); h++)
-#pragma unroll
-                        for (int q = NP - 1; q >= 0; q--) {  // small parts first
-                            t0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(am[m & 1][q][h],
-                                                                        bv[n][h], t0, 0, 0, 0);
-                            t1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(am[m & 1][q][h],
-                                                                        bv[n + 1][h], t1, 0, 0, 0);
-                        }
-                    g[s & 1][0] = t0;
-                    g[s & 1][1] = t1;
-                    if (s > 0) flush(s - 1);
-#pragma unroll
-                    for (int i = 0; i < 4 * NP / NS; i++) {
-                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, 2 * NS, 0);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            } else if (m == mf) {                        // the tile's last sums
-                flush(m * SPM - 1);
-            }
-        }
-        if (!RAGGED || mf == MF) flush(MF * SPM - 1);
+        multiply_step<NP, MF, 4, FG, RAGGED>(acc, bv, sc, sm, lane, mf);
         stage = stage == ST - 1 ? 0 : stage + 1;
     }
     // loads past the last step still write LDS
@@ -436,6 +457,164 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     }
 }
 
+// All but this wave's last n loads have arrived.
+template <int N>
+__device__ __forceinline__ void wait_own_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" :: "i"(N) : "memory");
+}
+
+// Narrow kernel: the tile kernel's arithmetic for products too small to fill
+// the GPU with its tiles.  A workgroup makes up to 16 MB rows of y x 16 NB
+// rows of W; its KW waves take the K steps in turn, each with stages of LDS of
+// its own, so the K loop needs no barrier, and their sums are joined through
+// LDS in a fixed order.  At 64 x 6144 x 12288 bf16 the tile kernel has 48
+// workgroups for 256 CUs and takes 89 us.
+template <int FMT, typename XT, int NP, int MB, int NB, bool GATED, int FG, bool RAGGED, int KW,
+          int ST>
+__global__ __launch_bounds__(KW * 64, KW / 4) void linear_narrow(TileArgs p)
+{
+    constexpr int NS = TK / FG;
+    constexpr int WB = FMT == FMT_FP8 ? 64 : 32;         // bytes of a row and step
+    constexpr int WD = WB / 16;                          // 16-byte pieces of it
+    constexpr int WL = NB * 16 * WD / 64;                // loads per lane and step
+    constexpr int AL = MB * 2;                           // per plane
+    constexpr int SL = (NB * 16 * NS + 63) / 64;
+    constexpr int CH = MB * 16 * 8;                      // 16-byte chunks of a plane
+    constexpr uint32_t WO = NP * CH * 16, SO = WO + WL * 1024, STAGE = SO + SL * 256;
+    constexpr int LDR = NB * 16 + 4;
+    constexpr uint32_t RED = KW * MB * 16 * LDR * 4;
+    __shared__ __align__(16) char smem[KW * ST * STAGE > RED ? KW * ST * STAGE : RED];
+    const LinearArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, lg = lane >> 4;
+    const int oc = GATED ? a.O / 2 : a.O;
+    constexpr int YC = GATED ? NB * 8 : NB * 16;         // columns of y
+    const int nt = (int)(blockIdx.x % p.ntn), mt = (int)(blockIdx.x / p.ntn);
+    RowTile t;
+    if (p.tiles) t = p.tiles[mt];
+    else t = RowTile{0, mt * (16 * MB), min(16 * MB, a.R - mt * (16 * MB)), 0};
+    t.n = __builtin_amdgcn_readfirstlane(t.n);
+    t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+    if (t.n <= 0) return;                                // uniform over the workgroup
+
+    uint32_t aoff[AL];                                   // lane: row c / 8, chunk c % 8
+#pragma unroll
+    for (int i = 0; i < AL; i++) {
+        const int c = lane + 64 * i;
+        const int row = c >> 3;
+        int r = t.row0 + (row < t.n ? row : 0);
+        if (a.rows) {
+            r = a.rows[r];
+            r = r < 0 || r >= a.T ? 0 : r;
+        }
+        aoff[i] = ((uint32_t)r * (uint32_t)p.Ip + ((c & 7) ^ swizzle(row & 15)) * 8) * 2;
+    }
+    const size_t rb = FMT == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
+    const uint8_t *const wbase = a.w + (size_t)t.expert * a.w_stride;
+    const float *const sbase = a.scales + (size_t)t.expert * a.s_stride;
+    auto weight_row = [&](int i) {
+        const int n = i >> 4;
+        const int half = GATED ? n / (NB / 2) : 0;
+        const int c = nt * YC + (GATED ? n % (NB / 2) : n) * 16 + (i & 15);
+        return (c < oc ? c : oc - 1) + half * oc;
+    };
+    uint32_t woff[WL], soff[SL];
+#pragma unroll
+    for (int i = 0; i < WL; i++) woff[i] = (uint32_t)(weight_row((lane + 64 * i) / WD) * rb);
+#pragma unroll
+    for (int i = 0; i < SL; i++) {
+        const int row = weight_row(min((lane + 64 * i) / NS, NB * 16 - 1));
+        soff[i] = (uint32_t)(FMT == FMT_I4G ? row : row >> 7) * (uint32_t)a.ng;
+    }
+    const uint32_t lane_b = (lane % WD) * 16;
+    const int mf = __builtin_amdgcn_readfirstlane((t.n + 15) / 16);
+    const uint32_t gs = FMT == FMT_FP8 ? 128 : a.gs;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem) +
+        wave * (ST * STAGE);
+    const char *const own = smem + wave * (ST * STAGE);
+    const int steps = p.Ip / TK;
+
+    // as the tile kernel's; a step past the last repeats it
+    constexpr int LOADS = NP * AL + WL + SL;
+    auto load = [&](int s, int stage) {
+        const int k0 = min(s, steps - 1) * TK;
+        const uint32_t at = lds0 + stage * STAGE;
+#pragma unroll
+        for (int q = 0; q < NP; q++)
+#pragma unroll
+            for (int i = 0; i < AL; i++)
+                load_lds16((q ? p.lo : p.hi) + k0, aoff[i], at + q * (CH * 16) + 1024 * i);
+        const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? k0 / 2 : k0) + lane_b,
+                                (uint32_t)rb - 16);
+#pragma unroll
+        for (int i = 0; i < WL; i++) load_lds16(wbase, woff[i] + kb, at + WO + 1024 * i);
+        const uint32_t gi = (uint32_t)min(k0 + (lane % NS) * FG, a.I - 1) / gs;
+#pragma unroll
+        for (int i = 0; i < SL; i++) load_lds4(sbase, (soff[i] + gi) * 4, at + SO + 256 * i);
+    };
+
+    f32x4v acc[MB][NB];
+#pragma unroll
+    for (int m = 0; m < MB; m++)
+#pragma unroll
+        for (int n = 0; n < NB; n++) acc[m][n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+
+    __builtin_amdgcn_s_waitcnt(QG_WAIT_VM0);             // earlier loads are done
+#pragma unroll
+    for (int i = 0; i < ST - 1; i++) load(wave + i * KW, i);
+    int stage = 0;
+    for (int s = wave; s < steps; s += KW) {
+        wait_own_loads<(ST - 2) * LOADS>();
+        load(s + (ST - 1) * KW, stage == 0 ? ST - 1 : stage - 1);
+        const char *const sm = own + stage * STAGE;
+        const float *const sl = reinterpret_cast<const float *>(sm + SO);
+        f16x8 bv[NB][2];
+        float sc[NB][NS];
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            unpack<FMT, FG>(sm + WO + (n * 16 + li) * WB, lg, bv[n]);
+#pragma unroll
+            for (int j = 0; j < NS; j++) sc[n][j] = sl[(n * 16 + li) * NS + j];
+        }
+        multiply_step<NP, MB, NB, FG, RAGGED>(acc, bv, sc, sm, lane, mf);
+        stage = stage == ST - 1 ? 0 : stage + 1;
+    }
+    wait_own_loads<0>();                                 // loads past the last step
+    __syncthreads();
+
+    float (*const red)[MB * 16][LDR] = reinterpret_cast<float (*)[MB * 16][LDR]>(smem);
+#pragma unroll
+    for (int m = 0; m < MB; m++)
+#pragma unroll
+        for (int n = 0; n < NB; n++)
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                red[wave][m * 16 + 4 * lg + r][n * 16 + li] = acc[m][n][r];
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < t.n * YC; i += KW * 64) {
+        const int r = i / YC, c = i % YC;
+        const int col = nt * YC + c;
+        if (col >= oc) continue;
+        int xr = t.row0 + r;
+        if (a.rows) xr = a.rows[xr];
+        const int e = xr < 0 || xr >= a.T ? BAD_ROW : p.rexp[xr];
+        float v = 0.0f, up = 0.0f;
+#pragma unroll
+        for (int w = 0; w < KW; w++) {
+            v += red[w][r][c];
+            if (GATED) up += red[w][r][c + YC];
+        }
+        v = ldexpf(v, e);
+        up = ldexpf(up, e);
+        if (e == BAD_ROW) v = up = __builtin_nanf("");
+        finish<XT>(a, t.expert, t.row0 + r, col, v, up);
+    }
+}
+
 #define QG_RUN1(FG, G, R)                                                                   \
     hipLaunchKernelGGL((linear_tile<FMT, XT, NP, MF, G, FG, R>), dim3(grid), dim3(256), 0, st, p)
 #define QG_RUN(FG)                                                                          \
@@ -465,6 +644,38 @@ hipError_t run_tile(const TileArgs &p, unsigned grid, hipStream_t st)
     }
     return hipGetLastError();
 }
+template <int FMT, typename XT, int MB, int NB>
+hipError_t run_narrow(const TileArgs &p, unsigned grid, hipStream_t st)
+{
+    // 8 waves where their stages fit the 160 KB of LDS, else 4
+    constexpr int NP = sizeof(typename XT::raw) == 4 ? 2 : 1;
+    constexpr int KW = FMT == FMT_I4G && NP * MB <= 2 ? 8 : 4, ST = 3;
+#define QG_RUN2(FG, G, R)                                                                   \
+    hipLaunchKernelGGL((linear_narrow<FMT, XT, NP, MB, NB, G, FG, R, KW, ST>), dim3(grid),  \
+                       dim3(KW * 64), 0, st, p)
+#define QG_RUN3(FG)                                                                         \
+    do {                                                                                    \
+        if constexpr (FMT == FMT_I4G) {                  /* grouped: int4 */                \
+            if (p.tiles) {                                                                  \
+                if (p.a.gated) QG_RUN2(FG, true, true);                                     \
+                else QG_RUN2(FG, false, true);                                              \
+                break;                                                                      \
+            }                                                                               \
+        }                                                                                   \
+        if (p.a.gated) QG_RUN2(FG, true, false);                                            \
+        else QG_RUN2(FG, false, false);                                                     \
+    } while (0)
+    if constexpr (FMT == FMT_FP8) {
+        QG_RUN3(64);
+    } else {
+        if (p.a.gs % 64 == 0) QG_RUN3(64);
+        else QG_RUN3(32);
+    }
+#undef QG_RUN2
+#undef QG_RUN3
+    return hipGetLastError();
+}
+
 int padded(int I) { return (I + TK - 1) / TK * TK; }
 
 }  // namespace
@@ -483,8 +694,8 @@ bool tile_fits(WeightFormat fmt, const LinearArgs &a)
            (size_t)a.ng * a.O * 4 < (1ull << 32) && (size_t)a.T * padded(a.I) * 2 < (1ull << 32);
 }
 
-hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, int bm, const RowTile *tiles,
-                       int ntm, void *ws, hipStream_t st)
+hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int bm,
+                       const RowTile *tiles, int ntm, void *ws, hipStream_t st)
 {
     TileArgs p{};
     p.a = a;
@@ -500,7 +711,8 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, int bm, const RowT
     p.rexp = rexp;
     p.tiles = tiles;
     p.ntm = ntm;
-    const int cols = a.gated ? TN / 2 : TN, oc = a.gated ? a.O / 2 : a.O;
+    const int tn = narrow ? 64 : TN;
+    const int cols = a.gated ? tn / 2 : tn, oc = a.gated ? a.O / 2 : a.O;
     p.ntn = (oc + cols - 1) / cols;
     const long long grid = (long long)ntm * p.ntn;
     if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
@@ -523,6 +735,14 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, int bm, const RowT
                                   : run_tile<FMT_I4G, F32, MF>(p, (unsigned)grid, st))      \
          : (a.dtype == QGEMV_BF16 ? run_tile<FMT_FP8, BF16, MF>(p, (unsigned)grid, st)      \
                                   : run_tile<FMT_FP8, F32, MF>(p, (unsigned)grid, st)))
+#define QG_NARROW(XT, MB)                                                                   \
+    (fmt == FMT_I4G ? run_narrow<FMT_I4G, XT, MB, 4>(p, (unsigned)grid, st)                  \
+                    : run_narrow<FMT_FP8, XT, MB, 4>(p, (unsigned)grid, st))
+    if (narrow) {
+        if (a.dtype != QGEMV_BF16) return QG_NARROW(F32, 2);
+        return bm == 64 ? QG_NARROW(BF16, 4) : QG_NARROW(BF16, 2);
+    }
+#undef QG_NARROW
     switch (bm) {
     case 128:                                            // bf16 only
         return fmt == FMT_I4G ? run_tile<FMT_I4G, BF16, 8>(p, (unsigned)grid, st)
