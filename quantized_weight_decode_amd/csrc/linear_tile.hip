@@ -22,50 +22,142 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 // where lo is subnormal), the size of f32's own rounding of a product.
 // The exponent E - 15 is undone on the f32 sum.  int4 weights unpack in the
 // column order 0 4 1 5 2 6 3 7 of each eight; x is stored in that order.
-// Rows are padded with zeros to whole K steps.  Bound by HBM: x read once, 2
-// or 4 bytes per element written.
+// Rows are padded with zeros to whole K steps.
+//
+// One workgroup of TH threads per row, the row in registers between the
+// maximum and the scaling (NCH pieces of eight per thread; NCH = 0: rows too
+// long for that are read twice), VEC: rows on 16 bytes.  Bound by HBM for many
+// rows (x read once, 2 or 4 bytes per element written), by latency for few.
 // ---------------------------------------------------------------------------
-template <typename XT, int FMT>
-__global__ __launch_bounds__(256) void pack_rows(const typename XT::raw *__restrict__ x,
-                                                 long long ldx, int I, int Ip,
-                                                 _Float16 *__restrict__ hi,
-                                                 _Float16 *__restrict__ lo,
-                                                 int *__restrict__ rexp)
+template <typename XT>
+__device__ __forceinline__ void load8(const typename XT::raw *src, bool vec, float v[8])
 {
-    __shared__ uint32_t wmax[4];
+    typedef typename XT::raw raw;
+    if (vec) {
+        typedef raw rawx8 __attribute__((ext_vector_type(8)));
+        const rawx8 t = *reinterpret_cast<const rawx8 *>(src);
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = XT::get(t[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = XT::get(src[j]);
+    }
+}
+
+// largest finite |v| by its bits
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, const float v[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu;
+        m = b < 0x7F800000u && b > m ? b : m;
+    }
+    return m;
+}
+
+template <int FMT>
+__device__ __forceinline__ void store8(const float v[8], int shift, _Float16 *hi, _Float16 *lo)
+{
+    f16x8 h, l;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const float t = ldexpf(v[FMT == FMT_I4G ? (j >> 1) + 4 * (j & 1) : j], shift);
+        h[j] = (_Float16)t;
+        l[j] = (_Float16)(t - (float)h[j]);
+    }
+    *reinterpret_cast<f16x8 *>(hi) = h;
+    if (lo) *reinterpret_cast<f16x8 *>(lo) = l;
+}
+
+template <typename XT, int FMT, int TH, int NCH, bool VEC>
+__global__ __launch_bounds__(TH) void pack_rows(const typename XT::raw *__restrict__ x,
+                                                long long ldx, int I, int Ip,
+                                                _Float16 *__restrict__ hi,
+                                                _Float16 *__restrict__ lo,
+                                                int *__restrict__ rexp)
+{
+    __shared__ uint32_t wmax[TH / 64];
     const int tid = threadIdx.x;
     const long long t = blockIdx.x;
     const typename XT::raw *src = x + (size_t)t * ldx;
-    // largest finite |x| by its bits
+    hi += (size_t)t * Ip;
+    if (lo) lo += (size_t)t * Ip;
+    float v[NCH ? NCH : 1][8];
     uint32_t m = 0;
-    for (int c = tid; c < I; c += 256) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, XT::get(src[c])) & 0x7FFFFFFFu;
-        m = b < 0x7F800000u && b > m ? b : m;
+    if (NCH) {
+#pragma unroll
+        for (int i = 0; i < NCH; i++) {
+            const int c = (tid + TH * i) * 8;            // I is a multiple of 32
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[i][j] = 0.0f;
+            if (c < I) load8<XT>(src + c, VEC, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NCH; i++) m = max_bits(m, v[i]);
+    } else {
+        for (int c = tid * 8; c < I; c += TH * 8) {
+            load8<XT>(src + c, VEC, v[0]);
+            m = max_bits(m, v[0]);
+        }
     }
 #pragma unroll
     for (int d = 32; d > 0; d /= 2) {
         const uint32_t o = (uint32_t)__shfl_xor((int)m, d);
         m = o > m ? o : m;
     }
-    if ((tid & 63) == 0) wmax[tid >> 6] = m;
-    __syncthreads();
-    m = 0;
-    for (int i = 0; i < 4; i++) m = wmax[i] > m ? wmax[i] : m;
+    if (TH > 64) {
+        if ((tid & 63) == 0) wmax[tid >> 6] = m;
+        __syncthreads();
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < TH / 64; i++) m = wmax[i] > m ? wmax[i] : m;
+    }
     int E = 0;
     if (m) frexpf(__builtin_bit_cast(float, m), &E);
     if (tid == 0) rexp[t] = E - 15;
-    for (int c = tid * 8; c < Ip; c += 256 * 8) {
-        f16x8 h, l;
+    if (NCH) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const int from = FMT == FMT_I4G ? (j >> 1) + 4 * (j & 1) : j;
-            const float v = c + from < I ? ldexpf(XT::get(src[c + from]), 15 - E) : 0.0f;
-            h[j] = (_Float16)v;
-            if (lo) l[j] = (_Float16)(v - (float)h[j]);
+        for (int i = 0; i < NCH; i++) {
+            const int c = (tid + TH * i) * 8;
+            if (c < Ip) store8<FMT>(v[i], 15 - E, hi + c, lo ? lo + c : nullptr);
         }
-        *reinterpret_cast<f16x8 *>(hi + (size_t)t * Ip + c) = h;
-        if (lo) *reinterpret_cast<f16x8 *>(lo + (size_t)t * Ip + c) = l;
+    } else {
+        for (int c = tid * 8; c < Ip; c += TH * 8) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[0][j] = 0.0f;
+            if (c < I) load8<XT>(src + c, VEC, v[0]);
+            store8<FMT>(v[0], 15 - E, hi + c, lo ? lo + c : nullptr);
+        }
     }
+}
+
+template <typename XT, int FMT, bool VEC>
+void run_pack(const LinearArgs &a, int Ip, _Float16 *hi, _Float16 *lo, int *rexp, hipStream_t st)
+{
+#define QG_PACK(TH, NCH)                                                                    \
+    hipLaunchKernelGGL((pack_rows<XT, FMT, TH, NCH, VEC>), dim3(a.T), dim3(TH), 0, st,      \
+                       static_cast<const typename XT::raw *>(a.x), a.ldx, a.I, Ip, hi, lo, rexp)
+    if (Ip <= 2048) QG_PACK(64, 4);
+    else if (Ip <= 8192) QG_PACK(256, 4);
+    else if (Ip <= 16384) QG_PACK(256, 8);
+    else QG_PACK(256, 0);
+#undef QG_PACK
+}
+
+template <typename XT>
+hipError_t pack(WeightFormat fmt, const LinearArgs &a, int Ip, _Float16 *hi, _Float16 *lo,
+                int *rexp, hipStream_t st)
+{
+    const bool vec =
+        (((uintptr_t)a.x | (uintptr_t)(a.ldx * sizeof(typename XT::raw))) & 15) == 0;
+    if (fmt == FMT_I4G) {
+        if (vec) run_pack<XT, FMT_I4G, true>(a, Ip, hi, lo, rexp, st);
+        else run_pack<XT, FMT_I4G, false>(a, Ip, hi, lo, rexp, st);
+    } else {
+        if (vec) run_pack<XT, FMT_FP8, true>(a, Ip, hi, lo, rexp, st);
+        else run_pack<XT, FMT_FP8, false>(a, Ip, hi, lo, rexp, st);
+    }
+    return hipGetLastError();
 }
 
 // (w & mask) | bits in one instruction: it takes one scalar operand and no
@@ -716,18 +808,8 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int b
     p.ntn = (oc + cols - 1) / cols;
     const long long grid = (long long)ntm * p.ntn;
     if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-#define QG_PACK(XT, F)                                                                      \
-    hipLaunchKernelGGL((pack_rows<XT, F>), dim3(a.T), dim3(256), 0, st,                     \
-                       static_cast<const XT::raw *>(a.x), a.ldx, a.I, p.Ip, hi, lo, rexp)
-    if (fmt == FMT_I4G) {
-        if (a.dtype == QGEMV_BF16) QG_PACK(BF16, FMT_I4G);
-        else QG_PACK(F32, FMT_I4G);
-    } else {
-        if (a.dtype == QGEMV_BF16) QG_PACK(BF16, FMT_FP8);
-        else QG_PACK(F32, FMT_FP8);
-    }
-#undef QG_PACK
-    hipError_t e = hipGetLastError();
+    const hipError_t e = a.dtype == QGEMV_BF16 ? pack<BF16>(fmt, a, p.Ip, hi, lo, rexp, st)
+                                               : pack<F32>(fmt, a, p.Ip, hi, lo, rexp, st);
     if (e != hipSuccess) return e;
 #define QG_TILE(MF)                                                                         \
     (fmt == FMT_I4G                                                                         \
