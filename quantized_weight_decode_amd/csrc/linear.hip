@@ -198,6 +198,51 @@ long long max_tiles(int R, int E, int bm)
     return (long long)R / bm + (E < R ? E : R);
 }
 
+// Tile of a product: the one whose busiest CU has the least to do, estimated
+// as workgroups per CU times the cost of one.  Costs of a workgroup relative
+// to 128 x 256, from bf16 int4 at 6144 columns (125 us with one 128 x 256
+// tile per CU, 200 with two, 323 with three); f32 counts two planes.  What the
+// rule decides, us with the tile chosen and with the next best: 256 x 12288:
+// 64 x 256 89, narrow 93, 128 x 256 125; 512 x 12288: 128 x 256 126, 64 x 256
+// 139; 512 x 4096 (4096 columns): narrow 49, 32 x 256 53, 128 x 256 95; f32
+// 333 x 11008 (4096 columns): 32 x 256 97, 64 x 256 117.  Grouped tiles know
+// neither their count (estimated with half a tile per expert) nor their
+// filling, and skip what they lack: only the largest of each kind.
+void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
+{
+    struct Kind {
+        int bm;
+        bool narrow, grouped;
+        double cost;
+    };
+    static const Kind bf16[] = {{128, false, true, 1.0},
+                                {64, false, false, 0.66},
+                                {32, false, false, 0.58},
+                                {64, true, true, 0.265},
+                                {32, true, false, 0.185}};
+    static const Kind f32[] = {{64, false, true, 0.93}, {32, false, false, 0.69},
+                               {32, true, true, 0.26}};
+    const bool half = a.dtype == QGEMV_BF16;
+    const Kind *kinds = half ? bf16 : f32;
+    const int n = half ? 5 : 3;
+    const long long ncu = cu_count();
+    double best = -1.0;
+    for (int i = 0; i < n; i++) {
+        const Kind &k = kinds[i];
+        if (a.offsets && !k.grouped) continue;
+        const int cols = (k.narrow ? 64 : 256) / (a.gated ? 2 : 1);
+        const long long mt = (a.R + k.bm - 1) / k.bm +
+                             (a.offsets ? (a.E < a.R ? a.E : a.R) / 2 : 0);
+        const long long wgs = mt * ((oc + cols - 1) / cols);
+        const double c = (double)((wgs + ncu - 1) / ncu) * k.cost;
+        if (best < 0.0 || c < best) {                    // ties: the larger tile
+            best = c;
+            bm = k.bm;
+            narrow = k.narrow;
+        }
+    }
+}
+
 template <int FMT, typename XT>
 void run_general(const LinearArgs &a, const RowTile *tiles, unsigned grid, hipStream_t st)
 {
@@ -228,14 +273,7 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStr
     if (stream) {
         bm = 16;
     } else if (fits) {
-        // the largest that the rows fill; grouped tiles skip what they lack
-        bm = a.dtype == QGEMV_BF16 ? 128 : 64;
-        const int wide = a.gated ? 128 : 256;            // columns of y of a tile
-        const long long t = (long long)(a.offsets ? (a.R + bm - 1) / bm + a.E / 2
-                                                  : (a.R + bm - 1) / bm) *
-                            ((oc + wide - 1) / wide);
-        narrow = 2 * t <= cu_count();
-        if (narrow) bm = rows > 32 && a.dtype == QGEMV_BF16 ? 64 : 32;
+        pick_tile(a, oc, bm, narrow);
     }
     RowTile *tiles = nullptr;
     long long mt = (a.R + bm - 1) / bm;
