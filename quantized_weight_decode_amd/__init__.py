@@ -15,6 +15,7 @@ Two layers:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -542,6 +543,20 @@ def moe_topk_error(workspace):
 # x, residual, h and a caller's out may be row-strided views (columns
 # contiguous); everything else is contiguous.  The launch goes to the device
 # of the tensors, on its current stream.
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes `device` current for a launch (nothing to do where it is)."""
+    cuda = _torch().cuda
+    return _NO_GUARD if device.index == cuda.current_device() else cuda.device(device)
+
+
+def _raw_stream(device):
+    """The device's current stream handle, without building a Stream object."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
 def _dtype_code(t, name):
     torch = _torch()
     if isinstance(t, torch.Tensor):
@@ -626,10 +641,10 @@ def _linear(fn, w, scales, x, gs, bias, act, gated, residual, workspace, out):
     y = out if out is not None else torch.empty((S, oc), dtype=x.dtype, device=x.device)
     yp, ldy = _rows(y, "out", x.dtype, (S, oc))
     wp, sp = _dev(w, "w", torch.uint8), _dev(scales, "scales", torch.float32)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         ws, wsp = _scratch(workspace, qgemv_linear_workspace(S, I, O, code), x.device)
         args = (wp, sp, xp, ldx, yp, ldy, S, I, O) + ((gs,) if gs is not None else ())
-        _call(fn, *args, code, _ref(epi), wsp, ws.numel(), _stream())
+        _call(fn, *args, code, _ref(epi), wsp, ws.numel(), _raw_stream(x.device))
     return y[0] if one else y
 
 
@@ -673,10 +688,10 @@ def moe_group(ids, E, workspace=None):
     offsets = torch.empty(min(max(int(E), 0), 1024) + 1, dtype=torch.int32, device=ids.device)
     tokens = torch.empty(T * K, dtype=torch.int32, device=ids.device)
     pos = torch.empty((T, K), dtype=torch.int32, device=ids.device)
-    with torch.cuda.device(ids.device):
+    with _on(ids.device):
         ws, wsp = _scratch(workspace, qgemv_moe_group_workspace(T, K, E), ids.device)
         _call("qgemv_moe_group", ip, T, K, E, _dev(offsets, "offsets"), _dev(tokens, "tokens"),
-              _dev(pos, "pos"), wsp, ws.numel(), _stream())
+              _dev(pos, "pos"), wsp, ws.numel(), _raw_stream(ids.device))
     return offsets, tokens, pos
 
 
@@ -716,10 +731,11 @@ def i4g_grouped(w, scales, x, offsets, gs, rows=None, bias=None, act=None, gated
     wp, sp = _dev(w, "w", torch.uint8), _dev(scales, "scales", torch.float32)
     op = _dev(offsets, "offsets", torch.int32)
     rp = _dev(rows, "rows", torch.int32) if rows is not None else None
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         ws, wsp = _scratch(workspace, qgemv_grouped_workspace(T, R, E, I, O, code), x.device)
         _call("qgemv_i4g_grouped", wp, sp, O * w.shape[2], O * scales.shape[2], E, op, rp, xp,
-              ldx, T, yp, ldy, R, I, O, gs, code, _ref(epi), wsp, ws.numel(), _stream())
+              ldx, T, yp, ldy, R, I, O, gs, code, _ref(epi), wsp, ws.numel(),
+              _raw_stream(x.device))
     return y
 
 
@@ -738,9 +754,10 @@ def moe_combine(h, pos, gates, residual=None, out=None):
     rp, ldr = _rows(residual, "residual", h.dtype, (T, O)) if residual is not None else (None, 0)
     y = out if out is not None else torch.empty((T, O), dtype=h.dtype, device=h.device)
     yp, ldy = _rows(y, "out", h.dtype, (T, O))
-    with torch.cuda.device(h.device):
+    with _on(h.device):
         _call("qgemv_moe_combine", hp, ldh, R, _dev(pos, "pos", torch.int32),
-              _dev(gates, "gates", torch.float32), T, K, O, rp, ldr, yp, ldy, code, _stream())
+              _dev(gates, "gates", torch.float32), T, K, O, rp, ldr, yp, ldy, code,
+              _raw_stream(h.device))
     return y
 
 
