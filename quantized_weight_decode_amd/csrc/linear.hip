@@ -125,18 +125,32 @@ __global__ __launch_bounds__(256) void linear_general(LinearArgs a,
         }
     }
 
+    // sums through LDS, 16 rows of each 32 at a time, so that one piece of code
+    // ends all outputs
+    float *const os = xs;                                // [32][GN + 1]; the gate's up: ws
+    static_assert(32 * (GN + 1) <= GM * GLD && GN == GM, "fits the operands' LDS");
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < 2; i++) {
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 2; j++)
+        for (int p = 0; p < NW; p++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int m = wm * 32 + i * 16 + 4 * (lane >> 4) + r;
-                const int c = o0 + wn * 32 + j * 16 + (lane & 15);
-                if (m < t.n && c < oc)
-                    finish<XT>(a, t.expert, t.row0 + m, c, acc[0][i][j][r],
-                               GATED ? acc[NW - 1][i][j][r] : 0.0f);
-            }
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+                    (p ? ws[0] : os)[(wm * 16 + 4 * (lane >> 4) + r) * (GN + 1) + wn * 32 +
+                                     j * 16 + (lane & 15)] = acc[p][i][j][r];
+        __syncthreads();
+        finish<XT, 4>(a, t.expert, tid, 256, 32 * GN,
+                      [&](int k, int &row, int &col, float &v, float &up) {
+                          const int m = k / GN, c = k % GN;
+                          const int tr = (m >> 4) * 32 + i * 16 + (m & 15);
+                          row = t.row0 + tr;
+                          col = tr < t.n && o0 + c < oc ? o0 + c : oc;
+                          v = os[m * (GN + 1) + c];
+                          up = GATED ? ws[0][m * (GN + 1) + c] : 0.0f;
+                      });
+    }
 }
 
 // Row tiles of a grouped product, from the experts' offsets on the device:

@@ -399,23 +399,22 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
 #pragma unroll
         for (int r = 0; r < 4; r++) red[wave][4 * lg + r][n * 16 + li] = acc[n][r];
     __syncthreads();
-#pragma unroll 1
-    for (int i = tid; i < t.n * YC; i += SW * 64) {
-        const int r = i / YC, c = i % YC;
-        const int col = nt * YC + c;
-        if (col >= oc) continue;
-        float v = 0.0f, up = 0.0f;
+    finish<XT, 2>(a, t.expert, tid, SW * 64, t.n * YC,
+                  [&](int i, int &row, int &col, float &v, float &up) {
+                      const int r = i / YC, c = i % YC;
+                      row = t.row0 + r;
+                      col = nt * YC + c;
+                      v = up = 0.0f;
 #pragma unroll
-        for (int w = 0; w < SW; w++) {
-            v += red[w][r][c];
-            if (GATED) up += red[w][r][c + YC];
-        }
-        if (a.rows) {
-            const int xi = a.rows[t.row0 + r];
-            if (xi < 0 || xi >= a.T) v = up = __builtin_nanf("");
-        }
-        finish<XT>(a, t.expert, t.row0 + r, col, v, up);
-    }
+                      for (int w = 0; w < SW; w++) {
+                          v += red[w][r][c];
+                          if (GATED) up += red[w][r][c + YC];
+                      }
+                      if (a.rows) {
+                          const int xi = a.rows[row];
+                          if (xi < 0 || xi >= a.T) v = up = __builtin_nanf("");
+                      }
+                  });
 }
 
 template <int FMT, typename XT, int NB, bool GATED>

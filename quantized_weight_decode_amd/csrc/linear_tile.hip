@@ -368,7 +368,8 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     // of loads in flight for int4, one for fp8's larger steps (three stages
     // and one workgroup per CU: 28 % slower at 2048 x 8192 x 8192)
     constexpr int ST = FMT == FMT_FP8 ? 2 : 3;
-    constexpr uint32_t OS = 16 * LDO * sizeof(float);
+    constexpr int EP = MF < 4 ? MF : 4;                  // row blocks of an epilogue pass
+    constexpr uint32_t OS = EP * 16 * LDO * sizeof(float);
     __shared__ __align__(16) char smem[ST * STAGE > OS ? ST * STAGE : OS];
     __shared__ int rx[BM];
     const LinearArgs &a = p.a;
@@ -522,34 +523,33 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     // loads past the last step still write LDS
     wait_loads<0>();
 
-    // Epilogue, 16 rows at a time through LDS: whole rows are stored, and the
-    // end of an output is one piece of code.
+    // Epilogue, EP row blocks at a time through LDS: whole rows are stored.
     float *os = reinterpret_cast<float *>(smem);
     constexpr int YC = 4 * CW;                           // columns of y
-    const int ec = tid % YC, er = tid / YC;
-    const int yc = nt * YC + ec;
-    const int oi = GATED ? (ec / 32) * 64 + ec % 32 : ec;
 #pragma unroll
-    for (int m = 0; m < MF; m++) {
-        if (m * 16 >= t.n) break;                        // uniform over the workgroup
-        if (m > 0) __syncthreads();
+    for (int m0 = 0; m0 < MF; m0 += EP) {
+        if (m0 * 16 >= t.n) break;                       // uniform over the workgroup
+        if (m0 > 0) __syncthreads();
 #pragma unroll
-        for (int n = 0; n < 4; n++)
+        for (int m = m0; m < m0 + EP; m++)
 #pragma unroll
-            for (int r = 0; r < 4; r++)
-                os[(4 * lg + r) * LDO + wave * 64 + n * 16 + li] = acc[m][n][r];
+            for (int n = 0; n < 4; n++)
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+                    os[((m - m0) * 16 + 4 * lg + r) * LDO + wave * 64 + n * 16 + li] =
+                        acc[m][n][r];
         __syncthreads();
-        if (yc < oc)
-#pragma unroll 1
-            for (int r = er; r < 16; r += 256 / YC) {
-                const int row = m * 16 + r;
-                if (row >= t.n) break;
-                const int e = rx[row];
-                float v = ldexpf(os[r * LDO + oi], e);
-                float up = GATED ? ldexpf(os[r * LDO + oi + 32], e) : 0.0f;
-                if (e == BAD_ROW) v = up = __builtin_nanf("");
-                finish<XT>(a, t.expert, t.row0 + row, yc, v, up);
-            }
+        finish<XT, 4>(a, t.expert, tid, 256, min(t.n - m0 * 16, EP * 16) * YC,
+                      [&](int i, int &row, int &col, float &v, float &up) {
+                          const int r = i / YC, c = i % YC;
+                          const int e = rx[m0 * 16 + r];
+                          const float *o = os + r * LDO + (GATED ? (c / 32) * 64 + c % 32 : c);
+                          row = t.row0 + m0 * 16 + r;
+                          col = nt * YC + c;
+                          v = ldexpf(o[0], e);
+                          up = GATED ? ldexpf(o[32], e) : 0.0f;
+                          if (e == BAD_ROW) v = up = __builtin_nanf("");
+                      });
     }
 }
 
@@ -690,25 +690,23 @@ __global__ __launch_bounds__(KW * 64, KW / 4) void linear_narrow(TileArgs p)
             for (int r = 0; r < 4; r++)
                 red[wave][m * 16 + 4 * lg + r][n * 16 + li] = acc[m][n][r];
     __syncthreads();
-#pragma unroll 1
-    for (int i = tid; i < t.n * YC; i += KW * 64) {
-        const int r = i / YC, c = i % YC;
-        const int col = nt * YC + c;
-        if (col >= oc) continue;
-        int xr = t.row0 + r;
-        if (a.rows) xr = a.rows[xr];
-        const int e = xr < 0 || xr >= a.T ? BAD_ROW : p.rexp[xr];
-        float v = 0.0f, up = 0.0f;
+    finish<XT, 4>(a, t.expert, tid, KW * 64, t.n * YC,
+                  [&](int i, int &row, int &col, float &v, float &up) {
+                      const int r = i / YC, c = i % YC;
+                      row = t.row0 + r;
+                      col = nt * YC + c;
+                      const int xr = a.rows ? a.rows[row] : row;
+                      const int e = xr < 0 || xr >= a.T ? BAD_ROW : p.rexp[xr];
+                      v = up = 0.0f;
 #pragma unroll
-        for (int w = 0; w < KW; w++) {
-            v += red[w][r][c];
-            if (GATED) up += red[w][r][c + YC];
-        }
-        v = ldexpf(v, e);
-        up = ldexpf(up, e);
-        if (e == BAD_ROW) v = up = __builtin_nanf("");
-        finish<XT>(a, t.expert, t.row0 + r, col, v, up);
-    }
+                      for (int w = 0; w < KW; w++) {
+                          v += red[w][r][c];
+                          if (GATED) up += red[w][r][c + YC];
+                      }
+                      v = ldexpf(v, e);
+                      up = ldexpf(up, e);
+                      if (e == BAD_ROW) v = up = __builtin_nanf("");
+                  });
 }
 
 #define QG_RUN1(FG, G, R)                                                                   \

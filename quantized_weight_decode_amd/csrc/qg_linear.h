@@ -84,41 +84,81 @@ struct BF16 {
 // -- epilogue ----------------------------------------------------------------
 // act(a) in f32.  silu a / (1 + e^-a); gelu a/2 (1 + erf(a / sqrt 2)), written
 // with erfc for negative a, where 1 + erf cancels; gelu_tanh the tanh form,
-// a * sigmoid(2u).
-__device__ __forceinline__ float activate(float a, int act)
+// a * sigmoid(2u).  The quotient by a reciprocal is within two roundings.
+template <int ACT>
+__device__ __forceinline__ float activate(float a)
 {
-    switch (act) {
-    case QGEMV_ACT_RELU: return a < 0.0f ? 0.0f : a;             // NaN stays NaN
-    case QGEMV_ACT_SILU: return a / (1.0f + expf(-a));
-    case QGEMV_ACT_GELU: {
+    if (ACT == QGEMV_ACT_RELU) return a < 0.0f ? 0.0f : a;       // NaN stays NaN
+    if (ACT == QGEMV_ACT_SILU) return a * __builtin_amdgcn_rcpf(1.0f + expf(-a));
+    if (ACT == QGEMV_ACT_GELU) {
         const float z = a * 0.70710678118654752f;
         return a * (z < 0.0f ? 0.5f * erfcf(-z) : 0.5f + 0.5f * erff(z));
     }
-    case QGEMV_ACT_GELU_TANH: {
+    if (ACT == QGEMV_ACT_GELU_TANH) {
         const float u = 0.79788456080286536f * (a + 0.044715f * a * a * a);
-        return a / (1.0f + expf(-2.0f * u));
+        return a * __builtin_amdgcn_rcpf(1.0f + expf(-2.0f * u));
     }
-    default: return a;
+    return a;
+}
+
+// The ends of a workgroup's outputs: bias and activation (and gate), residual,
+// store.  A thread takes the outputs first, first + stride, ... below count;
+// get(i, row, col, v, up) gives output i's row and column of y (col >= the
+// columns of y: none) and its sums.  The loads of U outputs are in flight
+// together.
+template <typename XT, int ACT, int U, typename Get>
+__device__ __forceinline__ void finish_act(const LinearArgs &a, int expert, int first, int stride,
+                                           int count, Get get)
+{
+    typedef typename XT::raw raw;
+    const int oc = a.gated ? a.O / 2 : a.O;
+    const raw *const bias =
+        a.bias ? static_cast<const raw *>(a.bias) + (size_t)expert * a.O : nullptr;
+#pragma unroll 1
+    for (int i0 = first; i0 < count; i0 += U * stride) {
+        float v[U], up[U], rs[U];
+        int row[U], col[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int i = i0 + u * stride;
+            get(i < count ? i : i0, row[u], col[u], v[u], up[u]);
+            if (i >= count) col[u] = oc;
+            rs[u] = 0.0f;
+            if (col[u] >= oc) continue;
+            if (a.residual)
+                rs[u] = XT::get(
+                    static_cast<const raw *>(a.residual)[(size_t)row[u] * a.ldr + col[u]]);
+            if (bias) {
+                v[u] += XT::get(bias[col[u]]);
+                if (a.gated) up[u] += XT::get(bias[oc + col[u]]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            float r = activate<ACT>(v[u]);
+            if (a.gated) r *= up[u];
+            if (col[u] < oc)
+                static_cast<raw *>(a.y)[(size_t)row[u] * a.ldy + col[u]] = XT::put(r + rs[u]);
+        }
     }
 }
 
-// The end of one output: bias and activation (and gate), residual, store.
-// c is the output column, row the row of y; up only where gated.
-template <typename XT>
-__device__ __forceinline__ void finish(const LinearArgs &a, int expert, int row, int c,
-                                       float acc, float up)
+template <typename XT, int U, typename Get>
+__device__ __forceinline__ void finish(const LinearArgs &a, int expert, int first, int stride,
+                                       int count, Get get)
 {
-    typedef typename XT::raw raw;
-    if (a.bias) {
-        const raw *b = static_cast<const raw *>(a.bias) + (size_t)expert * a.O;
-        acc += XT::get(b[c]);
-        if (a.gated) up += XT::get(b[a.O / 2 + c]);
+    switch (a.act) {
+    case QGEMV_ACT_RELU:
+        return finish_act<XT, QGEMV_ACT_RELU, U>(a, expert, first, stride, count, get);
+    case QGEMV_ACT_SILU:
+        return finish_act<XT, QGEMV_ACT_SILU, U>(a, expert, first, stride, count, get);
+    case QGEMV_ACT_GELU:
+        return finish_act<XT, QGEMV_ACT_GELU, U>(a, expert, first, stride, count, get);
+    case QGEMV_ACT_GELU_TANH:
+        return finish_act<XT, QGEMV_ACT_GELU_TANH, U>(a, expert, first, stride, count, get);
+    default:
+        return finish_act<XT, QGEMV_ACT_NONE, U>(a, expert, first, stride, count, get);
     }
-    float v = activate(acc, a.act);
-    if (a.gated) v *= up;
-    if (a.residual)
-        v += XT::get(static_cast<const raw *>(a.residual)[(size_t)row * a.ldr + c]);
-    static_cast<raw *>(a.y)[(size_t)row * a.ldy + c] = XT::put(v);
 }
 
 // One tile of rows: rows [row0, row0 + n) of y, all of one expert.
