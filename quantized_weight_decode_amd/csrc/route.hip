@@ -55,7 +55,7 @@ __global__ __launch_bounds__(GT) void group_rows(const int32_t *__restrict__ ids
                                                  int32_t *__restrict__ tokens,
                                                  int32_t *__restrict__ pos)
 {
-    extern __shared__ int hist[];        // [GW][E]
+    extern __shared__ int hist[];        // [GW][E], then all slots, earlier blocks' slots
     __shared__ int wsum[GW];
     __shared__ int total_s;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, blk = blockIdx.x;
@@ -71,22 +71,40 @@ __global__ __launch_bounds__(GT) void group_rows(const int32_t *__restrict__ ids
     }
     __syncthreads();
 
-    // thread: experts 2 tid and 2 tid + 1 (E <= 1024); this block's slots,
-    // the earlier blocks' and all of them
+    // all slots of each expert and those of the earlier blocks: waves take
+    // blocks in turn, lanes experts
+    int *const all_s = hist + GW * E, *const before_s = all_s + E;
+    for (int e = tid; e < E; e += GT) {
+        int n0 = 0;
+        if (nblk == 1)
+            for (int w = 0; w < GW; w++) n0 += hist[w * E + e];
+        all_s[e] = n0;
+        before_s[e] = 0;
+    }
+    if (nblk > 1) {
+        __syncthreads();
+        for (int e = lane; e < E; e += 64) {
+            int sum = 0, early = 0;
+#pragma unroll 8
+            for (int b = wave; b < nblk; b += GW) {
+                const int c = counts[(size_t)b * E + e];
+                sum += c;
+                early += b < blk ? c : 0;
+            }
+            atomicAdd(&all_s[e], sum);
+            atomicAdd(&before_s[e], early);
+        }
+    }
+    __syncthreads();
+
+    // thread: experts 2 tid and 2 tid + 1 (E <= 1024)
     int before[2] = {0, 0}, all[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 2; j++) {
         const int e = 2 * tid + j;
         if (e >= E) continue;
-        if (nblk > 1) {
-            for (int b = 0; b < nblk; b++) {
-                const int c = counts[(size_t)b * E + e];
-                all[j] += c;
-                before[j] += b < blk ? c : 0;
-            }
-        } else {
-            for (int w = 0; w < GW; w++) all[j] += hist[w * E + e];
-        }
+        all[j] = all_s[e];
+        before[j] = before_s[e];
     }
     int incl = all[0] + all[1];
 #pragma unroll
@@ -265,7 +283,7 @@ hipError_t launch_moe_group(const int32_t *ids, int T, int K, int E, int32_t *of
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(group_rows, dim3(nblk), dim3(GT), GW * E * sizeof(int), st, ids, n, K, E,
+    hipLaunchKernelGGL(group_rows, dim3(nblk), dim3(GT), (GW + 2) * E * sizeof(int), st, ids, n, K, E,
                        chunk, counts, nblk, offsets, tokens, pos);
     return hipGetLastError();
 }
