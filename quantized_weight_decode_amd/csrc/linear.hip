@@ -12,143 +12,252 @@ namespace {
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
-constexpr int GM = 64;          // rows of y per workgroup tile
 constexpr int GN = 64;          // columns of y per workgroup tile
 constexpr int GK = 32;          // columns of W per K step
 constexpr int GLD = GK + 4;     // LDS row stride in floats
+constexpr int GM_FEW = 16;      // rows of y per tile, few rows
+constexpr int GM = 64;          // and many
+
+// Eight values of a row of x from column k: one load of any alignment, or, for
+// a row's last columns, element by element with zeros behind them.
+template <typename XT>
+struct X8 {
+    typename XT::raw v[8];
+    __device__ __forceinline__ void load(const typename XT::raw *row, int k)
+    {
+        __builtin_memcpy(v, row + k, sizeof(v));
+    }
+    __device__ __forceinline__ void load_tail(const typename XT::raw *row, int k, int I)
+    {
+#pragma unroll
+        for (int c = 0; c < 8; c++) v[c] = k + c < I ? row[k + c] : typename XT::raw(0);
+    }
+};
+
+// Eight weights of a row from column k (a multiple of eight), decoded as the
+// definition has it.  Group sizes of eight or more have at most two scales
+// among them, smaller ones (SMALL, even) one per pair.  The tail's values
+// behind the row are finite and meet zeros of x.
+template <int FMT, bool SMALL>
+struct W8 {
+    uint32_t q[2];                       // int4: the first
+    float s[4];
+    int edge;                            // columns of s[0]
+    __device__ __forceinline__ void load_scales(const float *sc, int k, int ng, int gs)
+    {
+        if (SMALL) {
+#pragma unroll
+            for (int c = 0; c < 4; c++) s[c] = sc[min((k + 2 * c) / gs, ng - 1)];
+        } else {
+            const int g = min(k / gs, ng - 1);
+            edge = (g + 1) * gs - k;
+            s[0] = sc[g];
+            s[1] = sc[min(g + 1, ng - 1)];
+        }
+    }
+    __device__ __forceinline__ void load(const uint8_t *row, const float *sc, int k, int ng,
+                                         int gs)
+    {
+        __builtin_memcpy(q, row + (FMT == FMT_I4G ? k / 2 : k), FMT == FMT_I4G ? 4 : 8);
+        load_scales(sc, k, ng, gs);
+    }
+    __device__ __forceinline__ void load_tail(const uint8_t *row, const float *sc, int k, int I,
+                                              int ng, int gs)
+    {
+        q[0] = q[1] = 0;
+#pragma unroll
+        for (int c = 0; c < 8; c++) {
+            if (k + c >= I) continue;
+            if (FMT == FMT_I4G) {
+                if (c % 2 == 0) q[0] |= (uint32_t)row[(k + c) / 2] << (4 * c);
+            } else {
+                q[c / 4] |= (uint32_t)row[k + c] << (8 * (c % 4));
+            }
+        }
+        load_scales(sc, k, ng, gs);
+    }
+    __device__ __forceinline__ void decode(float w[8]) const
+    {
+        if (FMT == FMT_I4G) {
+            float e[4], o[4];
+            nib8(q[0], e, o);
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                w[2 * c] = e[c] * NIB_XSCALE - 8.0f;
+                w[2 * c + 1] = o[c] * NIB_XSCALE - 8.0f;
+            }
+        } else {
+            e4m3x4(q[0], w);
+            e4m3x4(q[1], w + 4);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; c++) w[c] *= SMALL ? s[c / 2] : c < edge ? s[0] : s[1];
+    }
+};
 
 // General kernel: every valid shape, alignment and group size.  W decoded to
 // f32 as the definition has it ((q - 8) * s or e4m3 * s, one rounding),
 // products and sums in f32 on v_mfma_f32_16x16x4_f32, whose 157 TFLOP/s peak
-// bounds it for many rows.  64 x 64 tiles of 4 waves (2 x 2 blocks each); a
-// gated product holds the gate's and the up projection's accumulators for the
-// same 64 columns of y.  Loads are per element with their column checked, so
-// nothing needs alignment or whole K steps.
-template <int FMT, typename XT, bool GATED>
+// bounds it for many rows.  A gated product holds the gate's and the up
+// projection's accumulators for the same columns of y.  The global loads of
+// the next K step are in flight during the products.
+//
+// FEW = false: 64 x 64 tiles of 4 waves (2 x 2 blocks of 16 each), a thread
+// stages eight columns of one row of each operand.  FEW = true: 16 x 64 tiles;
+// the waves take K steps in turn with LDS of their own, and their sums are
+// joined in a fixed order.
+template <int FMT, typename XT, bool GATED, bool FEW, bool SMALL>
 __global__ __launch_bounds__(256) void linear_general(LinearArgs a,
                                                       const RowTile *__restrict__ tiles)
 {
     typedef typename XT::raw raw;
     constexpr int NW = GATED ? 2 : 1;
-    __shared__ __align__(16) float xs[GM * GLD];
-    __shared__ __align__(16) float ws[NW][GN * GLD];
+    constexpr int BM = FEW ? GM_FEW : GM;
+    constexpr int MB = FEW ? 1 : 2, NB = FEW ? 4 : 2;    // blocks of a wave
+    constexpr int WR = FEW ? 4 : 1;                      // rows of W a thread stages
+    constexpr int STAGE = (BM + NW * GN) * GLD;          // floats
+    constexpr int OLD = GN + 1;                          // epilogue row stride
+    constexpr int OUT = (FEW ? 4 * GM_FEW : 32) * OLD * NW;
+    constexpr int STAGES = (FEW ? 4 : 1) * STAGE;
+    __shared__ __align__(16) float lds[STAGES > OUT ? STAGES : OUT];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave & 1, wn = wave >> 1;
+    const int wm = FEW ? 0 : wave & 1, wn = FEW ? 0 : wave >> 1;
+    float *const xs = lds + (FEW ? wave * STAGE : 0);
+    float *const ws = xs + BM * GLD;
     const int oc = GATED ? a.O / 2 : a.O;                // columns of y
     const int ntn = (oc + GN - 1) / GN;
     const int o0 = (int)(blockIdx.x % ntn) * GN;
     const int mt = (int)(blockIdx.x / ntn);
     RowTile t;
     if (tiles) t = tiles[mt];
-    else t = RowTile{0, mt * GM, min(GM, a.R - mt * GM), 0};
+    else t = RowTile{0, mt * BM, min(BM, a.R - mt * BM), 0};
     if (t.n <= 0) return;                                // uniform over the workgroup
 
-    f32x4v acc[NW][2][2];
+    f32x4v acc[NW][MB][NB];
 #pragma unroll
     for (int p = 0; p < NW; p++)
 #pragma unroll
-        for (int i = 0; i < 2; i++)
+        for (int i = 0; i < MB; i++)
 #pragma unroll
-            for (int j = 0; j < 2; j++) acc[p][i][j] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < NB; j++) acc[p][i][j] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // thread's staging place: row tid / 4, eight columns from 8 (tid % 4)
-    const int sr = tid >> 2, sc = (tid & 3) * 8;
-    const bool xok = sr < t.n;
-    bool xbad = false;
-    long long xrow = t.row0 + (xok ? sr : 0);
+    // this thread's staging place: row sr of x, rows sr + 16 i of W, eight
+    const int u = FEW ? lane : tid;
+    const int sr = u >> 2, sc = (u & 3) * 8;
+    // columns from sc; rows behind the tile or the matrix repeat the first
+    long long xrow = t.row0 + (sr < t.n ? sr : 0);
     if (a.rows) {
         const int r = a.rows[xrow];
-        xbad = r < 0 || r >= a.T;
-        xrow = xbad ? 0 : r;
+        xrow = r < 0 || r >= a.T ? 0 : r;                // marked in the epilogue
     }
     const raw *xsrc = static_cast<const raw *>(a.x) + (size_t)xrow * a.ldx;
-    const bool wok = o0 + sr < oc;
-    const int wrow = wok ? o0 + sr : 0;
     const size_t rb = FMT == FMT_I4G ? ((size_t)a.I + 1) / 2 : (size_t)a.I;
-    const uint8_t *wsrc = a.w + (size_t)t.expert * a.w_stride;
-    const float *ssrc = a.scales + (size_t)t.expert * a.s_stride;
+    const uint8_t *wsrc[NW][WR];
+    const float *ssrc[NW][WR];
+#pragma unroll
+    for (int p = 0; p < NW; p++)
+#pragma unroll
+        for (int i = 0; i < WR; i++) {
+            const int c = o0 + sr + 16 * i;
+            const int row = (c < oc ? c : 0) + p * oc;
+            wsrc[p][i] = a.w + (size_t)t.expert * a.w_stride + (size_t)row * rb;
+            ssrc[p][i] = a.scales + (size_t)t.expert * a.s_stride +
+                         (size_t)(FMT == FMT_I4G ? row : row / 128) * a.ng;
+        }
+    const int gs = FMT == FMT_FP8 ? 128 : a.gs;
 
-    for (int k0 = 0; k0 < a.I; k0 += GK) {
-        float xv[8], wv[NW][8];
+    X8<XT> xv;
+    W8<FMT, SMALL> wv[NW][WR];
+    auto load = [&](int k0) {
         const int k = k0 + sc;
+        if (k0 + GK <= a.I) {                            // uniform over the wave
+            xv.load(xsrc, k);
 #pragma unroll
-        for (int c = 0; c < 8; c++) {
-            xv[c] = 0.0f;
-            if (xok && k + c < a.I)
-                xv[c] = xbad ? __builtin_nanf("") : XT::get(xsrc[k + c]);
+            for (int p = 0; p < NW; p++)
+#pragma unroll
+                for (int i = 0; i < WR; i++)
+                    wv[p][i].load(wsrc[p][i], ssrc[p][i], k, a.ng, gs);
+        } else {
+            xv.load_tail(xsrc, k, a.I);
+#pragma unroll
+            for (int p = 0; p < NW; p++)
+#pragma unroll
+                for (int i = 0; i < WR; i++)
+                    wv[p][i].load_tail(wsrc[p][i], ssrc[p][i], k, a.I, a.ng, gs);
         }
+    };
+    constexpr int STEP = (FEW ? 4 : 1) * GK;
+    const int first = FEW ? wave * GK : 0;
+    if (first < a.I) load(first);
+    for (int k0 = first; k0 < a.I; k0 += STEP) {
+        if (!FEW && k0 > 0) __syncthreads();             // the previous step's reads are done
 #pragma unroll
-        for (int p = 0; p < NW; p++) {
-            const int row = wrow + p * oc;
-            const uint8_t *wp = wsrc + (size_t)row * rb;
-            const float *sp = ssrc + (size_t)(FMT == FMT_I4G ? row : row / 128) * a.ng;
-#pragma unroll
-            for (int c = 0; c < 8; c++) {
-                wv[p][c] = 0.0f;
-                if (!wok || k + c >= a.I) continue;
-                if (FMT == FMT_I4G) {
-                    const uint8_t b = wp[(size_t)(k + c) >> 1];
-                    const int q = (c & 1) ? b >> 4 : b & 15;
-                    wv[p][c] = (float)(q - 8) * sp[(k + c) / a.gs];
-                } else {
-                    wv[p][c] = fp8pair_lo(wp[k + c]).x * sp[(k + c) / 128];
-                }
-            }
-        }
-        if (k0 > 0) __syncthreads();                     // the previous step's reads are done
-#pragma unroll
-        for (int c = 0; c < 8; c++) xs[sr * GLD + sc + c] = xv[c];
+        for (int c = 0; c < 8; c++) xs[sr * GLD + sc + c] = XT::get(xv.v[c]);
 #pragma unroll
         for (int p = 0; p < NW; p++)
 #pragma unroll
-            for (int c = 0; c < 8; c++) ws[p][sr * GLD + sc + c] = wv[p][c];
-        __syncthreads();
+            for (int i = 0; i < WR; i++) {
+                float w[8];
+                wv[p][i].decode(w);
+#pragma unroll
+                for (int c = 0; c < 8; c++) ws[(p * GN + sr + 16 * i) * GLD + sc + c] = w[c];
+            }
+        if (!FEW) __syncthreads();
+        if (k0 + STEP < a.I) load(k0 + STEP);
 #pragma unroll
         for (int kk = 0; kk < GK; kk += 4) {
-            float av[2], bv[NW][2];
+            float av[MB], bv[NW][NB];
 #pragma unroll
-            for (int i = 0; i < 2; i++)
+            for (int i = 0; i < MB; i++)
                 av[i] = xs[(wm * 32 + i * 16 + (lane & 15)) * GLD + kk + (lane >> 4)];
 #pragma unroll
             for (int p = 0; p < NW; p++)
 #pragma unroll
-                for (int j = 0; j < 2; j++)
-                    bv[p][j] = ws[p][(wn * 32 + j * 16 + (lane & 15)) * GLD + kk + (lane >> 4)];
+                for (int j = 0; j < NB; j++)
+                    bv[p][j] =
+                        ws[(p * GN + wn * 32 + j * 16 + (lane & 15)) * GLD + kk + (lane >> 4)];
 #pragma unroll
             for (int p = 0; p < NW; p++)
 #pragma unroll
-                for (int i = 0; i < 2; i++)
+                for (int i = 0; i < MB; i++)
 #pragma unroll
-                    for (int j = 0; j < 2; j++)
+                    for (int j = 0; j < NB; j++)
                         acc[p][i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
                             av[i], bv[p][j], acc[p][i][j], 0, 0, 0);
         }
     }
 
-    // sums through LDS, 16 rows of each 32 at a time, so that one piece of code
-    // ends all outputs
-    float *const os = xs;                                // [32][GN + 1]; the gate's up: ws
-    static_assert(32 * (GN + 1) <= GM * GLD && GN == GM, "fits the operands' LDS");
+    // sums through LDS (FEW: of all waves; else 16 rows of each 32 at a time),
+    // so that one piece of code ends all outputs
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < MB; i++) {
         __syncthreads();
 #pragma unroll
         for (int p = 0; p < NW; p++)
 #pragma unroll
-            for (int j = 0; j < 2; j++)
+            for (int j = 0; j < NB; j++)
 #pragma unroll
-                for (int r = 0; r < 4; r++)
-                    (p ? ws[0] : os)[(wm * 16 + 4 * (lane >> 4) + r) * (GN + 1) + wn * 32 +
-                                     j * 16 + (lane & 15)] = acc[p][i][j][r];
+                for (int r = 0; r < 4; r++) {
+                    const int m = (FEW ? wave : wm) * 16 + 4 * (lane >> 4) + r;
+                    lds[(m * NW + p) * OLD + wn * 32 + j * 16 + (lane & 15)] = acc[p][i][j][r];
+                }
         __syncthreads();
-        finish<XT, 4>(a, t.expert, tid, 256, 32 * GN,
+        finish<XT, 4>(a, t.expert, tid, 256, (FEW ? GM_FEW : 32) * GN,
                       [&](int k, int &row, int &col, float &v, float &up) {
                           const int m = k / GN, c = k % GN;
-                          const int tr = (m >> 4) * 32 + i * 16 + (m & 15);
+                          const int tr = FEW ? m : (m >> 4) * 32 + i * 16 + (m & 15);
                           row = t.row0 + tr;
                           col = tr < t.n && o0 + c < oc ? o0 + c : oc;
-                          v = os[m * (GN + 1) + c];
-                          up = GATED ? ws[0][m * (GN + 1) + c] : 0.0f;
+                          v = up = 0.0f;
+#pragma unroll
+                          for (int w = 0; w < (FEW ? 4 : 1); w++) {
+                              v += lds[((w * 16 + m) * NW) * OLD + c];
+                              if (GATED) up += lds[((w * 16 + m) * NW + 1) * OLD + c];
+                          }
+                          if (a.rows && col < oc) {
+                              const int xi = a.rows[row];
+                              if (xi < 0 || xi >= a.T) v = up = __builtin_nanf("");
+                          }
                       });
     }
 }
@@ -258,13 +367,27 @@ void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
 }
 
 template <int FMT, typename XT>
-void run_general(const LinearArgs &a, const RowTile *tiles, unsigned grid, hipStream_t st)
+void run_general(const LinearArgs &a, bool few, const RowTile *tiles, unsigned grid,
+                 hipStream_t st)
 {
-    if (a.gated)
-        hipLaunchKernelGGL((linear_general<FMT, XT, true>), dim3(grid), dim3(256), 0, st, a, tiles);
-    else
-        hipLaunchKernelGGL((linear_general<FMT, XT, false>), dim3(grid), dim3(256), 0, st, a,
-                           tiles);
+#define QG_RUN(G, F, S)                                                                     \
+    hipLaunchKernelGGL((linear_general<FMT, XT, G, F, S>), dim3(grid), dim3(256), 0, st, a, tiles)
+#define QG_RUN_G(F, S)                                                                      \
+    do {                                                                                    \
+        if (a.gated) QG_RUN(true, F, S);                                                    \
+        else QG_RUN(false, F, S);                                                           \
+    } while (0)
+    if constexpr (FMT == FMT_I4G) {
+        if (a.gs < 8) {
+            if (few) QG_RUN_G(true, true);
+            else QG_RUN_G(false, true);
+            return;
+        }
+    }
+    if (few) QG_RUN_G(true, false);
+    else QG_RUN_G(false, false);
+#undef QG_RUN_G
+#undef QG_RUN
 }
 
 }  // namespace
@@ -282,7 +405,14 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStr
     const bool fits = tile_fits(fmt, a);
     const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
     const bool stream = rows <= 16 && stream_fits(fmt, a);
-    int bm = GM;
+    // the general kernel's tiles: 16 rows also where 64-row tiles would leave
+    // CUs without one (64 x 6001 x 12288 bf16: 135 us, 227 us in 192 tiles of
+    // 64 rows)
+    const long long tiles64 =
+        (long long)((a.R + GM - 1) / GM + (a.offsets ? (a.E < a.R ? a.E : a.R) / 2 : 0)) *
+        ((oc + GN - 1) / GN);
+    const bool few = rows <= GM_FEW || tiles64 <= cu_count();
+    int bm = few ? GM_FEW : GM;
     bool narrow = false;
     if (stream) {
         bm = 16;
@@ -305,11 +435,11 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStr
     const long long grid = mt * ((oc + GN - 1) / GN);
     if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     if (fmt == FMT_I4G) {
-        if (a.dtype == QGEMV_BF16) run_general<FMT_I4G, BF16>(a, tiles, (unsigned)grid, st);
-        else run_general<FMT_I4G, F32>(a, tiles, (unsigned)grid, st);
+        if (a.dtype == QGEMV_BF16) run_general<FMT_I4G, BF16>(a, few, tiles, (unsigned)grid, st);
+        else run_general<FMT_I4G, F32>(a, few, tiles, (unsigned)grid, st);
     } else {
-        if (a.dtype == QGEMV_BF16) run_general<FMT_FP8, BF16>(a, tiles, (unsigned)grid, st);
-        else run_general<FMT_FP8, F32>(a, tiles, (unsigned)grid, st);
+        if (a.dtype == QGEMV_BF16) run_general<FMT_FP8, BF16>(a, few, tiles, (unsigned)grid, st);
+        else run_general<FMT_FP8, F32>(a, few, tiles, (unsigned)grid, st);
     }
     return hipGetLastError();
 }
