@@ -339,6 +339,7 @@ void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
         double cost;
     };
     static const Kind bf16[] = {{128, false, true, 1.0},
+                                {96, false, false, 0.83},
                                 {64, false, false, 0.66},
                                 {32, false, false, 0.58},
                                 {64, true, true, 0.265},
@@ -347,7 +348,7 @@ void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
                                {32, true, true, 0.26}};
     const bool half = a.dtype == QGEMV_BF16;
     const Kind *kinds = half ? bf16 : f32;
-    const int n = half ? 5 : 3;
+    const int n = half ? 6 : 3;
     const long long ncu = cu_count();
     double best = -1.0;
     for (int i = 0; i < n; i++) {

@@ -71,7 +71,7 @@ __device__ __forceinline__ void store8(const float v[8], int shift, _Float16 *hi
 
 template <typename XT, int FMT, int TH, int NCH, bool VEC>
 __global__ __launch_bounds__(TH) void pack_rows(const typename XT::raw *__restrict__ x,
-                                                long long ldx, int I, int Ip,
+                                                long long ldx, int I, int Ip, int ldp,
                                                 _Float16 *__restrict__ hi,
                                                 _Float16 *__restrict__ lo,
                                                 int *__restrict__ rexp)
@@ -80,8 +80,8 @@ __global__ __launch_bounds__(TH) void pack_rows(const typename XT::raw *__restri
     const int tid = threadIdx.x;
     const long long t = blockIdx.x;
     const typename XT::raw *src = x + (size_t)t * ldx;
-    hi += (size_t)t * Ip;
-    if (lo) lo += (size_t)t * Ip;
+    hi += (size_t)t * ldp;
+    if (lo) lo += (size_t)t * ldp;
     float v[NCH ? NCH : 1][8];
     uint32_t m = 0;
     if (NCH) {
@@ -132,11 +132,11 @@ __global__ __launch_bounds__(TH) void pack_rows(const typename XT::raw *__restri
 }
 
 template <typename XT, int FMT, bool VEC>
-void run_pack(const LinearArgs &a, int Ip, _Float16 *hi, _Float16 *lo, int *rexp, hipStream_t st)
+void run_pack(const LinearArgs &a, int Ip, int ldp, _Float16 *hi, _Float16 *lo, int *rexp, hipStream_t st)
 {
 #define QG_PACK(TH, NCH)                                                                    \
     hipLaunchKernelGGL((pack_rows<XT, FMT, TH, NCH, VEC>), dim3(a.T), dim3(TH), 0, st,      \
-                       static_cast<const typename XT::raw *>(a.x), a.ldx, a.I, Ip, hi, lo, rexp)
+                       static_cast<const typename XT::raw *>(a.x), a.ldx, a.I, Ip, ldp, hi, lo, rexp)
     if (Ip <= 2048) QG_PACK(64, 4);
     else if (Ip <= 8192) QG_PACK(256, 4);
     else if (Ip <= 16384) QG_PACK(256, 8);
@@ -145,17 +145,17 @@ void run_pack(const LinearArgs &a, int Ip, _Float16 *hi, _Float16 *lo, int *rexp
 }
 
 template <typename XT>
-hipError_t pack(WeightFormat fmt, const LinearArgs &a, int Ip, _Float16 *hi, _Float16 *lo,
-                int *rexp, hipStream_t st)
+hipError_t pack(WeightFormat fmt, const LinearArgs &a, int Ip, int ldp, _Float16 *hi,
+                _Float16 *lo, int *rexp, hipStream_t st)
 {
     const bool vec =
         (((uintptr_t)a.x | (uintptr_t)(a.ldx * sizeof(typename XT::raw))) & 15) == 0;
     if (fmt == FMT_I4G) {
-        if (vec) run_pack<XT, FMT_I4G, true>(a, Ip, hi, lo, rexp, st);
-        else run_pack<XT, FMT_I4G, false>(a, Ip, hi, lo, rexp, st);
+        if (vec) run_pack<XT, FMT_I4G, true>(a, Ip, ldp, hi, lo, rexp, st);
+        else run_pack<XT, FMT_I4G, false>(a, Ip, ldp, hi, lo, rexp, st);
     } else {
-        if (vec) run_pack<XT, FMT_FP8, true>(a, Ip, hi, lo, rexp, st);
-        else run_pack<XT, FMT_FP8, false>(a, Ip, hi, lo, rexp, st);
+        if (vec) run_pack<XT, FMT_FP8, true>(a, Ip, ldp, hi, lo, rexp, st);
+        else run_pack<XT, FMT_FP8, false>(a, Ip, ldp, hi, lo, rexp, st);
     }
     return hipGetLastError();
 }
@@ -262,7 +262,7 @@ struct TileArgs {
     const _Float16 *hi, *lo;
     const int *rexp;
     const RowTile *tiles;
-    int Ip, ntm, ntn;
+    int Ip, ldp, ntm, ntn;                               // padded columns, row stride of hi, lo
 };
 
 // One K step of a wave: 16 MF rows of x (packed in LDS at sm, NP planes of 8
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     // of loads in flight for int4, one for fp8's larger steps (three stages
     // and one workgroup per CU: 28 % slower at 2048 x 8192 x 8192)
     constexpr int ST = FMT == FMT_FP8 ? 2 : 3;
-    constexpr int EP = MF < 4 ? MF : 4;                  // row blocks of an epilogue pass
+    constexpr int EP = MF % 4 == 0 ? 4 : MF % 3 == 0 ? 3 : MF;   // row blocks of an epilogue pass
     constexpr uint32_t OS = EP * 16 * LDO * sizeof(float);
     __shared__ __align__(16) char smem[ST * STAGE > OS ? ST * STAGE : OS];
     __shared__ int rx[BM];
@@ -418,7 +418,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
             r = a.rows[r];
             r = r < 0 || r >= a.T ? 0 : r;
         }
-        aoff[i] = ((uint32_t)r * (uint32_t)p.Ip + ((c & 7) ^ swizzle(row)) * 8) * 2;
+        aoff[i] = ((uint32_t)r * (uint32_t)p.ldp + ((c & 7) ^ swizzle(row)) * 8) * 2;
     }
 
     // weight rows of this lane
@@ -605,7 +605,7 @@ __global__ __launch_bounds__(KW * 64, KW / 4) void linear_narrow(TileArgs p)
             r = a.rows[r];
             r = r < 0 || r >= a.T ? 0 : r;
         }
-        aoff[i] = ((uint32_t)r * (uint32_t)p.Ip + ((c & 7) ^ swizzle(row & 15)) * 8) * 2;
+        aoff[i] = ((uint32_t)r * (uint32_t)p.ldp + ((c & 7) ^ swizzle(row & 15)) * 8) * 2;
     }
     const size_t rb = FMT == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
     const uint8_t *const wbase = a.w + (size_t)t.expert * a.w_stride;
@@ -771,13 +771,16 @@ hipError_t run_narrow(const TileArgs &p, unsigned grid, hipStream_t st)
 }
 
 int padded(int I) { return (I + TK - 1) / TK * TK; }
+// Row stride of the packed planes: an odd count of 256 bytes, so that a K
+// step's pieces of a tile's rows lie in all of the 16 L2 channels.
+int plane_stride(int I) { return ((padded(I) + 127) / 128 | 1) * 128; }
 
 }  // namespace
 
 size_t tile_workspace(int T, int I, int dtype)
 {
     return align256((size_t)T * sizeof(int)) +
-           align256((size_t)T * padded(I) * 2) * (dtype == QGEMV_BF16 ? 1 : 2);
+           align256((size_t)T * plane_stride(I) * 2) * (dtype == QGEMV_BF16 ? 1 : 2);
 }
 
 bool tile_fits(WeightFormat fmt, const LinearArgs &a)
@@ -785,7 +788,7 @@ bool tile_fits(WeightFormat fmt, const LinearArgs &a)
     const size_t rb = fmt == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
     return a.I % 32 == 0 && (fmt == FMT_FP8 || a.gs % 32 == 0) && ((uintptr_t)a.w & 15) == 0 &&
            (!a.offsets || a.w_stride % 16 == 0) && rb * a.O < (1ull << 32) &&
-           (size_t)a.ng * a.O * 4 < (1ull << 32) && (size_t)a.T * padded(a.I) * 2 < (1ull << 32);
+           (size_t)a.ng * a.O * 4 < (1ull << 32) && (size_t)a.T * plane_stride(a.I) * 2 < (1ull << 32);
 }
 
 hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int bm,
@@ -794,11 +797,12 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int b
     TileArgs p{};
     p.a = a;
     p.Ip = padded(a.I);
+    p.ldp = plane_stride(a.I);
     char *at = static_cast<char *>(ws);
     int *rexp = reinterpret_cast<int *>(at);
     at += align256((size_t)a.T * sizeof(int));
     _Float16 *hi = reinterpret_cast<_Float16 *>(at);
-    at += align256((size_t)a.T * p.Ip * 2);
+    at += align256((size_t)a.T * p.ldp * 2);
     _Float16 *lo = a.dtype == QGEMV_BF16 ? nullptr : reinterpret_cast<_Float16 *>(at);
     p.hi = hi;
     p.lo = lo;
@@ -810,8 +814,8 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int b
     p.ntn = (oc + cols - 1) / cols;
     const long long grid = (long long)ntm * p.ntn;
     if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-    const hipError_t e = a.dtype == QGEMV_BF16 ? pack<BF16>(fmt, a, p.Ip, hi, lo, rexp, st)
-                                               : pack<F32>(fmt, a, p.Ip, hi, lo, rexp, st);
+    const hipError_t e = a.dtype == QGEMV_BF16 ? pack<BF16>(fmt, a, p.Ip, p.ldp, hi, lo, rexp, st)
+                                               : pack<F32>(fmt, a, p.Ip, p.ldp, hi, lo, rexp, st);
     if (e != hipSuccess) return e;
 #define QG_TILE(MF)                                                                         \
     (fmt == FMT_I4G                                                                         \
@@ -831,6 +835,9 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int b
     case 128:                                            // bf16 only
         return fmt == FMT_I4G ? run_tile<FMT_I4G, BF16, 8>(p, (unsigned)grid, st)
                               : run_tile<FMT_FP8, BF16, 8>(p, (unsigned)grid, st);
+    case 96:                                             // bf16 only
+        return fmt == FMT_I4G ? run_tile<FMT_I4G, BF16, 6>(p, (unsigned)grid, st)
+                              : run_tile<FMT_FP8, BF16, 6>(p, (unsigned)grid, st);
     case 64: return QG_TILE(4);
     default: return QG_TILE(2);
     }

@@ -35,7 +35,7 @@ size_t linear_workspace(int T, int R, int E, int I, int O, int dtype);
 hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStream_t st);
 
 // The f16 tile kernels (linear_tile.hip): shapes they take, workspace, launch
-// with row tiles of bm in {32, 64, 128} (narrow: {32, 64}); tiles == nullptr:
+// with row tiles of bm in {32, 64, 96, 128} (narrow: {32, 64}); tiles == nullptr:
 // dense.
 struct RowTile;
 bool tile_fits(WeightFormat fmt, const LinearArgs &a);
