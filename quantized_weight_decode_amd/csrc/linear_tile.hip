@@ -221,25 +221,6 @@ __device__ __forceinline__ void wait_loads()
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "i"(N) : "memory");
 }
 
-// A lane's two fragments (h = 0, 1) of one weight row and K step from the
-// row's bytes in LDS.
-template <int FMT, int FG>
-__device__ __forceinline__ void unpack(const char *row, int lg, f16x8 out[2])
-{
-    if constexpr (FMT == FMT_FP8) {
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(row + lg * 16);
-        out[0] = fp8x8_f16(v.x, v.y);
-        out[1] = fp8x8_f16(v.z, v.w);
-    } else if constexpr (FG == 64) {
-        const u32x2 v = *reinterpret_cast<const u32x2 *>(row + lg * 8);
-        out[0] = nib8_f16(v.x);
-        out[1] = nib8_f16(v.y);
-    } else {
-        out[0] = nib8_f16(*reinterpret_cast<const uint32_t *>(row + lg * 4));
-        out[1] = nib8_f16(*reinterpret_cast<const uint32_t *>(row + 16 + lg * 4));
-    }
-}
-
 constexpr int BAD_ROW = -0x7FFFFFFF;     // exponent of a row of y without a row of x
 
 constexpr int TK = 64;          // columns per K step
@@ -263,6 +244,98 @@ struct TileArgs {
     const int *rexp;
     const RowTile *tiles;
     int Ip, ldp, ntm, ntn;                               // padded columns, row stride of hi, lo
+    uint32_t g32, gmagic;                                // gs / 32 and 2^32 over it, rounded down
+};
+
+// Scale group of column 32 k32, by multiplication (the quotient is at most one
+// too small).
+__device__ __forceinline__ uint32_t scale_group(uint32_t k32, uint32_t g32, uint32_t magic)
+{
+    const uint32_t q = __umulhi(k32, magic);
+    return q + ((q + 1) * g32 <= k32 ? 1u : 0u);
+}
+
+// A wave's weights and scales on their way through its part of LDS: ROWS rows
+// of W by stages of 64 bytes per row (WS K steps: two of int4, one of fp8),
+// two stages.  64 bytes at a time: loads of 32 bytes in one K step and the
+// next 32 of the same line in the next one stall the vector cache while the
+// line is on its way (routed prompt of 1024 tokens: half of all cycles).
+// Lanes next to each other load 16-byte pieces of one row.  Piece c of a row
+// sits at c ^ key(row), which spreads a fragment's rows over the banks.
+template <int FMT, int FG, int ROWS>
+struct Weights {
+    static constexpr int WS = FMT == FMT_FP8 ? 1 : 2;
+    static constexpr int SG = WS * TK / FG;              // scale groups of a stage
+    static constexpr int NS = TK / FG;                   // and of a K step
+    static constexpr int WL = ROWS * 4 / 64, SL = ROWS * SG / 64, LOADS = WL + SL;
+    static constexpr uint32_t WBYTES = ROWS * 64, BYTES = WBYTES + ROWS * SG * 4;
+    static constexpr int NB = ROWS / 16;
+    uint32_t woff[WL], soff[SL], piece;
+
+    static __device__ __forceinline__ int key(int row)
+    {
+        const int j = (row >> 2) & 3;
+        return j ^ ((j & 1) << 1);
+    }
+    // row(i): row i of the wave's, as a row of W
+    template <typename Row>
+    __device__ __forceinline__ void init(const LinearArgs &a, uint32_t rb, int lane, Row row)
+    {
+#pragma unroll
+        for (int i = 0; i < WL; i++) woff[i] = (uint32_t)row(lane / 4 + 16 * i) * rb;
+        piece = ((lane & 3) ^ key(lane / 4)) * 16;
+#pragma unroll
+        for (int i = 0; i < SL; i++) {
+            const int r = row((lane + 64 * i) / SG);
+            soff[i] = (uint32_t)(FMT == FMT_I4G ? r : r >> 7) * (uint32_t)a.ng;
+        }
+    }
+    // Stage st into LDS at `lds`.  Behind the row's end its last bytes are read
+    // again, which meet zeros of x.
+    __device__ __forceinline__ void load(const TileArgs &p, const uint8_t *wbase,
+                                         const float *sbase, uint32_t rb, int st, uint32_t lds,
+                                         int lane) const
+    {
+        const uint32_t kb = min((uint32_t)st * 64 + piece, rb - 16);
+#pragma unroll
+        for (int i = 0; i < WL; i++) load_lds16(wbase, woff[i] + kb, lds + 1024 * i);
+        const uint32_t k32 = (uint32_t)st * (WS * TK / 32) + (lane % SG) * (FG / 32);
+        const uint32_t g = min(scale_group(k32, p.g32, p.gmagic), (uint32_t)p.a.ng - 1);
+#pragma unroll
+        for (int i = 0; i < SL; i++)
+            load_lds4(sbase, (soff[i] + g) * 4, lds + WBYTES + 256 * i);
+    }
+    // The lane's fragments and scales of K step `half` of the stage at `at`.
+    static __device__ __forceinline__ void unpack(const char *at, int half, int lane,
+                                                  f16x8 (&bv)[NB][2], float (&sc)[NB][NS])
+    {
+        const int li = lane & 15, lg = lane >> 4;
+        const float *const sl = reinterpret_cast<const float *>(at + WBYTES) + half * NS;
+        const char *row = at + li * 64;
+        if (FMT == FMT_FP8) row += (lg ^ key(li)) * 16;
+        else if (FG == 64) row += (((lg >> 1) ^ key(li) ^ (half * 2)) * 16) + (lg & 1) * 8;
+        else row += ((key(li) ^ (half * 2)) * 16) + lg * 4;
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            const char *const r = row + n * 1024;
+            if constexpr (FMT == FMT_FP8) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(r);
+                bv[n][0] = fp8x8_f16(v.x, v.y);
+                bv[n][1] = fp8x8_f16(v.z, v.w);
+            } else if constexpr (FG == 64) {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(r);
+                bv[n][0] = nib8_f16(v.x);
+                bv[n][1] = nib8_f16(v.y);
+            } else {
+                // the other 16 bytes of the K step: piece ^ 1
+                const char *const o = at + ((r - at) ^ 16);
+                bv[n][0] = nib8_f16(*reinterpret_cast<const uint32_t *>(r));
+                bv[n][1] = nib8_f16(*reinterpret_cast<const uint32_t *>(o));
+            }
+#pragma unroll
+            for (int j = 0; j < NS; j++) sc[n][j] = sl[(n * 16 + li) * SG + j];
+        }
+    }
 };
 
 // One K step of a wave: 16 MF rows of x (packed in LDS at sm, NP planes of 8
@@ -359,18 +432,17 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     constexpr int PT = CH / 256;                         // per thread
     static_assert(CH % 256 == 0, "whole chunks per thread");
     constexpr int LDO = TN + 4;                          // epilogue row stride, floats
-    constexpr int WB = FMT == FMT_FP8 ? 64 : 32;         // bytes of a row and step
-    constexpr int WD = WB / 16;                          // 16-byte pieces per lane and step
+    typedef Weights<FMT, FG, 64> W;
     constexpr int NS = TK / FG;                          // scales per row and step
-    // a stage of LDS: activations, weights, scales of one K step
-    constexpr uint32_t XB = NP * CH * 16, WO = XB, SO = WO + TN * WB, STAGE = SO + TN * NS * 4;
-    // stages, so that two workgroups share the 160 KB of a CU's LDS: two steps
-    // of loads in flight for int4, one for fp8's larger steps (three stages
-    // and one workgroup per CU: 28 % slower at 2048 x 8192 x 8192)
-    constexpr int ST = FMT == FMT_FP8 ? 2 : 3;
+    // LDS: AST stages of one K step of activations, two of each wave's weights.
+    // Two workgroups share the 160 KB of a CU (one workgroup with more steps of
+    // loads in flight: 28 % slower for fp8 at 2048 x 8192 x 8192); where the
+    // activations are small, two steps of them are in flight.
+    constexpr int AST = MF * NP >= 8 || FMT == FMT_FP8 ? 2 : 3;
+    constexpr uint32_t XB = NP * CH * 16, WO = AST * XB, LDS = WO + 8 * W::BYTES;
     constexpr int EP = MF % 4 == 0 ? 4 : MF % 3 == 0 ? 3 : MF;   // row blocks of an epilogue pass
     constexpr uint32_t OS = EP * 16 * LDO * sizeof(float);
-    __shared__ __align__(16) char smem[ST * STAGE > OS ? ST * STAGE : OS];
+    __shared__ __align__(16) char smem[LDS > OS ? LDS : OS];
     __shared__ int rx[BM];
     const LinearArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -421,28 +493,16 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
         aoff[i] = ((uint32_t)r * (uint32_t)p.ldp + ((c & 7) ^ swizzle(row)) * 8) * 2;
     }
 
-    // weight rows of this lane
-    const size_t rb = FMT == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
+    const uint32_t rb = FMT == FMT_I4G ? (uint32_t)a.I / 2 : (uint32_t)a.I;
     const uint8_t *const wbase = a.w + (size_t)t.expert * a.w_stride;
     const float *const sbase = a.scales + (size_t)t.expert * a.s_stride;
     constexpr int CW = GATED ? 32 : 64;                  // columns of y per wave
-    // row i of the wave's 64 (block i / 16 of n)
-    auto weight_row = [&](int i) {
+    W w;
+    w.init(a, rb, lane, [&](int i) {                     // block i / 16 of the wave's rows
         const int n = i >> 4;
         const int c = nt * (4 * CW) + wave * CW + (GATED ? n & 1 : n) * 16 + (i & 15);
         return (c < oc ? c : oc - 1) + (GATED && n >= 2 ? oc : 0);
-    };
-    uint32_t woff[WD];                                   // lanes of a row next to each other
-#pragma unroll
-    for (int i = 0; i < WD; i++)
-        woff[i] = (uint32_t)(weight_row((lane + 64 * i) / WD) * rb);
-    const uint32_t lane_b = (lane % WD) * 16;
-    uint32_t soff[NS];
-#pragma unroll
-    for (int j = 0; j < NS; j++) {
-        const int row = weight_row((lane + 64 * j) / NS);
-        soff[j] = (uint32_t)(FMT == FMT_I4G ? row : row >> 7) * (uint32_t)a.ng;
-    }
+    });
 
     f32x4v acc[MF][4];
 #pragma unroll
@@ -454,71 +514,56 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     // in a dense product, the tile's own in a grouped one
     const int mf = RAGGED ? __builtin_amdgcn_readfirstlane((t.n + 15) / 16) : MF;
     const int na = RAGGED ? __builtin_amdgcn_readfirstlane((t.n + 31) / 32) : PT;
-    const int gs = FMT == FMT_FP8 ? 128 : a.gs;
-    uint32_t group = 0;                                  // scale group of the next load
-    int done = 0;                                        // its columns already loaded
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem);
+    const int steps = p.Ip / TK;
 
-    // Loads of one step into a stage.  Past the last step they repeat it; in a
-    // last half step (I % 64 == 32) the lanes behind the row's end read its
-    // last bytes again, which meet zeros of x.
-    constexpr int WLOADS = WD + NS;                      // per wave, and NP na of x
-    auto load = [&](int k0, int stage) {
-        k0 = min(k0, p.Ip - TK);
-        const uint32_t at = lds0 + stage * STAGE;
+    // Loads of a step past the last repeat it.
+    auto load_x = [&](int s, int stage) {
+        const int k0 = min(s, steps - 1) * TK;
 #pragma unroll
         for (int q = 0; q < NP; q++)
 #pragma unroll
             for (int i = 0; i < PT; i++)
                 if (!RAGGED || i < na)
                     load_lds16((q ? p.lo : p.hi) + k0, aoff[i],
-                               at + (q * CH + wave * 64 + 256 * i) * 16);
-        const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? k0 / 2 : k0) + lane_b,
-                                (uint32_t)rb - 16);
-#pragma unroll
-        for (int i = 0; i < WD; i++)
-            load_lds16(wbase, woff[i] + kb, at + WO + wave * (64 * WB) + 1024 * i);
-        // lane: row (lane + 64 j) / NS of the wave's, group lane % NS
-        uint32_t gl = 0;
-#pragma unroll
-        for (int j = 0; j < NS; j++) {
-            gl = j == 0 || (lane & 1) ? group : gl;
-            done += FG;
-            group += done == gs;
-            done = done == gs ? 0 : done;
-        }
-        gl = min(gl, (uint32_t)a.ng - 1);
-#pragma unroll
-        for (int j = 0; j < NS; j++)
-            load_lds4(sbase, (soff[j] + gl) * 4, at + SO + wave * (256 * NS) + 256 * j);
+                               lds0 + stage * XB + (q * CH + wave * 64 + 256 * i) * 16);
+    };
+    auto load_w = [&](int st) {
+        w.load(p, wbase, sbase, rb, st, lds0 + WO + ((st & 1) * 4 + wave) * W::BYTES, lane);
     };
 
     __syncthreads();                                     // rx; earlier loads are done
-#pragma unroll
-    for (int i = 0; i < ST - 1; i++) load(i * TK, i);
+    load_x(0, 0);
+    load_w(0);
+    if (AST == 3) load_x(1, 1);
     int stage = 0;
-    for (int k0 = 0; k0 < p.Ip; k0 += TK) {
-        // this step's stage is there; the one that the last step read is free
-        constexpr int LATER = ST - 2;                    // steps that may be outstanding
-        if (PT >= 4 && na == 4) wait_loads<LATER * (NP * 4 + WLOADS)>();
-        else if (PT >= 3 && na == 3) wait_loads<LATER * (NP * 3 + WLOADS)>();
-        else if (PT >= 2 && na == 2) wait_loads<LATER * (NP * 2 + WLOADS)>();
-        else wait_loads<LATER * (NP + WLOADS)>();
-        load(k0 + (ST - 1) * TK, stage == 0 ? ST - 1 : stage - 1);
-        const char *const sm = smem + stage * STAGE;
-        const char *const wl = sm + WO + wave * (64 * WB);
-        const float *const sl = reinterpret_cast<const float *>(sm + SO) + wave * (64 * NS);
+    for (int s = 0; s < steps; s++) {
+        // This step's data is there, and the stages that the last one read are
+        // free.  Later loads may be on their way: one step of x (AST == 3), and
+        // in a weight stage's second step the next one.
+        const int half = s % W::WS;
+        const int later = (AST == 3 ? na : 0) + (half ? 8 : 0);
+        switch (later) {
+        case 0: wait_loads<0>(); break;
+        case 1: wait_loads<NP>(); break;
+        case 2: wait_loads<2 * NP>(); break;
+        case 3: wait_loads<3 * NP>(); break;
+        case 8: wait_loads<W::LOADS>(); break;
+        case 9: wait_loads<NP + W::LOADS>(); break;
+        case 10: wait_loads<2 * NP + W::LOADS>(); break;
+        default: wait_loads<3 * NP + W::LOADS>(); break;
+        }
+        // (fp8's next weights are due a step before the x asked for here)
+        if (W::WS == 1) load_w(s + 1);
+        load_x(s + AST - 1, stage == 0 ? AST - 1 : stage - 1);
+        if (W::WS == 2 && half == 0) load_w(s / 2 + 1);
+        const char *const sm = smem + stage * XB;
         f16x8 bv[4][2];
         float sc[4][NS];
-#pragma unroll
-        for (int n = 0; n < 4; n++) {
-            unpack<FMT, FG>(wl + (n * 16 + li) * WB, lg, bv[n]);
-#pragma unroll
-            for (int j = 0; j < NS; j++) sc[n][j] = sl[(n * 16 + li) * NS + j];
-        }
+        W::unpack(smem + WO + (((s / W::WS) & 1) * 4 + wave) * W::BYTES, half, lane, bv, sc);
         multiply_step<NP, MF, 4, FG, RAGGED>(acc, bv, sc, sm, lane, mf);
-        stage = stage == ST - 1 ? 0 : stage + 1;
+        stage = stage == AST - 1 ? 0 : stage + 1;
     }
     // loads past the last step still write LDS
     wait_loads<0>();
@@ -566,21 +611,17 @@ __device__ __forceinline__ void wait_own_loads()
 // its own, so the K loop needs no barrier, and their sums are joined through
 // LDS in a fixed order.  At 64 x 6144 x 12288 bf16 the tile kernel has 48
 // workgroups for 256 CUs and takes 89 us.
-template <int FMT, typename XT, int NP, int MB, int NB, bool GATED, int FG, bool RAGGED, int KW,
-          int ST>
+template <int FMT, typename XT, int NP, int MB, bool GATED, int FG, bool RAGGED, int KW, int AST>
 __global__ __launch_bounds__(KW * 64, KW / 4) void linear_narrow(TileArgs p)
 {
-    constexpr int NS = TK / FG;
-    constexpr int WB = FMT == FMT_FP8 ? 64 : 32;         // bytes of a row and step
-    constexpr int WD = WB / 16;                          // 16-byte pieces of it
-    constexpr int WL = NB * 16 * WD / 64;                // loads per lane and step
-    constexpr int AL = MB * 2;                           // per plane
-    constexpr int SL = (NB * 16 * NS + 63) / 64;
+    typedef Weights<FMT, FG, 64> W;
+    constexpr int NB = 4, NS = TK / FG;
+    constexpr int AL = MB * 2;                           // loads of x per plane and step
     constexpr int CH = MB * 16 * 8;                      // 16-byte chunks of a plane
-    constexpr uint32_t WO = NP * CH * 16, SO = WO + WL * 1024, STAGE = SO + SL * 256;
+    constexpr uint32_t XB = NP * CH * 16, WO = AST * XB, OWN = WO + 2 * W::BYTES;
     constexpr int LDR = NB * 16 + 4;
     constexpr uint32_t RED = KW * MB * 16 * LDR * 4;
-    __shared__ __align__(16) char smem[KW * ST * STAGE > RED ? KW * ST * STAGE : RED];
+    __shared__ __align__(16) char smem[KW * OWN > RED ? KW * OWN : RED];
     const LinearArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -607,49 +648,38 @@ __global__ __launch_bounds__(KW * 64, KW / 4) void linear_narrow(TileArgs p)
         }
         aoff[i] = ((uint32_t)r * (uint32_t)p.ldp + ((c & 7) ^ swizzle(row & 15)) * 8) * 2;
     }
-    const size_t rb = FMT == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
+    const uint32_t rb = FMT == FMT_I4G ? (uint32_t)a.I / 2 : (uint32_t)a.I;
     const uint8_t *const wbase = a.w + (size_t)t.expert * a.w_stride;
     const float *const sbase = a.scales + (size_t)t.expert * a.s_stride;
-    auto weight_row = [&](int i) {
+    W w;
+    w.init(a, rb, lane, [&](int i) {
         const int n = i >> 4;
         const int half = GATED ? n / (NB / 2) : 0;
         const int c = nt * YC + (GATED ? n % (NB / 2) : n) * 16 + (i & 15);
         return (c < oc ? c : oc - 1) + half * oc;
-    };
-    uint32_t woff[WL], soff[SL];
-#pragma unroll
-    for (int i = 0; i < WL; i++) woff[i] = (uint32_t)(weight_row((lane + 64 * i) / WD) * rb);
-#pragma unroll
-    for (int i = 0; i < SL; i++) {
-        const int row = weight_row(min((lane + 64 * i) / NS, NB * 16 - 1));
-        soff[i] = (uint32_t)(FMT == FMT_I4G ? row : row >> 7) * (uint32_t)a.ng;
-    }
-    const uint32_t lane_b = (lane % WD) * 16;
+    });
     const int mf = __builtin_amdgcn_readfirstlane((t.n + 15) / 16);
-    const uint32_t gs = FMT == FMT_FP8 ? 128 : a.gs;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
-        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem) +
-        wave * (ST * STAGE);
-    const char *const own = smem + wave * (ST * STAGE);
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem) + wave * OWN;
+    const char *const own = smem + wave * OWN;
     const int steps = p.Ip / TK;
+    const int stages = (steps + W::WS - 1) / W::WS;      // of weights
 
-    // as the tile kernel's; a step past the last repeats it
-    constexpr int LOADS = NP * AL + WL + SL;
-    auto load = [&](int s, int stage) {
+    // The wave's i-th step is step i % WS of weight stage wave + KW (i / WS);
+    // loads past the last repeat it.
+    auto load_x = [&](int i, int stage) {
+        const int s = (wave + KW * (i / W::WS)) * W::WS + i % W::WS;
         const int k0 = min(s, steps - 1) * TK;
-        const uint32_t at = lds0 + stage * STAGE;
 #pragma unroll
         for (int q = 0; q < NP; q++)
 #pragma unroll
-            for (int i = 0; i < AL; i++)
-                load_lds16((q ? p.lo : p.hi) + k0, aoff[i], at + q * (CH * 16) + 1024 * i);
-        const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? k0 / 2 : k0) + lane_b,
-                                (uint32_t)rb - 16);
-#pragma unroll
-        for (int i = 0; i < WL; i++) load_lds16(wbase, woff[i] + kb, at + WO + 1024 * i);
-        const uint32_t gi = (uint32_t)min(k0 + (lane % NS) * FG, a.I - 1) / gs;
-#pragma unroll
-        for (int i = 0; i < SL; i++) load_lds4(sbase, (soff[i] + gi) * 4, at + SO + 256 * i);
+            for (int j = 0; j < AL; j++)
+                load_lds16((q ? p.lo : p.hi) + k0, aoff[j],
+                           lds0 + stage * XB + q * (CH * 16) + 1024 * j);
+    };
+    auto load_w = [&](int i) {                           // the wave's i-th weight stage
+        const int st = min(wave + KW * i, stages - 1);
+        w.load(p, wbase, sbase, rb, st, lds0 + WO + (i & 1) * W::BYTES, lane);
     };
 
     f32x4v acc[MB][NB];
@@ -659,24 +689,28 @@ __global__ __launch_bounds__(KW * 64, KW / 4) void linear_narrow(TileArgs p)
         for (int n = 0; n < NB; n++) acc[m][n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 
     __builtin_amdgcn_s_waitcnt(QG_WAIT_VM0);             // earlier loads are done
-#pragma unroll
-    for (int i = 0; i < ST - 1; i++) load(wave + i * KW, i);
+    load_x(0, 0);
+    load_w(0);
+    if (AST == 3) load_x(1, 1);
+    // a stage behind the last step of a last half stage has zero steps
+    const int mine = wave < stages ? (stages - 1 - wave) / KW + 1 : 0;
+    const int last = (stages - 1) % KW == wave ? steps - (stages - 1) * W::WS : W::WS;
+    const int count = mine ? (mine - 1) * W::WS + last : 0;
     int stage = 0;
-    for (int s = wave; s < steps; s += KW) {
-        wait_own_loads<(ST - 2) * LOADS>();
-        load(s + (ST - 1) * KW, stage == 0 ? ST - 1 : stage - 1);
-        const char *const sm = own + stage * STAGE;
-        const float *const sl = reinterpret_cast<const float *>(sm + SO);
+    for (int i = 0; i < count; i++) {
+        // as the tile kernel's
+        const int half = i % W::WS;
+        constexpr int XLATER = AST == 3 ? NP * AL : 0;
+        if (half) wait_own_loads<XLATER + W::LOADS>();
+        else wait_own_loads<XLATER>();
+        if (W::WS == 1) load_w(i + 1);
+        load_x(i + AST - 1, stage == 0 ? AST - 1 : stage - 1);
+        if (W::WS == 2 && half == 0) load_w(i / 2 + 1);
         f16x8 bv[NB][2];
         float sc[NB][NS];
-#pragma unroll
-        for (int n = 0; n < NB; n++) {
-            unpack<FMT, FG>(sm + WO + (n * 16 + li) * WB, lg, bv[n]);
-#pragma unroll
-            for (int j = 0; j < NS; j++) sc[n][j] = sl[(n * 16 + li) * NS + j];
-        }
-        multiply_step<NP, MB, NB, FG, RAGGED>(acc, bv, sc, sm, lane, mf);
-        stage = stage == ST - 1 ? 0 : stage + 1;
+        W::unpack(own + WO + ((i / W::WS) & 1) * W::BYTES, half, lane, bv, sc);
+        multiply_step<NP, MB, NB, FG, RAGGED>(acc, bv, sc, own + stage * XB, lane, mf);
+        stage = stage == AST - 1 ? 0 : stage + 1;
     }
     wait_own_loads<0>();                                 // loads past the last step
     __syncthreads();
@@ -738,14 +772,14 @@ hipError_t run_tile(const TileArgs &p, unsigned grid, hipStream_t st)
     }
     return hipGetLastError();
 }
-template <int FMT, typename XT, int MB, int NB>
+template <int FMT, typename XT, int MB>
 hipError_t run_narrow(const TileArgs &p, unsigned grid, hipStream_t st)
 {
     // 8 waves where their stages fit the 160 KB of LDS, else 4
     constexpr int NP = sizeof(typename XT::raw) == 4 ? 2 : 1;
-    constexpr int KW = FMT == FMT_I4G && NP * MB <= 2 ? 8 : 4, ST = 3;
+    constexpr int KW = NP * MB <= 2 ? 8 : 4, AST = KW == 8 ? 2 : 3;
 #define QG_RUN2(FG, G, R)                                                                   \
-    hipLaunchKernelGGL((linear_narrow<FMT, XT, NP, MB, NB, G, FG, R, KW, ST>), dim3(grid),  \
+    hipLaunchKernelGGL((linear_narrow<FMT, XT, NP, MB, G, FG, R, KW, AST>), dim3(grid),  \
                        dim3(KW * 64), 0, st, p)
 #define QG_RUN3(FG)                                                                         \
     do {                                                                                    \
@@ -798,6 +832,8 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int b
     p.a = a;
     p.Ip = padded(a.I);
     p.ldp = plane_stride(a.I);
+    p.g32 = (uint32_t)a.gs / 32;
+    p.gmagic = 0xFFFFFFFFu / p.g32;
     char *at = static_cast<char *>(ws);
     int *rexp = reinterpret_cast<int *>(at);
     at += align256((size_t)a.T * sizeof(int));
@@ -824,8 +860,8 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int b
          : (a.dtype == QGEMV_BF16 ? run_tile<FMT_FP8, BF16, MF>(p, (unsigned)grid, st)      \
                                   : run_tile<FMT_FP8, F32, MF>(p, (unsigned)grid, st)))
 #define QG_NARROW(XT, MB)                                                                   \
-    (fmt == FMT_I4G ? run_narrow<FMT_I4G, XT, MB, 4>(p, (unsigned)grid, st)                  \
-                    : run_narrow<FMT_FP8, XT, MB, 4>(p, (unsigned)grid, st))
+    (fmt == FMT_I4G ? run_narrow<FMT_I4G, XT, MB>(p, (unsigned)grid, st)                  \
+                    : run_narrow<FMT_FP8, XT, MB>(p, (unsigned)grid, st))
     if (narrow) {
         if (a.dtype != QGEMV_BF16) return QG_NARROW(F32, 2);
         return bm == 64 ? QG_NARROW(BF16, 4) : QG_NARROW(BF16, 2);
