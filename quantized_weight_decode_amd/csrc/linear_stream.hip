@@ -420,7 +420,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
 template <int FMT, typename XT, int NB, bool GATED>
 void run_nb(const StreamArgs &p, unsigned grid, hipStream_t st)
 {
-    constexpr int P = FMT == FMT_I4G || NB <= 2 ? 2 : 1;
+    constexpr int P = FMT == FMT_I4G ? 2 : 1;
 #define QG_RUN(FG)                                                                          \
     hipLaunchKernelGGL((linear_stream<FMT, XT, NB, GATED, FG, P>), dim3(grid), dim3(SW * 64), 0, \
                        st, p)
