@@ -203,6 +203,7 @@ __global__ __launch_bounds__(256) void linear_general(LinearArgs a,
                 for (int c = 0; c < 8; c++) ws[(p * GN + sr + 16 * i) * GLD + sc + c] = w[c];
             }
         if (!FEW) __syncthreads();
+        else __builtin_amdgcn_wave_barrier();            // lanes read each other's values
         if (k0 + STEP < a.I) load(k0 + STEP);
 #pragma unroll
         for (int kk = 0; kk < GK; kk += 4) {
@@ -327,8 +328,9 @@ long long max_tiles(int R, int E, int bm)
 // tile per CU, 200 with two, 323 with three); f32 counts two planes.  What the
 // rule decides, us with the tile chosen and with the next best: 256 x 12288:
 // 64 x 256 89, narrow 93, 128 x 256 125; 512 x 12288: 128 x 256 126, 64 x 256
-// 139; 512 x 4096 (4096 columns): narrow 49, 32 x 256 53, 128 x 256 95; f32
-// 333 x 11008 (4096 columns): 32 x 256 97, 64 x 256 117.  Grouped tiles know
+// 139; 700 x 12288: 96 x 256 164, 128 x 256 188; 512 x 4096 (4096 columns):
+// narrow 49, 64 x 256 65; f32 333 x 11008 (4096 columns): 32 x 256 97, 64 x
+// 256 117.  Grouped tiles know
 // neither their count (estimated with half a tile per expert) nor their
 // filling, and skip what they lack: only the largest of each kind.
 void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
@@ -341,14 +343,13 @@ void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
     static const Kind bf16[] = {{128, false, true, 1.0},
                                 {96, false, false, 0.83},
                                 {64, false, false, 0.66},
-                                {32, false, false, 0.58},
                                 {64, true, true, 0.265},
                                 {32, true, false, 0.185}};
     static const Kind f32[] = {{64, false, true, 0.93}, {32, false, false, 0.69},
                                {32, true, true, 0.26}};
     const bool half = a.dtype == QGEMV_BF16;
     const Kind *kinds = half ? bf16 : f32;
-    const int n = half ? 6 : 3;
+    const int n = half ? 5 : 3;
     const long long ncu = cu_count();
     double best = -1.0;
     for (int i = 0; i < n; i++) {
@@ -396,16 +397,38 @@ void run_general(const LinearArgs &a, bool few, const RowTile *tiles, unsigned g
 size_t linear_workspace(int T, int R, int E, int I, int O, int dtype)
 {
     (void)O;
+    const int slice = tile_rows(I);
     return (E > 0 ? align256((size_t)max_tiles(R, E, 16) * sizeof(RowTile)) : 0) +
-           tile_workspace(T, I, dtype);
+           tile_workspace(E > 0 || T < slice ? T : slice, I, dtype);
 }
 
-hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStream_t st)
+hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hipStream_t st)
 {
+    LinearArgs a = args;
     const int oc = a.gated ? a.O / 2 : a.O;
+    // a dense product's packed activations must lie within 4 GB: slices of rows
+    const int slice = tile_rows(a.I);
+    if (!a.offsets && a.R > slice) {
+        const size_t el = a.dtype == QGEMV_BF16 ? 2 : 4;
+        for (int r = 0; r < args.R; r += slice) {
+            a.T = a.R = args.R - r < slice ? args.R - r : slice;
+            a.x = static_cast<const char *>(args.x) + (size_t)r * a.ldx * el;
+            a.y = static_cast<char *>(args.y) + (size_t)r * a.ldy * el;
+            if (args.residual)
+                a.residual = static_cast<const char *>(args.residual) + (size_t)r * a.ldr * el;
+            const hipError_t e = launch_linear(fmt, a, ws, st);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
     const bool fits = tile_fits(fmt, a);
     const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
-    const bool stream = rows <= 16 && stream_fits(fmt, a);
+    // Stream up to 16 rows; grouped by the rows an expert has on average.
+    // 7168 x 2048, 256 experts, bf16: 320 tokens (10 rows) stream 578 us, tiles
+    // 696; 512 (16) 767 and 762; 768 (24) 1000 and 802.  f32: 192 tokens (6
+    // rows) 706 and 683, 512 tokens 1223 and 849.
+    const int few_rows = a.offsets && a.dtype == QGEMV_F32 ? 6 : 16;
+    const bool stream = rows <= few_rows && stream_fits(fmt, a);
     // the general kernel's tiles: 16 rows also where 64-row tiles would leave
     // CUs without one (64 x 6001 x 12288 bf16: 135 us, 227 us in 192 tiles of
     // 64 rows)

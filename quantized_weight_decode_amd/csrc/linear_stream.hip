@@ -270,7 +270,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     const int gs = FMT == FMT_FP8 ? 128 : a.gs;
     const int nx = (t.n + XR - 1) / XR;                  // loads of x that hold rows
     // Past the last block, and for a lane behind the row's end, loads repeat
-    // valid data, which meets zeros of x.
+    // valid data (of x, the row's first piece), which meets zeros of x.
     auto load_w = [&](int c) {
         const int k0 = min(c, blocks - 1) * (P * SC);
         const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? (k0 + lane_k) / 2 : k0 + lane_k),
@@ -288,7 +288,8 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     auto load_x = [&](int c) {
 #pragma unroll
         for (int q = 0; q < P; q++) {
-            const int kx = x_inside(c, q) ? (c * P + q) * SC : 0;
+            const int kx =
+                x_inside(c, q) ? (c * P + q) * SC : -(lane % XP) * (int)(16 / sizeof(raw));
 #pragma unroll
             for (int i = 0; i < XL; i++)
                 if (i < nx) xr[q][i] = *reinterpret_cast<const u32x4 *>(xp[i] + kx);
@@ -385,7 +386,10 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < P; q++) {
-            if (q > 0) store_x(c, q);
+            if (q > 0) {
+                store_x(c, q);
+                __builtin_amdgcn_wave_barrier();         // lanes read each other's pieces
+            }
             if (q == P - 1) load_x(c + SW);
             multiply(q);
             __builtin_amdgcn_sched_barrier(0);

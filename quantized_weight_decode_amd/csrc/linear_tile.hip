@@ -817,6 +817,12 @@ size_t tile_workspace(int T, int I, int dtype)
            align256((size_t)T * plane_stride(I) * 2) * (dtype == QGEMV_BF16 ? 1 : 2);
 }
 
+int tile_rows(int I)
+{
+    const size_t n = ((1ull << 32) - 1) / ((size_t)plane_stride(I) * 2) / 128 * 128;
+    return n > (1 << 24) ? 1 << 24 : n < 128 ? 128 : (int)n;
+}
+
 bool tile_fits(WeightFormat fmt, const LinearArgs &a)
 {
     const size_t rb = fmt == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
@@ -853,30 +859,19 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int b
     const hipError_t e = a.dtype == QGEMV_BF16 ? pack<BF16>(fmt, a, p.Ip, p.ldp, hi, lo, rexp, st)
                                                : pack<F32>(fmt, a, p.Ip, p.ldp, hi, lo, rexp, st);
     if (e != hipSuccess) return e;
-#define QG_TILE(MF)                                                                         \
-    (fmt == FMT_I4G                                                                         \
-         ? (a.dtype == QGEMV_BF16 ? run_tile<FMT_I4G, BF16, MF>(p, (unsigned)grid, st)      \
-                                  : run_tile<FMT_I4G, F32, MF>(p, (unsigned)grid, st))      \
-         : (a.dtype == QGEMV_BF16 ? run_tile<FMT_FP8, BF16, MF>(p, (unsigned)grid, st)      \
-                                  : run_tile<FMT_FP8, F32, MF>(p, (unsigned)grid, st)))
+#define QG_TILE(XT, MF)                                                                     \
+    (fmt == FMT_I4G ? run_tile<FMT_I4G, XT, MF>(p, (unsigned)grid, st)                      \
+                    : run_tile<FMT_FP8, XT, MF>(p, (unsigned)grid, st))
 #define QG_NARROW(XT, MB)                                                                   \
-    (fmt == FMT_I4G ? run_narrow<FMT_I4G, XT, MB>(p, (unsigned)grid, st)                  \
+    (fmt == FMT_I4G ? run_narrow<FMT_I4G, XT, MB>(p, (unsigned)grid, st)                    \
                     : run_narrow<FMT_FP8, XT, MB>(p, (unsigned)grid, st))
-    if (narrow) {
-        if (a.dtype != QGEMV_BF16) return QG_NARROW(F32, 2);
-        return bm == 64 ? QG_NARROW(BF16, 4) : QG_NARROW(BF16, 2);
+    if (a.dtype == QGEMV_F32) {
+        if (narrow) return QG_NARROW(F32, 2);
+        return bm == 64 ? QG_TILE(F32, 4) : QG_TILE(F32, 2);
     }
+    if (narrow) return bm == 64 ? QG_NARROW(BF16, 4) : QG_NARROW(BF16, 2);
+    return bm == 128 ? QG_TILE(BF16, 8) : bm == 96 ? QG_TILE(BF16, 6) : QG_TILE(BF16, 4);
 #undef QG_NARROW
-    switch (bm) {
-    case 128:                                            // bf16 only
-        return fmt == FMT_I4G ? run_tile<FMT_I4G, BF16, 8>(p, (unsigned)grid, st)
-                              : run_tile<FMT_FP8, BF16, 8>(p, (unsigned)grid, st);
-    case 96:                                             // bf16 only
-        return fmt == FMT_I4G ? run_tile<FMT_I4G, BF16, 6>(p, (unsigned)grid, st)
-                              : run_tile<FMT_FP8, BF16, 6>(p, (unsigned)grid, st);
-    case 64: return QG_TILE(4);
-    default: return QG_TILE(2);
-    }
 #undef QG_TILE
 }
 

@@ -35,11 +35,12 @@ size_t linear_workspace(int T, int R, int E, int I, int O, int dtype);
 hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStream_t st);
 
 // The f16 tile kernels (linear_tile.hip): shapes they take, workspace, launch
-// with row tiles of bm in {32, 64, 96, 128} (narrow: {32, 64}); tiles == nullptr:
-// dense.
+// with row tiles of bm: bf16 64, 96 or 128 (narrow 32 or 64), f32 32 or 64
+// (narrow 32); tiles == nullptr: dense.
 struct RowTile;
 bool tile_fits(WeightFormat fmt, const LinearArgs &a);
 size_t tile_workspace(int T, int I, int dtype);
+int tile_rows(int I);                    // rows whose packed plane stays below 4 GB
 hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int bm,
                        const RowTile *tiles, int ntm, void *ws, hipStream_t st);
 

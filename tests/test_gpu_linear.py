@@ -240,3 +240,61 @@ def test_misaligned_weights(q):
             x = L.acts(S, I, torch.bfloat16, 22)
             ref, bound = L.reference(L.decode_int4(w, s, I, gs), x, torch.bfloat16)
             L.assert_within(q.i4g_linear(v, dev(s), x.cuda(), gs), ref, bound)
+
+
+
+
+# products large enough for the wide tiles: 128, 96 and 64 rows (bf16), 64 and
+# 32 rows (f32); half K steps (I % 64 == 32), scale groups of 32, 64 and 96
+@pytest.mark.parametrize("fmt", ["i4g", "fp8"])
+@pytest.mark.parametrize("S,O,dtype", [(2000, 4000, torch.bfloat16), (2060, 4100, torch.bfloat16),
+                                       (900, 4000, torch.bfloat16), (1000, 4000, torch.float32),
+                                       (500, 4000, torch.float32)])
+@pytest.mark.parametrize("I,gs,gated", [(160, 32, False), (256, 64, True), (96, 96, False),
+                                        (32, 32, True), (448, 64, False)])
+def test_wide_tiles(q, fmt, S, O, dtype, I, gs, gated):
+    k = {"act": "silu", "gated": True, "bias": True, "residual": True} if gated else {}
+    y, ref, bound = _run(q, fmt, S, I, O, gs, dtype, seed=S + I, **k)
+    L.assert_within(y, ref, bound)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("outlier", [1e4, 1e6])
+@pytest.mark.parametrize("S", [2, 20, 60, 200])
+def test_outlier_on_a_zero_weight_column(q, S, outlier, dtype):
+    """A column whose weights are all zero takes a large activation: its size
+    must not cost the other columns their bits (f32: relative L2 1e-5)."""
+    I, O, gs = 2048, 256, 64
+    w, s = L.int4((O,), I, gs, 30)
+    w[:, 100] = 0x88                                 # q = 8, columns 200 and 201
+    W = L.decode_int4(w, s, I, gs)
+    x = L.acts(S, I, dtype, 31)
+    x[:, 200] = outlier
+    y = q.i4g_linear(dev(w), dev(s), x.cuda(), gs)
+    ref, bound = L.reference(W, x, dtype)
+    if dtype == torch.float32:
+        assert L.rel_l2(y, ref) <= 1e-5
+    else:
+        # bf16's rounding and the outlier's share of the offset form: two
+        # roundings of 24 |x| s per scale group
+        extra = 2 * L.U * 48 * outlier * 0.02
+        L.assert_within(y, ref, bound + extra)
+
+
+def test_more_activations_than_one_slice(q):
+    """Rows whose packed form exceeds 4 GB run in slices: rows on both sides of
+    the cut against the same rows alone."""
+    I, O, S, gs = 1 << 20, 64, 2100, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    w = torch.randint(0, 256, (O, I // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s = 0.002 + 0.018 * torch.rand((O, I // gs), device="cuda", generator=g)
+    x = torch.randn((S, I), dtype=torch.bfloat16, device="cuda", generator=g)
+    r = torch.randn((S, O), dtype=torch.bfloat16, device="cuda", generator=g)
+    y = q.i4g_linear(w, s, x, gs, residual=r)
+    for lo in (0, 1900, 2070):
+        part = q.i4g_linear(w, s, x[lo:lo + 30], gs, residual=r[lo:lo + 30])
+        # the same exact products in other orders: 2^20 of rms 5 * 0.012 in f32
+        # sums, one bf16 rounding each
+        d = (part.double() - y[lo:lo + 30].double()).abs()
+        assert float((d / (2.0 ** -7 * y[lo:lo + 30].double().abs() + 0.05)).max()) <= 1.0

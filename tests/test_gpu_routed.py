@@ -283,3 +283,30 @@ def test_routed_mlp_captured_and_replayed(q, T):
         want = step(xin, lin)
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("I,gs,gated", [(160, 32, False), (128, 64, True)])
+def test_grouped_wide_tiles(q, I, gs, gated, dtype):
+    """Enough rows for the wide tiles, the experts' rows filling them to every
+    sixteenth."""
+    counts = [1500, 7, 0, 16, 2000, 33, 100, 344, 49, 65, 81, 113]
+    E, R, O = len(counts), sum(counts), 4096
+    w, s = L.int4((E, O), I, gs, 40)
+    off = counts_offsets(counts)
+    r = np.random.default_rng(2)
+    T = 600
+    x = L.acts(T, I, dtype, 41)
+    rows = r.integers(0, T, R).astype(np.int32)
+    rows[10], rows[1507 + 3] = -1, T                 # experts 0 and 3
+    y = q.i4g_grouped(dev(w), dev(s), x.cuda(), dev(off), gs, rows=dev(rows),
+                      act="silu" if gated else None, gated=gated)
+    bad = [10, 1507 + 3]
+    assert bool(torch.isnan(y[bad]).all())
+    for e in range(E):
+        keep = [i for i in range(off[e], off[e + 1]) if i not in bad]
+        if keep:
+            ref, bound = L.reference(L.decode_int4(w[e], s[e], I, gs),
+                                     x[torch.from_numpy(rows[keep]).long()], dtype,
+                                     act="silu" if gated else None, gated=gated)
+            L.assert_within(y[keep], ref, bound, f"expert {e}")
