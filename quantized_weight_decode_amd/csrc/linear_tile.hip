@@ -450,19 +450,26 @@ __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
     const int li = lane & 15, lg = lane >> 4;
     const int oc = GATED ? a.O / 2 : a.O;
 
-    // consecutive tiles go to one XCD (workgroups are dealt to the 8 in turn)
-    const int nb = gridDim.x, q8 = nb / 8, r8 = nb % 8;
-    const int xcd = blockIdx.x % 8, in = blockIdx.x / 8;
-    const int b = xcd * q8 + min(xcd, r8) + in;
+    // Workgroups are dealt to the 8 XCDs in turn.
     int mt, nt;
     RowTile t;
-    if (p.tiles) {                                       // an expert's columns together
-        mt = b / p.ntn;
-        nt = b % p.ntn;
+    if (RAGGED) {
+        // A row tile's columns together on one XCD (they share its x), tiles
+        // dealt out one by one: the empty ones at the list's end, of unknown
+        // number, must not leave one XCD without work.
+        const int xcd = blockIdx.x % 8, in = blockIdx.x / 8;
+        mt = in / p.ntn * 8 + xcd;
+        nt = in % p.ntn;
+        if (mt >= p.ntm) return;
         t = p.tiles[mt];
         t.expert = __builtin_amdgcn_readfirstlane(t.expert);
         if (t.n <= 0) return;
-    } else {                                             // a column block's rows together
+    } else {
+        // Consecutive tiles to one XCD, a column block's rows together (they
+        // share its weights).
+        const int nb = gridDim.x, q8 = nb / 8, r8 = nb % 8;
+        const int xcd = blockIdx.x % 8, in = blockIdx.x / 8;
+        const int b = xcd * q8 + min(xcd, r8) + in;
         nt = b / p.ntm;
         mt = b % p.ntm;
         t = RowTile{0, mt * BM, min(BM, a.R - mt * BM), 0};
@@ -854,7 +861,8 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int b
     const int tn = narrow ? 64 : TN;
     const int cols = a.gated ? tn / 2 : tn, oc = a.gated ? a.O / 2 : a.O;
     p.ntn = (oc + cols - 1) / cols;
-    const long long grid = (long long)ntm * p.ntn;
+    // the grouped tile kernel deals row tiles by eights
+    const long long grid = (long long)(tiles && !narrow ? (ntm + 7) / 8 * 8 : ntm) * p.ntn;
     if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     const hipError_t e = a.dtype == QGEMV_BF16 ? pack<BF16>(fmt, a, p.Ip, p.ldp, hi, lo, rexp, st)
                                                : pack<F32>(fmt, a, p.Ip, p.ldp, hi, lo, rexp, st);
