@@ -264,53 +264,83 @@ __global__ __launch_bounds__(256) void linear_general(LinearArgs a,
 }
 
 // Row tiles of a grouped product, from the experts' offsets on the device:
-// tile i of the list is the i-th block of bm rows, experts in ascending
-// order; the rest of the list is empty.  Offsets are clamped to 0..R and a
-// negative count counts as none, so that every tile lies within y.  One
-// workgroup; each thread takes one expert, then finds its tiles by bisection.
+// first the whole blocks of bm rows, experts in ascending order, then the
+// experts' last, shorter blocks, the longest first (in sixteenths of rows), so
+// that the short ones fill the end of the launch; the rest of the list is
+// empty.  Offsets are clamped to 0..R and a negative count counts as none, so
+// that every tile lies within y.  One workgroup, a thread per expert.
 __global__ __launch_bounds__(1024) void plan_tiles(const int32_t *__restrict__ offsets, int E,
                                                    int R, int bm, RowTile *__restrict__ tiles,
                                                    int ntiles)
 {
-    __shared__ int base[1025];      // first tile of each expert
+    __shared__ int base[1025];      // first whole tile of each expert
     __shared__ int start[1024];     // first row
-    __shared__ int count[1024];     // rows
-    __shared__ int wsum[16];
+    __shared__ int wsum[64];        // whole tiles of each wave's experts (16), then the sum before
+    __shared__ int wcls[128];       // short tiles by length and wave, then the sum before
+    __shared__ int totals[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int lo = 0, n = 0;
     if (tid < E) {
         lo = min(max(offsets[tid], 0), R);
         n = max(min(max(offsets[tid + 1], 0), R) - lo, 0);
     }
-    const int mine = (n + bm - 1) / bm;
-    int incl = mine;
+    const int whole = n / bm, rest = n - whole * bm;
+    int incl = whole;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
         const int v = __shfl_up(incl, d);
         if (lane >= d) incl += v;
     }
     if (lane == 63) wsum[wave] = incl;
+    // length class of the short tile: 0 the longest, -1 none
+    const int cls = rest ? (bm - rest) / 16 : -1;
+    int rank = 0;
+#pragma unroll
+    for (int c = 0; c < 8; c++) {
+        const unsigned long long m = __ballot(cls == c);
+        if (cls == c) rank = __popcll(m & ((1ull << lane) - 1));
+        if (lane == c) wcls[c * 16 + wave] = __popcll(m);
+    }
     __syncthreads();
-    int before = 0;
-    for (int i = 0; i < wave; i++) before += wsum[i];
+    if (wave < 2) {                                      // exclusive sums, one wave each
+        const int w = wave == 0 ? (lane < 16 ? wsum[lane] : 0) : wcls[2 * lane];
+        const int w1 = wave == 0 ? 0 : wcls[2 * lane + 1];
+        int s = w + w1;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int v = __shfl_up(s, d);
+            if (lane >= d) s += v;
+        }
+        if (lane == 63) totals[wave] = s;
+        if (wave == 0) {
+            wsum[lane] = s - w;
+        } else {
+            wcls[2 * lane] = s - w - w1;
+            wcls[2 * lane + 1] = s - w1;
+        }
+    }
+    __syncthreads();
+    const int before = wsum[wave], total = totals[0], shorts = totals[1];
     // overlapping offsets (not allowed) could name more tiles than the list
     // holds; sums of up to 1024 counts of 2^24 / 16 tiles stay below 2^31
     base[tid + 1] = before + incl;
     if (tid == 0) base[0] = 0;
     start[tid] = lo;
-    count[tid] = n;
+    const int at = cls >= 0 ? wcls[cls * 16 + wave] : 0;
     __syncthreads();
+    if (cls >= 0 && total + at + rank < ntiles)
+        tiles[total + at + rank] = RowTile{tid, lo + whole * bm, rest, 0};
     for (int i = tid; i < ntiles; i += 1024) {
+        if (i >= total && i < total + shorts) continue;
         RowTile t{0, 0, 0, 0};
-        if (i < base[1024]) {
+        if (i < total) {
             int a = 0, b = 1024;                         // base[a] <= i < base[b]
             while (b - a > 1) {
                 const int m = (a + b) / 2;
                 if (base[m] <= i) a = m;
                 else b = m;
             }
-            const int r = (i - base[a]) * bm;
-            t = RowTile{a, start[a] + r, min(bm, count[a] - r), 0};
+            t = RowTile{a, start[a] + (i - base[a]) * bm, bm, 0};
         }
         tiles[i] = t;
     }
