@@ -353,7 +353,8 @@ long long max_tiles(int R, int E, int bm)
 }
 
 // Tile of a product: the one whose busiest CU has the least to do, estimated
-// as workgroups per CU times the cost of one.  Costs of a workgroup relative
+// as workgroups per CU times the cost of one (a fifth more for a tile that has
+// its CU to itself, one wave per SIMD).  Costs of a workgroup relative
 // to 128 x 256, from bf16 int4 at 6144 columns (125 us with one 128 x 256
 // tile per CU, 200 with two, 323 with three); f32 counts two planes.  What the
 // rule decides, us with the tile chosen and with the next best: 256 x 12288:
@@ -373,10 +374,10 @@ void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
     static const Kind bf16[] = {{128, false, true, 1.0},
                                 {96, false, false, 0.83},
                                 {64, false, false, 0.66},
-                                {64, true, true, 0.265},
-                                {32, true, false, 0.185}};
+                                {64, true, true, 0.235},
+                                {32, true, false, 0.16}};
     static const Kind f32[] = {{64, false, true, 0.93}, {32, false, false, 0.69},
-                               {32, true, true, 0.26}};
+                               {32, true, true, 0.21}};
     const bool half = a.dtype == QGEMV_BF16;
     const Kind *kinds = half ? bf16 : f32;
     const int n = half ? 5 : 3;
@@ -389,7 +390,8 @@ void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
         const long long mt = (a.R + k.bm - 1) / k.bm +
                              (a.offsets ? (a.E < a.R ? a.E : a.R) / 2 : 0);
         const long long wgs = mt * ((oc + cols - 1) / cols);
-        const double c = (double)((wgs + ncu - 1) / ncu) * k.cost;
+        const long long per_cu = (wgs + ncu - 1) / ncu;
+        const double c = per_cu * k.cost * (per_cu == 1 && !k.narrow ? 1.2 : 1.0);
         if (best < 0.0 || c < best) {                    // ties: the larger tile
             best = c;
             bm = k.bm;

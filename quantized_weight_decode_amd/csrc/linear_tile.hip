@@ -619,7 +619,7 @@ __device__ __forceinline__ void wait_own_loads()
 // LDS in a fixed order.  At 64 x 6144 x 12288 bf16 the tile kernel has 48
 // workgroups for 256 CUs and takes 89 us.
 template <int FMT, typename XT, int NP, int MB, bool GATED, int FG, bool RAGGED, int KW, int AST>
-__global__ __launch_bounds__(KW * 64, KW / 4) void linear_narrow(TileArgs p)
+__global__ __launch_bounds__(KW * 64, (KW + 3) / 4) void linear_narrow(TileArgs p)
 {
     typedef Weights<FMT, FG, 64> W;
     constexpr int NB = 4, NS = TK / FG;
@@ -784,7 +784,7 @@ hipError_t run_narrow(const TileArgs &p, unsigned grid, hipStream_t st)
 {
     // 8 waves where their stages fit the 160 KB of LDS, else 4
     constexpr int NP = sizeof(typename XT::raw) == 4 ? 2 : 1;
-    constexpr int KW = NP * MB <= 2 ? 8 : 4, AST = KW == 8 ? 2 : 3;
+    constexpr int KW = NP * MB <= 2 ? 8 : 6, AST = 2;
 #define QG_RUN2(FG, G, R)                                                                   \
     hipLaunchKernelGGL((linear_narrow<FMT, XT, NP, MB, G, FG, R, KW, AST>), dim3(grid),  \
                        dim3(KW * 64), 0, st, p)
