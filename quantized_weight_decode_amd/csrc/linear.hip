@@ -353,17 +353,18 @@ long long max_tiles(int R, int E, int bm)
 }
 
 // Tile of a product: the one whose busiest CU has the least to do, estimated
-// as workgroups per CU times the cost of one (a fifth more for a tile that has
-// its CU to itself, one wave per SIMD).  Costs of a workgroup relative
-// to 128 x 256, from bf16 int4 at 6144 columns (125 us with one 128 x 256
-// tile per CU, 200 with two, 323 with three); f32 counts two planes.  What the
-// rule decides, us with the tile chosen and with the next best: 256 x 12288:
-// 64 x 256 89, narrow 93, 128 x 256 125; 512 x 12288: 128 x 256 126, 64 x 256
-// 139; 700 x 12288: 96 x 256 164, 128 x 256 188; 512 x 4096 (4096 columns):
-// narrow 49, 64 x 256 65; f32 333 x 11008 (4096 columns): 32 x 256 97, 64 x
-// 256 117.  Grouped tiles know
-// neither their count (estimated with half a tile per expert) nor their
-// filling, and skip what they lack: only the largest of each kind.
+// as workgroups per CU times the cost of one, relative to 128 x 256 (a fifth
+// more for a tile that has its CU to itself, one wave per SIMD); f32 counts two
+// planes.  What the rule decides for int4, us with the tile chosen and with the
+// next best: bf16, 12288 deep, 6144 columns: 256 rows: 64 x 256 78, narrow 93;
+// 512: 128 x 256 126, 64 x 256 139; 700: 96 x 256 164, 128 x 256 188; 4096
+// deep, 4096 columns: 512 rows: narrow 49, 64 x 256 65.  f32, 11008 deep, 4096
+// columns: 333 rows: 32 x 256 86, 64 x 256 117.
+// Grouped tiles are the largest of each kind, their count estimated with half a
+// tile per expert, and a tile skips the rows it lacks: the cost has a fixed part
+// and one that goes with the filling.  512 tokens of 8 among 256 experts, 7168 x
+// 2048: 128 x 256 618, narrow 760; 200 of 2 among 8, 1024 x 512: narrow 19, 128
+// x 256 62.
 void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
 {
     struct Kind {
@@ -391,7 +392,11 @@ void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
                              (a.offsets ? (a.E < a.R ? a.E : a.R) / 2 : 0);
         const long long wgs = mt * ((oc + cols - 1) / cols);
         const long long per_cu = (wgs + ncu - 1) / ncu;
-        const double c = per_cu * k.cost * (per_cu == 1 && !k.narrow ? 1.2 : 1.0);
+        double c = per_cu * k.cost * (per_cu == 1 && !k.narrow ? 1.2 : 1.0);
+        if (a.offsets) {
+            const double fill = (double)a.R / ((double)mt * k.bm), fixed = k.narrow ? 0.5 : 0.35;
+            c *= fixed + (1.0 - fixed) * fill;
+        }
         if (best < 0.0 || c < best) {                    // ties: the larger tile
             best = c;
             bm = k.bm;
@@ -454,13 +459,18 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hip
         return hipSuccess;
     }
     const bool fits = tile_fits(fmt, a);
+    // Stream up to 16 rows, a grouped bf16 product up to 9 for an expert on
+    // average, a grouped f32 one up to 8 in all.  us, stream and tiles:
+    // bf16, 7168 x 2048, 256 experts: 128 tokens of 8 (4 rows) 396 and 465, 256
+    // (8) 531 and 557, 320 (10) 591 and 574, 512 (16) 789 and 622; 2048 x 1024,
+    // 32 experts: 8 rows 24.1 and 27.7, 10 rows 32.2 and 28.8.
+    // f32, 2048 x 4096, 8 experts: 2 rows in all 11.6 and 14.9, 8 rows 20.4 and
+    // 21.0, 16 rows 27.1 and 24.8; 7168 x 2048, 64 rows 200 and 154.
     const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
-    // Stream up to 16 rows; grouped by the rows an expert has on average.
-    // 7168 x 2048, 256 experts, bf16: 320 tokens (10 rows) stream 578 us, tiles
-    // 696; 512 (16) 767 and 762; 768 (24) 1000 and 802.  f32: 192 tokens (6
-    // rows) 706 and 683, 512 tokens 1223 and 849.
-    const int few_rows = a.offsets && a.dtype == QGEMV_F32 ? 6 : 16;
-    const bool stream = rows <= few_rows && stream_fits(fmt, a);
+    const bool few_rows = !a.offsets                ? rows <= 16
+                          : a.dtype == QGEMV_BF16 ? rows <= 9
+                                                  : a.R <= 8;
+    const bool stream = few_rows && stream_fits(fmt, a);
     // the general kernel's tiles: 16 rows also where 64-row tiles would leave
     // CUs without one (64 x 6001 x 12288 bf16: 135 us, 227 us in 192 tiles of
     // 64 rows)
