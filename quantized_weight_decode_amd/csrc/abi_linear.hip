@@ -23,7 +23,7 @@ bool bad_sizes(int rows, int I, int O)
     return rows < 0 || rows > MAX_DIM || I < 1 || O < 1 || I > MAX_DIM || O > MAX_DIM;
 }
 
-// 64 x 64 tiles of y, the smallest of all kernels, must fit a launch
+// 16 x 16 tiles of y, the smallest of all kernels, must fit a launch
 bool too_many_tiles(long long row_tiles, int oc)
 {
     return row_tiles * ((oc + 15) / 16) > 0x7FFFFFFFLL;

@@ -13,6 +13,7 @@ namespace {
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
 constexpr int GN = 64;          // columns of y per workgroup tile
+constexpr int GN_THIN = 16;     // and per thin one
 constexpr int GK = 32;          // columns of W per K step
 constexpr int GLD = GK + 4;     // LDS row stride in floats
 constexpr int GM_FEW = 16;      // rows of y per tile, few rows
@@ -102,31 +103,37 @@ struct W8 {
 // projection's accumulators for the same columns of y.  The global loads of
 // the next K step are in flight during the products.
 //
-// FEW = false: 64 x 64 tiles of 4 waves (2 x 2 blocks of 16 each), a thread
-// stages eight columns of one row of each operand.  FEW = true: 16 x 64 tiles;
-// the waves take K steps in turn with LDS of their own, and their sums are
-// joined in a fixed order.
-template <int FMT, typename XT, bool GATED, bool FEW, bool SMALL>
-__global__ __launch_bounds__(256) void linear_general(LinearArgs a,
-                                                      const RowTile *__restrict__ tiles)
+// MANY: 64 x 64 tiles of 4 waves (2 x 2 blocks of 16 each), a thread stages
+// eight columns of one row of each operand.  FEW: 16 x 64 tiles of 4 waves,
+// which take K steps in turn with LDS of their own; their sums are joined in a
+// fixed order.  THIN: the same with 16 x 16 tiles of 16 waves, where wider ones
+// are too few to cover the latency of their loads.
+enum Shape { MANY, FEW, THIN };
+
+template <int FMT, typename XT, bool GATED, Shape SHAPE, bool SMALL>
+__global__ __launch_bounds__(SHAPE == THIN ? 1024 : 256) void
+linear_general(LinearArgs a, const RowTile *__restrict__ tiles)
 {
     typedef typename XT::raw raw;
+    constexpr bool SPLIT = SHAPE != MANY;                // K split over the waves
+    constexpr int WAVES = SHAPE == THIN ? 16 : 4;
+    constexpr int BN = SHAPE == THIN ? GN_THIN : GN;
     constexpr int NW = GATED ? 2 : 1;
-    constexpr int BM = FEW ? GM_FEW : GM;
-    constexpr int MB = FEW ? 1 : 2, NB = FEW ? 4 : 2;    // blocks of a wave
-    constexpr int WR = FEW ? 4 : 1;                      // rows of W a thread stages
-    constexpr int STAGE = (BM + NW * GN) * GLD;          // floats
-    constexpr int OLD = GN + 1;                          // epilogue row stride
-    constexpr int OUT = (FEW ? 4 * GM_FEW : 32) * OLD * NW;
-    constexpr int STAGES = (FEW ? 4 : 1) * STAGE;
+    constexpr int BM = SPLIT ? GM_FEW : GM;
+    constexpr int MB = SPLIT ? 1 : 2, NB = SPLIT ? BN / 16 : 2;   // blocks of a wave
+    constexpr int WR = SPLIT ? BN / 16 : 1;              // rows of W a thread stages
+    constexpr int STAGE = (BM + NW * BN) * GLD;          // floats
+    constexpr int OLD = BN + 1;                          // epilogue row stride
+    constexpr int OUT = (SPLIT ? WAVES * GM_FEW : 32) * OLD * NW;
+    constexpr int STAGES = (SPLIT ? WAVES : 1) * STAGE;
     __shared__ __align__(16) float lds[STAGES > OUT ? STAGES : OUT];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = FEW ? 0 : wave & 1, wn = FEW ? 0 : wave >> 1;
-    float *const xs = lds + (FEW ? wave * STAGE : 0);
+    const int wm = SPLIT ? 0 : wave & 1, wn = SPLIT ? 0 : wave >> 1;
+    float *const xs = lds + (SPLIT ? wave * STAGE : 0);
     float *const ws = xs + BM * GLD;
     const int oc = GATED ? a.O / 2 : a.O;                // columns of y
-    const int ntn = (oc + GN - 1) / GN;
-    const int o0 = (int)(blockIdx.x % ntn) * GN;
+    const int ntn = (oc + BN - 1) / BN;
+    const int o0 = (int)(blockIdx.x % ntn) * BN;
     const int mt = (int)(blockIdx.x / ntn);
     RowTile t;
     if (tiles) t = tiles[mt];
@@ -142,9 +149,9 @@ __global__ __launch_bounds__(256) void linear_general(LinearArgs a,
             for (int j = 0; j < NB; j++) acc[p][i][j] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 
     // this thread's staging place: row sr of x, rows sr + 16 i of W, eight
-    const int u = FEW ? lane : tid;
-    const int sr = u >> 2, sc = (u & 3) * 8;
     // columns from sc; rows behind the tile or the matrix repeat the first
+    const int u = SPLIT ? lane : tid;
+    const int sr = u >> 2, sc = (u & 3) * 8;
     long long xrow = t.row0 + (sr < t.n ? sr : 0);
     if (a.rows) {
         const int r = a.rows[xrow];
@@ -186,11 +193,11 @@ __global__ __launch_bounds__(256) void linear_general(LinearArgs a,
                     wv[p][i].load_tail(wsrc[p][i], ssrc[p][i], k, a.I, a.ng, gs);
         }
     };
-    constexpr int STEP = (FEW ? 4 : 1) * GK;
-    const int first = FEW ? wave * GK : 0;
+    constexpr int STEP = (SPLIT ? WAVES : 1) * GK;
+    const int first = SPLIT ? wave * GK : 0;
     if (first < a.I) load(first);
     for (int k0 = first; k0 < a.I; k0 += STEP) {
-        if (!FEW && k0 > 0) __syncthreads();             // the previous step's reads are done
+        if (!SPLIT && k0 > 0) __syncthreads();             // the previous step's reads are done
 #pragma unroll
         for (int c = 0; c < 8; c++) xs[sr * GLD + sc + c] = XT::get(xv.v[c]);
 #pragma unroll
@@ -200,9 +207,9 @@ __global__ __launch_bounds__(256) void linear_general(LinearArgs a,
                 float w[8];
                 wv[p][i].decode(w);
 #pragma unroll
-                for (int c = 0; c < 8; c++) ws[(p * GN + sr + 16 * i) * GLD + sc + c] = w[c];
+                for (int c = 0; c < 8; c++) ws[(p * BN + sr + 16 * i) * GLD + sc + c] = w[c];
             }
-        if (!FEW) __syncthreads();
+        if (!SPLIT) __syncthreads();
         else __builtin_amdgcn_wave_barrier();            // lanes read each other's values
         if (k0 + STEP < a.I) load(k0 + STEP);
 #pragma unroll
@@ -216,7 +223,7 @@ __global__ __launch_bounds__(256) void linear_general(LinearArgs a,
 #pragma unroll
                 for (int j = 0; j < NB; j++)
                     bv[p][j] =
-                        ws[(p * GN + wn * 32 + j * 16 + (lane & 15)) * GLD + kk + (lane >> 4)];
+                        ws[(p * BN + wn * 32 + j * 16 + (lane & 15)) * GLD + kk + (lane >> 4)];
 #pragma unroll
             for (int p = 0; p < NW; p++)
 #pragma unroll
@@ -228,7 +235,7 @@ __global__ __launch_bounds__(256) void linear_general(LinearArgs a,
         }
     }
 
-    // sums through LDS (FEW: of all waves; else 16 rows of each 32 at a time),
+    // sums through LDS (K split: of all waves; else 16 rows of each 32 at a time),
     // so that one piece of code ends all outputs
 #pragma unroll
     for (int i = 0; i < MB; i++) {
@@ -239,19 +246,19 @@ __global__ __launch_bounds__(256) void linear_general(LinearArgs a,
             for (int j = 0; j < NB; j++)
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-                    const int m = (FEW ? wave : wm) * 16 + 4 * (lane >> 4) + r;
+                    const int m = (SPLIT ? wave : wm) * 16 + 4 * (lane >> 4) + r;
                     lds[(m * NW + p) * OLD + wn * 32 + j * 16 + (lane & 15)] = acc[p][i][j][r];
                 }
         __syncthreads();
-        finish<XT, 4>(a, t.expert, tid, 256, (FEW ? GM_FEW : 32) * GN,
+        finish<XT, 4>(a, t.expert, tid, WAVES * 64, (SPLIT ? GM_FEW : 32) * BN,
                       [&](int k, int &row, int &col, float &v, float &up) {
-                          const int m = k / GN, c = k % GN;
-                          const int tr = FEW ? m : (m >> 4) * 32 + i * 16 + (m & 15);
+                          const int m = k / BN, c = k % BN;
+                          const int tr = SPLIT ? m : (m >> 4) * 32 + i * 16 + (m & 15);
                           row = t.row0 + tr;
                           col = tr < t.n && o0 + c < oc ? o0 + c : oc;
                           v = up = 0.0f;
 #pragma unroll
-                          for (int w = 0; w < (FEW ? 4 : 1); w++) {
+                          for (int w = 0; w < (SPLIT ? WAVES : 1); w++) {
                               v += lds[((w * 16 + m) * NW) * OLD + c];
                               if (GATED) up += lds[((w * 16 + m) * NW + 1) * OLD + c];
                           }
@@ -356,9 +363,9 @@ long long max_tiles(int R, int E, int bm)
 // as workgroups per CU times the cost of one, relative to 128 x 256 (a fifth
 // more for a tile that has its CU to itself, one wave per SIMD); f32 counts two
 // planes.  What the rule decides for int4, us with the tile chosen and with the
-// next best: bf16, 12288 deep, 6144 columns: 256 rows: 64 x 256 78, narrow 93;
+// next best: bf16, 6144 deep, 12288 columns: 256 rows: 64 x 256 78, narrow 93;
 // 512: 128 x 256 126, 64 x 256 139; 700: 96 x 256 164, 128 x 256 188; 4096
-// deep, 4096 columns: 512 rows: narrow 49, 64 x 256 65.  f32, 11008 deep, 4096
+// deep, 4096 columns: 512 rows: narrow 49, 64 x 256 65.  f32, 4096 deep, 11008
 // columns: 333 rows: 32 x 256 86, 64 x 256 117.
 // Grouped tiles are the largest of each kind, their count estimated with half a
 // tile per expert, and a tile skips the rows it lacks: the cost has a fixed part
@@ -406,26 +413,33 @@ void pick_tile(const LinearArgs &a, int oc, int &bm, bool &narrow)
 }
 
 template <int FMT, typename XT>
-void run_general(const LinearArgs &a, bool few, const RowTile *tiles, unsigned grid,
+void run_general(const LinearArgs &a, Shape shape, const RowTile *tiles, unsigned grid,
                  hipStream_t st)
 {
-#define QG_RUN(G, F, S)                                                                     \
-    hipLaunchKernelGGL((linear_general<FMT, XT, G, F, S>), dim3(grid), dim3(256), 0, st, a, tiles)
-#define QG_RUN_G(F, S)                                                                      \
+#define QG_RUN(G, H, S)                                                                     \
+    hipLaunchKernelGGL((linear_general<FMT, XT, G, H, S>), dim3(grid),                      \
+                       dim3((H) == THIN ? 1024 : 256), 0, st, a, tiles)
+#define QG_RUN_S(S)                                                                         \
     do {                                                                                    \
-        if (a.gated) QG_RUN(true, F, S);                                                    \
-        else QG_RUN(false, F, S);                                                           \
+        if (shape == THIN) {                                                                \
+            if (a.gated) QG_RUN(true, THIN, S);                                             \
+            else QG_RUN(false, THIN, S);                                                    \
+        } else if (shape == FEW) {                                                          \
+            if (a.gated) QG_RUN(true, FEW, S);                                              \
+            else QG_RUN(false, FEW, S);                                                     \
+        } else {                                                                            \
+            if (a.gated) QG_RUN(true, MANY, S);                                             \
+            else QG_RUN(false, MANY, S);                                                    \
+        }                                                                                   \
     } while (0)
     if constexpr (FMT == FMT_I4G) {
         if (a.gs < 8) {
-            if (few) QG_RUN_G(true, true);
-            else QG_RUN_G(false, true);
+            QG_RUN_S(true);
             return;
         }
     }
-    if (few) QG_RUN_G(true, false);
-    else QG_RUN_G(false, false);
-#undef QG_RUN_G
+    QG_RUN_S(false);
+#undef QG_RUN_S
 #undef QG_RUN
 }
 
@@ -471,14 +485,18 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hip
                           : a.dtype == QGEMV_BF16 ? rows <= 9
                                                   : a.R <= 8;
     const bool stream = few_rows && stream_fits(fmt, a);
-    // the general kernel's tiles: 16 rows also where 64-row tiles would leave
-    // CUs without one (64 x 6001 x 12288 bf16: 135 us, 227 us in 192 tiles of
-    // 64 rows)
-    const long long tiles64 =
-        (long long)((a.R + GM - 1) / GM + (a.offsets ? (a.E < a.R ? a.E : a.R) / 2 : 0)) *
-        ((oc + GN - 1) / GN);
-    const bool few = rows <= GM_FEW || tiles64 <= cu_count();
-    int bm = few ? GM_FEW : GM;
+    // The general kernel's tiles: 16 rows also where 64-row tiles would give a
+    // CU less than two, thin ones where those of 16 x 64 would.  us, bf16 int4:
+    // 512 x 3001 x 3001 (376 tiles of 64 rows) 141 in tiles of 16 rows, 160 of
+    // 64; 512 x 3001 x 6001 (752) 268 and 205; 2 x 4069 x 2742 (43 tiles of 16 x
+    // 64) 45, thin 13; 128 x 3001 x 3001 (376) 56, thin 44; 128 x 3001 x 6001
+    // (752) 73, thin 83.
+    const long long shorts = a.offsets ? (a.E < a.R ? a.E : a.R) / 2 : 0;
+    const long long ntn = (oc + GN - 1) / GN, most = cu_count() * 3 / 2;
+    const long long tiles64 = ((a.R + GM - 1) / GM + shorts) * ntn;
+    const long long tiles16 = ((a.R + GM_FEW - 1) / GM_FEW + shorts) * ntn;
+    const Shape shape = rows > GM_FEW && tiles64 > most ? MANY : tiles16 > most ? FEW : THIN;
+    int bm = shape == MANY ? GM : GM_FEW;
     bool narrow = false;
     if (stream) {
         bm = 16;
@@ -498,14 +516,15 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hip
     }
     if (stream) return launch_stream(fmt, a, tiles, (int)mt, st);
     if (fits) return launch_tile(fmt, a, narrow, bm, tiles, (int)mt, ws, st);
-    const long long grid = mt * ((oc + GN - 1) / GN);
+    const int bn = shape == THIN ? GN_THIN : GN;
+    const long long grid = mt * ((oc + bn - 1) / bn);
     if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     if (fmt == FMT_I4G) {
-        if (a.dtype == QGEMV_BF16) run_general<FMT_I4G, BF16>(a, few, tiles, (unsigned)grid, st);
-        else run_general<FMT_I4G, F32>(a, few, tiles, (unsigned)grid, st);
+        if (a.dtype == QGEMV_BF16) run_general<FMT_I4G, BF16>(a, shape, tiles, (unsigned)grid, st);
+        else run_general<FMT_I4G, F32>(a, shape, tiles, (unsigned)grid, st);
     } else {
-        if (a.dtype == QGEMV_BF16) run_general<FMT_FP8, BF16>(a, few, tiles, (unsigned)grid, st);
-        else run_general<FMT_FP8, F32>(a, few, tiles, (unsigned)grid, st);
+        if (a.dtype == QGEMV_BF16) run_general<FMT_FP8, BF16>(a, shape, tiles, (unsigned)grid, st);
+        else run_general<FMT_FP8, F32>(a, shape, tiles, (unsigned)grid, st);
     }
     return hipGetLastError();
 }

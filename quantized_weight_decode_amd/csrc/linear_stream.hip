@@ -168,8 +168,9 @@ struct StreamArgs {
 
 // Stream kernel.  A workgroup of 8 waves makes up to 16 rows of y x 16 NB
 // rows of W; the waves take blocks of P chunks of 128 columns in turn, and
-// their sums are joined through LDS in a fixed order.  v_mfma_f32_16x16x32_bf16, lane l: A row of x
-// l % 16, B row of W l % 16, eight columns from the lane group l / 16.
+// their sums are joined through LDS in a fixed order.
+// v_mfma_f32_16x16x32_bf16, lane l: A row of x l % 16, B row of W l % 16, eight
+// columns from the lane group l / 16.
 //
 // Lanes next to each other load 16-byte pieces of one row (a load of 64 lanes
 // in 64 different rows takes the vector cache 64 cycles, whatever its width),

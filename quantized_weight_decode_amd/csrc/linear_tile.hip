@@ -412,18 +412,22 @@ __device__ __forceinline__ void multiply_step(f32x4v (&acc)[MF][NB], const f16x8
 
 // Tile kernel.  A workgroup of 4 waves makes 16 MF rows of y x 256 rows of W;
 // each wave all 16 MF rows x 64 rows of W, so a weight is unpacked once per
-// workgroup, from registers, and never passes LDS, while the waves share the
-// packed activations through LDS (two buffers, 16-byte chunks XOR-swizzled by
-// row).  v_mfma_f32_16x16x32_f16, lane l: A row l % 16, B column l % 16, eight
-// k from the lane group l / 16; D rows 4 (l / 16) + i, column l % 16.  The k
-// order inside a K step is free as long as A and B agree: with one scale per
-// 64 columns a lane group owns 16 consecutive columns (one 8-byte load of
-// int4), with one per 32 it owns eight of each 32.
-// Integer (or fp8) products are summed exactly-scaled per scale group: the
-// group's sum starts at zero and is added to the total as acc += s * sum, one
-// FMA per output and group, beside two matrix instructions.  RAGGED (grouped): row
-// blocks of 16 behind the tile's rows are neither loaded nor multiplied; a
-// dense product does without those branches (5 % faster at 2048 rows).
+// workgroup.  Everything comes by memory-to-LDS loads: the packed activations
+// shared by the four waves, 16-byte chunks XOR-swizzled by row, each wave's
+// weights and scales in a part of its own.  v_mfma_f32_16x16x32_f16, lane l: A
+// row l % 16, B column l % 16, eight k from the lane group l / 16; D rows
+// 4 (l / 16) + i, column l % 16.  The k order inside a K step is free as long
+// as A and B agree: with one scale per 64 columns a lane group owns 16
+// consecutive columns (8 bytes of int4), with one per 32 it owns eight of each
+// 32.
+// A scale group's products are summed from zero and added to the total as
+// acc += s * sum in f32, one FMA per output and group, beside two matrix
+// instructions.  RAGGED (grouped): row blocks of 16 behind the tile's rows are
+// neither loaded nor multiplied; a dense product does without those branches
+// (5 % faster at 2048 rows).
+// Bound by the matrix cores: int4 2048 x 6144 x 12288 bf16, packing included,
+// 318 us (972 TFLOP/s); the library's bf16 product of the same size takes 289
+// us (1069 TFLOP/s), of 8192^3 1364 TFLOP/s.
 template <int FMT, typename XT, int NP, int MF, bool GATED, int FG, bool RAGGED>
 __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
 {
@@ -616,8 +620,9 @@ __device__ __forceinline__ void wait_own_loads()
 // the GPU with its tiles.  A workgroup makes up to 16 MB rows of y x 16 NB
 // rows of W; its KW waves take the K steps in turn, each with stages of LDS of
 // its own, so the K loop needs no barrier, and their sums are joined through
-// LDS in a fixed order.  At 64 x 6144 x 12288 bf16 the tile kernel has 48
-// workgroups for 256 CUs and takes 89 us.
+// LDS in a fixed order.  Bound by the loads in flight, which LDS limits: 64 x
+// 6144 x 12288 bf16 31 us, 40 MB of weights; the tile kernel's 48 workgroups
+// take 89 us.
 template <int FMT, typename XT, int NP, int MB, bool GATED, int FG, bool RAGGED, int KW, int AST>
 __global__ __launch_bounds__(KW * 64, (KW + 3) / 4) void linear_narrow(TileArgs p)
 {
@@ -779,14 +784,15 @@ hipError_t run_tile(const TileArgs &p, unsigned grid, hipStream_t st)
     }
     return hipGetLastError();
 }
+
 template <int FMT, typename XT, int MB>
 hipError_t run_narrow(const TileArgs &p, unsigned grid, hipStream_t st)
 {
-    // 8 waves where their stages fit the 160 KB of LDS, else 4
+    // 8 waves where their stages fit the 160 KB of LDS, else 6
     constexpr int NP = sizeof(typename XT::raw) == 4 ? 2 : 1;
     constexpr int KW = NP * MB <= 2 ? 8 : 6, AST = 2;
 #define QG_RUN2(FG, G, R)                                                                   \
-    hipLaunchKernelGGL((linear_narrow<FMT, XT, NP, MB, G, FG, R, KW, AST>), dim3(grid),  \
+    hipLaunchKernelGGL((linear_narrow<FMT, XT, NP, MB, G, FG, R, KW, AST>), dim3(grid),     \
                        dim3(KW * 64), 0, st, p)
 #define QG_RUN3(FG)                                                                         \
     do {                                                                                    \

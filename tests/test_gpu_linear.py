@@ -298,3 +298,40 @@ def test_more_activations_than_one_slice(q):
         # sums, one bf16 rounding each
         d = (part.double() - y[lo:lo + 30].double()).abs()
         assert float((d / (2.0 ** -7 * y[lo:lo + 30].double().abs() + 0.05)).max()) <= 1.0
+
+
+@pytest.mark.parametrize("fmt", ["i4g", "fp8"])
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("S,O", [(100, 3700), (900, 2000), (5, 26000)])
+@pytest.mark.parametrize("I,gs,gated", [(45, 2, False), (70, 6, True), (101, 64, True),
+                                        (161, 10, False)])
+def test_wide_general(q, fmt, S, O, dtype, I, gs, gated):
+    """Shapes of the general kernel with many tiles of 16 and of 64 rows."""
+    k = {"act": "gelu", "gated": True, "bias": True, "residual": True} if gated else {}
+    y, ref, bound = _run(q, fmt, S, I, O, gs, dtype, seed=S + I, **k)
+    L.assert_within(y, ref, bound)
+
+
+def test_two_streams_at_once(q):
+    """Calls of all kernels on two streams side by side, a workspace each."""
+    gs, cases = 64, []
+    for S, I, O in [(3, 2048, 1000), (40, 2048, 1000), (300, 1024, 4000), (60, 1001, 900)]:
+        w, s = L.int4((O,), I, gs, S)
+        cases.append((dev(w), dev(s), L.acts(S, I, torch.bfloat16, S + 1).cuda()))
+    want = [q.i4g_linear(w, s, x, gs, act="silu") for w, s, x in cases]
+    wsp = [[q.linear_workspace(x.shape[0], x.shape[1], w.shape[0], x.dtype, "cuda")
+            for w, s, x in cases] for _ in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(5):
+        for j, st in enumerate(streams):
+            order = range(len(cases)) if j else reversed(range(len(cases)))
+            with torch.cuda.stream(st):
+                for c in order:
+                    w, s, x = cases[c]
+                    got[j].append((c, q.i4g_linear(w, s, x, gs, act="silu", workspace=wsp[j][c])))
+    torch.cuda.synchronize()
+    for c, y in got[0] + got[1]:
+        assert torch.equal(y, want[c])

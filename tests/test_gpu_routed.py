@@ -310,3 +310,26 @@ def test_grouped_wide_tiles(q, I, gs, gated, dtype):
                                      x[torch.from_numpy(rows[keep]).long()], dtype,
                                      act="silu" if gated else None, gated=gated)
             L.assert_within(y[keep], ref, bound, f"expert {e}")
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("counts,O", [([7, 13, 0, 16, 17, 1, 3, 20] * 8, 600),
+                                      ([900, 3, 0, 400, 64, 65], 2600)])
+@pytest.mark.parametrize("I,gs,gated", [(45, 2, False), (101, 64, True)])
+def test_grouped_wide_general(q, counts, O, I, gs, gated, dtype):
+    """Shapes of the general kernel with many tiles of 16 and of 64 rows."""
+    E, R, T = len(counts), sum(counts), 50
+    w, s = L.int4((E, O), I, gs, 42)
+    off = counts_offsets(counts)
+    x, bias = L.acts(T, I, dtype, 43), L.acts(E, O, dtype, 44)
+    rows = np.random.default_rng(3).integers(0, T, R).astype(np.int32)
+    k = {"act": "gelu_tanh" if gated else None, "gated": gated}
+    y = q.i4g_grouped(dev(w), dev(s), x.cuda(), dev(off), gs, rows=dev(rows), bias=bias.cuda(),
+                      **k)
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        if hi > lo:
+            ref, bound = L.reference(L.decode_int4(w[e], s[e], I, gs),
+                                     x[torch.from_numpy(rows[lo:hi]).long()], dtype,
+                                     bias=bias[e], **k)
+            L.assert_within(y[lo:hi], ref, bound, f"expert {e}")
