@@ -160,6 +160,52 @@ struct XFrag<F32, FMT> {
     }
 };
 
+// A lane's 16 bytes of x on the way to LDS as bf16 in the weights' column order
+// (of each eight), f32 as three parts of eight bits each, exactly: each part is
+// the high half of what is left.
+template <typename XT, int FMT>
+struct XParts;
+template <int FMT>
+struct XParts<BF16, FMT> {                               // eight columns
+    static constexpr int NP = 1;
+    static __device__ __forceinline__ void store(char *at, int, int, u32x4 v)
+    {
+        u32x4 o = v;
+        if (FMT == FMT_I4G) {
+            o.x = low_halves(v.x, v.z);
+            o.y = high_halves(v.x, v.z);
+            o.z = low_halves(v.y, v.w);
+            o.w = high_halves(v.y, v.w);
+        }
+        *reinterpret_cast<u32x4 *>(at) = o;
+    }
+};
+template <int FMT>
+struct XParts<F32, FMT> {                                // four columns, odd: the last of eight
+    static constexpr int NP = 3;
+    static __device__ __forceinline__ void store(char *at, int odd, int part_stride, u32x4 v)
+    {
+        uint32_t *const to = reinterpret_cast<uint32_t *>(at);
+#pragma unroll
+        for (int q = 0; q < 3; q++) {
+            uint32_t *const d = to + q * (part_stride / 4);
+            if (FMT == FMT_I4G) {
+                d[odd] = high_halves(v.x, v.z);
+                d[odd + 2] = high_halves(v.y, v.w);
+            } else {
+                d[2 * odd] = high_halves(v.x, v.y);
+                d[2 * odd + 1] = high_halves(v.z, v.w);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t all = v[j], high = all & 0xFFFF0000u;
+                v[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, all) -
+                                                        __builtin_bit_cast(float, high));
+            }
+        }
+    }
+};
+
 struct StreamArgs {
     LinearArgs a;
     const RowTile *tiles;
@@ -184,13 +230,26 @@ struct StreamArgs {
 // activations multiply q - 8, whose unpacking costs 2.5 instead of 0.9
 // instructions per weight: an outlier of x at a zero weight must not cost the
 // small elements their bits.
-template <int FMT, typename XT, int NB, bool GATED, int FG, int P>
+//
+// ROWS = 16: x goes to LDS as it is in memory, and each fragment is turned into
+// bf16 parts as it is read; three parts of f32 take three matrix instructions.
+// ROWS = 4 (dense): the parts are made on the way to LDS, once per element
+// instead of once per lane of a fragment, and the three parts of four rows are
+// the rows of one fragment; their sums are added in the end.  One f32 row of
+// 6144 x 12288 15.7 us (with ROWS = 16 20.8), of 7168 x 2048 7.9 (11.9); bf16
+// 12.4 (13.3) and 6.6 (7.4).
+// 42 MB of weights and scales at the 4.8 TB/s of a large copy take 8.8 us; two
+// blocks in flight per wave (14.3 us) and blocks of 512 columns (13.8) are
+// slower than one of 256.
+template <int FMT, typename XT, int NB, bool GATED, int FG, int P, int ROWS>
 __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
 {
     typedef typename XT::raw raw;
     typedef XFrag<XT, FMT> Frag;
-    constexpr int NP = Frag::NP;
-    constexpr bool OFFSET = FMT == FMT_I4G && NP == 1;
+    constexpr bool FEW = ROWS == 4;
+    constexpr int NP = FEW ? 1 : Frag::NP;               // matrix instructions per step
+    constexpr int XQ = FEW ? Frag::NP : 1;               // parts of x beside each other
+    constexpr bool OFFSET = FMT == FMT_I4G && Frag::NP == 1;
     constexpr int NG = SC / FG;                          // scale groups of a chunk
     constexpr int TPG = 4 / NG;                          // 32-column steps of a group
     constexpr int WC = FMT == FMT_FP8 ? 8 : 4;           // 16-byte pieces of a row and chunk
@@ -201,12 +260,12 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     constexpr int SL = (NB * 16 * NGB + 63) / 64;        // scale loads
     constexpr int XP = SC * sizeof(raw) / 16;            // 16-byte pieces of a row and chunk of x
     constexpr int XR = 64 / XP;                          // rows of x per load
-    constexpr int XL = 16 / XR;                          // loads of x for 16 rows
-    constexpr int XROW = SC * sizeof(raw) + 16;          // LDS row stride, bytes
+    constexpr int XL = ROWS / XR;                        // loads of x
+    constexpr int XROW = (FEW ? P * SC * 2 : SC * (int)sizeof(raw)) + 16;   // LDS row stride, bytes
     constexpr int YC = GATED ? NB * 8 : NB * 16;         // columns of y
     constexpr int LDR = NB * 16 + 4;
     constexpr int WB = NB * 16 * WROW, SB = SL * 256;
-    constexpr int WAVE_LDS = WB + SB + 16 * XROW;
+    constexpr int WAVE_LDS = WB + SB + ROWS * XQ * XROW;
     constexpr int RED = SW * 16 * LDR * 4;
     __shared__ __align__(16) char smem[SW * WAVE_LDS > RED ? SW * WAVE_LDS : RED];
     const LinearArgs &a = p.a;
@@ -217,7 +276,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     const int nt = (int)(blockIdx.x % p.ntn), mt = (int)(blockIdx.x / p.ntn);
     RowTile t;
     if (p.tiles) t = p.tiles[mt];
-    else t = RowTile{0, mt * 16, min(16, a.R - mt * 16), 0};
+    else t = RowTile{0, mt * ROWS, min(ROWS, a.R - mt * ROWS), 0};
     t.n = __builtin_amdgcn_readfirstlane(t.n);
     t.expert = __builtin_amdgcn_readfirstlane(t.expert);
     if (t.n <= 0) return;                                // uniform over the workgroup
@@ -257,21 +316,21 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     }
     const int lane_k = (lane % WP) * (FMT == FMT_FP8 ? 16 : 32);
 
-    // the wave's LDS: weights, scales, 16 rows of x; rows past the tile's stay
-    // zero
+    // the wave's LDS: weights, scales, rows of x
     char *const wl = smem + wave * WAVE_LDS;
     float *const sl = reinterpret_cast<float *>(wl + WB);
     char *const xl = wl + WB + SB;
-    for (int i = lane; i < 16 * XROW / 16; i += 64)
-        reinterpret_cast<u32x4 *>(xl)[i] = u32x4{0, 0, 0, 0};
+    if (!FEW)                                            // rows past the tile's: zero
+        for (int i = lane; i < 16 * XROW / 16; i += 64)
+            reinterpret_cast<u32x4 *>(xl)[i] = u32x4{0, 0, 0, 0};
 
     u32x4 wr[WL], xr[P][XL];
     float sr[SL];
     const int blocks = (a.I + P * SC - 1) / (P * SC);
     const int gs = FMT == FMT_FP8 ? 128 : a.gs;
     const int nx = (t.n + XR - 1) / XR;                  // loads of x that hold rows
-    // Past the last block, and for a lane behind the row's end, loads repeat
-    // valid data (of x, the row's first piece), which meets zeros of x.
+    // A wave without a block, and a lane behind the row's end, load valid data
+    // again (of x, the row's first piece); it meets zeros of x.
     auto load_w = [&](int c) {
         const int k0 = min(c, blocks - 1) * (P * SC);
         const uint32_t kb = min((uint32_t)(FMT == FMT_I4G ? (k0 + lane_k) / 2 : k0 + lane_k),
@@ -310,8 +369,14 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
 #pragma unroll
         for (int i = 0; i < XL; i++) {
             const u32x4 v = x_inside(c, q) ? xr[q][i] : u32x4{0, 0, 0, 0};
-            if (i < nx && lane / XP + XR * i < t.n)
-                *reinterpret_cast<u32x4 *>(xl + (lane / XP + XR * i) * XROW + (lane % XP) * 16) =
+            const int r = lane / XP + XR * i;
+            if (FEW) {
+                constexpr int PW = 16 / sizeof(raw);     // columns of a piece
+                const int k = q * SC + (lane % XP) * PW;
+                if (i < nx)
+                    XParts<XT, FMT>::store(xl + r * XROW + k / 8 * 16, k / 4 & 1, ROWS * XROW, v);
+            } else if (i < nx && r < t.n)
+                *reinterpret_cast<u32x4 *>(xl + r * XROW + (lane % XP) * 16) =
                     v;
         }
     };
@@ -341,7 +406,11 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
                 const int st = g * TPG + s;
                 const int k = FMT == FMT_I4G ? 32 * st + 8 * lg
                                              : 64 * (st >> 1) + 16 * lg + 8 * (st & 1);
-                Frag::parts(xl + li * XROW + k * sizeof(raw), xv[s]);
+                if (FEW)                                 // rows behind the last repeat others
+                    xv[s][0] = *reinterpret_cast<const bf16x8 *>(
+                        xl + (li % (ROWS * XQ)) * XROW + (q * SC + k) * 2);
+                else
+                    Frag::parts(xl + li * XROW + k * sizeof(raw), xv[s]);
             }
             f32x4v z = {0.0f, 0.0f, 0.0f, 0.0f};
             if (OFFSET) {
@@ -380,18 +449,18 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     load_x(wave);
     load_w(wave);
     for (int c = wave; c < blocks; c += SW) {
+        const bool more = c + SW < blocks;               // uniform over the wave
         store_w();
-        store_x(c, 0);
+#pragma unroll
+        for (int q = 0; q < (FEW ? P : 1); q++) store_x(c, q);
         __builtin_amdgcn_sched_barrier(0);
-        load_w(c + SW);
+        if (more) load_w(c + SW);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < P; q++) {
-            if (q > 0) {
-                store_x(c, q);
-                __builtin_amdgcn_wave_barrier();         // lanes read each other's pieces
-            }
-            if (q == P - 1) load_x(c + SW);
+            if (!FEW && q > 0) store_x(c, q);
+            __builtin_amdgcn_wave_barrier();             // lanes read each other's pieces
+            if (more && q == (FEW ? 0 : P - 1)) load_x(c + SW);
             multiply(q);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -411,10 +480,12 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
                       col = nt * YC + c;
                       v = up = 0.0f;
 #pragma unroll
-                      for (int w = 0; w < SW; w++) {
-                          v += red[w][r][c];
-                          if (GATED) up += red[w][r][c + YC];
-                      }
+                      for (int w = 0; w < SW; w++)
+#pragma unroll
+                          for (int q = XQ - 1; q >= 0; q--) {
+                              v += red[w][q * 4 + r][c];
+                              if (GATED) up += red[w][q * 4 + r][c + YC];
+                          }
                       if (a.rows) {
                           const int xi = a.rows[row];
                           if (xi < 0 || xi >= a.T) v = up = __builtin_nanf("");
@@ -422,13 +493,20 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
                   });
 }
 
+bool few_rows(const LinearArgs &a) { return !a.offsets && a.R <= 4; }
+
 template <int FMT, typename XT, int NB, bool GATED>
 void run_nb(const StreamArgs &p, unsigned grid, hipStream_t st)
 {
     constexpr int P = FMT == FMT_I4G ? 2 : 1;
+#define QG_RUN_R(FG, ROWS)                                                                  \
+    hipLaunchKernelGGL((linear_stream<FMT, XT, NB, GATED, FG, P, ROWS>), dim3(grid),        \
+                       dim3(SW * 64), 0, st, p)
 #define QG_RUN(FG)                                                                          \
-    hipLaunchKernelGGL((linear_stream<FMT, XT, NB, GATED, FG, P>), dim3(grid), dim3(SW * 64), 0, \
-                       st, p)
+    do {                                                                                    \
+        if (few_rows(p.a)) QG_RUN_R(FG, 4);                                                 \
+        else QG_RUN_R(FG, 16);                                                              \
+    } while (0)
     if constexpr (FMT == FMT_FP8) {
         QG_RUN(128);
     } else {
@@ -437,6 +515,7 @@ void run_nb(const StreamArgs &p, unsigned grid, hipStream_t st)
         else QG_RUN(32);
     }
 #undef QG_RUN
+#undef QG_RUN_R
 }
 
 template <int FMT, typename XT>
@@ -469,9 +548,12 @@ hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, const RowTile *t
 {
     // Row blocks per workgroup: the count that leaves the busiest CU the
     // fewest row blocks; among equals the largest, which shares each x
-    // fragment among the most rows.
+    // fragment among the most rows, but for up to four rows of bf16 by int4,
+    // where that is cheap, the smallest (1 x 6144 x 12288: 12.4 us, three
+    // blocks 13.0; f32 16.3 and 16.0; fp8 1 x 7168 x 16384: 22.7, four 21.4).
     const int oc = a.gated ? a.O / 2 : a.O;
     const long long ncu = cu_count();
+    const bool small = few_rows(a) && fmt == FMT_I4G && a.dtype == QGEMV_BF16;
     int best = 0, ntn = 0;
     long long cost = 0;
     for (int nb = 4; nb >= 1; nb--) {
@@ -479,7 +561,7 @@ hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, const RowTile *t
         const int yc = a.gated ? nb * 8 : nb * 16;
         const int n = (oc + yc - 1) / yc;
         const long long c = (((long long)n * ntm + ncu - 1) / ncu) * nb;
-        if (!best || c < cost) {
+        if (!best || c < cost || (c == cost && small)) {
             best = nb;
             cost = c;
             ntn = n;
