@@ -612,13 +612,26 @@ def _ref(e):
 
 
 def _scratch(workspace, need, device):
-    """The caller's workspace (checked) or a new one; (tensor, pointer)."""
+    """The caller's workspace (checked) or a new one, none where none is needed;
+    (tensor, pointer, bytes)."""
     torch = _torch()
     if workspace is None:
-        workspace = torch.empty(max(int(need), 1), dtype=torch.uint8, device=device)
-    elif workspace.numel() < need:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(int(need), dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
+    if workspace.numel() < need:
         raise ValueError(f"workspace must hold {need} bytes")
-    return workspace, _dev(workspace, "workspace", torch.uint8)
+    return workspace, _dev(workspace, "workspace", torch.uint8), workspace.numel()
+
+
+def _new_rows(out, name, n, width, like):
+    """(y, pointer, row stride): the caller's out (checked) or new rows of like's
+    type."""
+    if out is None:
+        out = _torch().empty((n, width), dtype=like.dtype, device=like.device)
+        return out, out.data_ptr(), width
+    return (out, *_rows(out, name, like.dtype, (n, width)))
 
 
 def _linear(fn, w, scales, x, gs, bias, act, gated, residual, workspace, out):
@@ -638,13 +651,12 @@ def _linear(fn, w, scales, x, gs, bias, act, gated, residual, workspace, out):
     _one_device(w, scales, x, bias, residual, workspace, out)
     xp, ldx = _rows(x, "x", x.dtype)
     epi, oc = _epilogue(x.dtype, O, bias, act, gated, residual, S)
-    y = out if out is not None else torch.empty((S, oc), dtype=x.dtype, device=x.device)
-    yp, ldy = _rows(y, "out", x.dtype, (S, oc))
+    y, yp, ldy = _new_rows(out, "out", S, oc, x)
     wp, sp = _dev(w, "w", torch.uint8), _dev(scales, "scales", torch.float32)
     with _on(x.device):
-        ws, wsp = _scratch(workspace, qgemv_linear_workspace(S, I, O, code), x.device)
+        ws, wsp, nbytes = _scratch(workspace, qgemv_linear_workspace(S, I, O, code), x.device)
         args = (wp, sp, xp, ldx, yp, ldy, S, I, O) + ((gs,) if gs is not None else ())
-        _call(fn, *args, code, _ref(epi), wsp, ws.numel(), _raw_stream(x.device))
+        _call(fn, *args, code, _ref(epi), wsp, nbytes, _raw_stream(x.device))
     return y[0] if one else y
 
 
@@ -689,9 +701,9 @@ def moe_group(ids, E, workspace=None):
     tokens = torch.empty(T * K, dtype=torch.int32, device=ids.device)
     pos = torch.empty((T, K), dtype=torch.int32, device=ids.device)
     with _on(ids.device):
-        ws, wsp = _scratch(workspace, qgemv_moe_group_workspace(T, K, E), ids.device)
-        _call("qgemv_moe_group", ip, T, K, E, _dev(offsets, "offsets"), _dev(tokens, "tokens"),
-              _dev(pos, "pos"), wsp, ws.numel(), _raw_stream(ids.device))
+        ws, wsp, nbytes = _scratch(workspace, qgemv_moe_group_workspace(T, K, E), ids.device)
+        _call("qgemv_moe_group", ip, T, K, E, offsets.data_ptr(), tokens.data_ptr(),
+              pos.data_ptr(), wsp, nbytes, _raw_stream(ids.device))
     return offsets, tokens, pos
 
 
@@ -726,15 +738,15 @@ def i4g_grouped(w, scales, x, offsets, gs, rows=None, bias=None, act=None, gated
     _one_device(w, scales, x, offsets, rows, bias, workspace, out)
     xp, ldx = _rows(x, "x", x.dtype)
     epi, oc = _epilogue(x.dtype, O, bias, act, gated, None, R, E)
-    y = out if out is not None else torch.empty((R, oc), dtype=x.dtype, device=x.device)
-    yp, ldy = _rows(y, "out", x.dtype, (R, oc))
+    y, yp, ldy = _new_rows(out, "out", R, oc, x)
     wp, sp = _dev(w, "w", torch.uint8), _dev(scales, "scales", torch.float32)
     op = _dev(offsets, "offsets", torch.int32)
     rp = _dev(rows, "rows", torch.int32) if rows is not None else None
     with _on(x.device):
-        ws, wsp = _scratch(workspace, qgemv_grouped_workspace(T, R, E, I, O, code), x.device)
+        ws, wsp, nbytes = _scratch(workspace, qgemv_grouped_workspace(T, R, E, I, O, code),
+                                   x.device)
         _call("qgemv_i4g_grouped", wp, sp, O * w.shape[2], O * scales.shape[2], E, op, rp, xp,
-              ldx, T, yp, ldy, R, I, O, gs, code, _ref(epi), wsp, ws.numel(),
+              ldx, T, yp, ldy, R, I, O, gs, code, _ref(epi), wsp, nbytes,
               _raw_stream(x.device))
     return y
 
@@ -752,8 +764,7 @@ def moe_combine(h, pos, gates, residual=None, out=None):
     _one_device(h, pos, gates, residual, out)
     hp, ldh = _rows(h, "h", h.dtype)
     rp, ldr = _rows(residual, "residual", h.dtype, (T, O)) if residual is not None else (None, 0)
-    y = out if out is not None else torch.empty((T, O), dtype=h.dtype, device=h.device)
-    yp, ldy = _rows(y, "out", h.dtype, (T, O))
+    y, yp, ldy = _new_rows(out, "out", T, O, h)
     with _on(h.device):
         _call("qgemv_moe_combine", hp, ldh, R, _dev(pos, "pos", torch.int32),
               _dev(gates, "gates", torch.float32), T, K, O, rp, ldr, yp, ldy, code,
