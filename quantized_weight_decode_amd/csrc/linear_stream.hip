@@ -546,21 +546,24 @@ bool stream_fits(WeightFormat fmt, const LinearArgs &a)
 hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, const RowTile *tiles, int ntm,
                          hipStream_t st)
 {
-    // Row blocks per workgroup: the count that leaves the busiest CU the
-    // fewest row blocks; among equals the largest, which shares each x
-    // fragment among the most rows, but for up to four rows of bf16 by int4,
-    // where that is cheap, the smallest (1 x 6144 x 12288: 12.4 us, three
+    // Row blocks per workgroup: the count that leaves the busiest CU the least to
+    // do, a workgroup of 16 rows of x counted as its row blocks and 1.5 for its x
+    // (48 x 4096 x 4096 f32: one workgroup of four blocks per CU 17.5 us, three of
+    // one 27.7); among equals the largest, which shares each x fragment among
+    // the most rows, but for up to four rows of bf16 by int4, where that is
+    // cheap, the smallest (1 x 6144 x 12288: 12.4 us, three
     // blocks 13.0; f32 16.3 and 16.0; fp8 1 x 7168 x 16384: 22.7, four 21.4).
     const int oc = a.gated ? a.O / 2 : a.O;
     const long long ncu = cu_count();
     const bool small = few_rows(a) && fmt == FMT_I4G && a.dtype == QGEMV_BF16;
     int best = 0, ntn = 0;
-    long long cost = 0;
+    double cost = 0.0;
     for (int nb = 4; nb >= 1; nb--) {
         if (a.gated && (nb & 1)) continue;
         const int yc = a.gated ? nb * 8 : nb * 16;
         const int n = (oc + yc - 1) / yc;
-        const long long c = (((long long)n * ntm + ncu - 1) / ncu) * nb;
+        const double c = (double)(((long long)n * ntm + ncu - 1) / ncu) *
+                         (nb + (few_rows(a) ? 0.0 : 1.5));
         if (!best || c < cost || (c == cost && small)) {
             best = nb;
             cost = c;

@@ -335,3 +335,94 @@ def test_two_streams_at_once(q):
     torch.cuda.synchronize()
     for c, y in got[0] + got[1]:
         assert torch.equal(y, want[c])
+
+
+# more workgroups of 16 rows x 64 rows of W than CUs: the narrow kernel
+NARROW = [(20, 9000), (40, 6100), (100, 2500), (300, 1002)]
+
+
+@pytest.mark.parametrize("fmt", ["i4g", "fp8"])
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("S,O", NARROW)
+@pytest.mark.parametrize("I,gs,gated", [(160, 32, False), (256, 64, True), (96, 96, False),
+                                        (544, 32, True), (1024, 128, False), (32, 32, False)])
+def test_narrow_tiles(q, fmt, S, O, dtype, I, gs, gated):
+    k = {"act": "silu", "gated": True, "bias": True, "residual": True} if gated else {}
+    y, ref, bound = _run(q, fmt, S, I, O, gs, dtype, seed=S + I, **k)
+    L.assert_within(y, ref, bound)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("S,O", NARROW)
+def test_narrow_tiles_rows_apart(q, S, O, dtype):
+    """Strided x, residual and out, gaps untouched; rows of very different scale,
+    an outlier, a row of zeros, a row with an infinity and one with NaN."""
+    I, gs = 320, 64
+    w, s = L.int4((O,), I, gs, 50)
+    x = L.acts(S, I, dtype, 51)
+    x[0] *= 1e-30
+    x[1] *= 1e25
+    x[2, 77] = 3e4
+    x[3] = 0.0
+    res = L.acts(S, O, dtype, 52)
+    ref, bound = L.reference(L.decode_int4(w, s, I, gs), x, dtype, residual=res)
+    x[4, 5], x[5, 300] = float("nan"), float("inf")
+    xb = torch.zeros((S + 2, I + 37), dtype=dtype, device="cuda")
+    rb = torch.zeros((S + 2, O + 11), dtype=dtype, device="cuda")
+    ob = torch.full((S + 2, O + 23), 7.5, dtype=dtype, device="cuda")
+    xs, rs, out = xb[1:S + 1, 5:5 + I], rb[1:S + 1, 3:3 + O], ob[1:S + 1, 7:7 + O]
+    xs.copy_(x)
+    rs.copy_(res)
+    y = q.i4g_linear(dev(w), dev(s), xs, gs, residual=rs, out=out)
+    assert not bool(torch.isfinite(y[4:6]).any())
+    keep = [i for i in range(S) if i not in (4, 5)]
+    L.assert_within(y[keep], ref[keep], bound[keep])
+    ob[1:S + 1, 7:7 + O] = 7.5
+    assert bool((ob == 7.5).all())
+
+
+@pytest.mark.parametrize("outlier", [1e4, 1e6])
+@pytest.mark.parametrize("S,O", NARROW)
+def test_narrow_tiles_outlier_on_a_zero_weight_column(q, S, O, outlier):
+    I, gs = 1024, 64
+    w, s = L.int4((O,), I, gs, 53)
+    w[:, 100] = 0x88
+    x = L.acts(S, I, torch.float32, 54)
+    x[:, 200] = outlier
+    ref, _ = L.reference(L.decode_int4(w, s, I, gs), x, torch.float32)
+    assert L.rel_l2(q.i4g_linear(dev(w), dev(s), x.cuda(), gs), ref) <= 1e-5
+
+
+@pytest.mark.parametrize("S,O", NARROW)
+def test_narrow_tiles_replayed_graph(q, S, O):
+    I, gs = 512, 64
+    w, s = (dev(t) for t in L.int4((O,), I, gs, 55))
+    x = L.acts(S, I, torch.bfloat16, 56).cuda()
+    q.i4g_linear(w, s, x, gs, act="silu")
+    xin, ws = x.clone(), q.linear_workspace(S, I, O, x.dtype, "cuda")
+    out = torch.zeros((S, O), dtype=x.dtype, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.i4g_linear(w, s, xin, gs, act="silu", workspace=ws, out=out)
+    for i in range(4):
+        xin.copy_(x * (1 + i))
+        out.zero_()
+        g.replay()
+        want = q.i4g_linear(w, s, xin, gs, act="silu")
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_more_packed_activations_than_one_slice(q):
+    """test_more_activations_than_one_slice with columns enough for the tiles."""
+    I, O, S, gs = 1 << 20, 160, 2100, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    w = torch.randint(0, 256, (O, I // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s = 0.002 + 0.018 * torch.rand((O, I // gs), device="cuda", generator=g)
+    x = torch.randn((S, I), dtype=torch.bfloat16, device="cuda", generator=g)
+    y = q.i4g_linear(w, s, x, gs)
+    for lo in (0, 1900, 2070):
+        part = q.i4g_linear(w, s, x[lo:lo + 30], gs)
+        d = (part.double() - y[lo:lo + 30].double()).abs()
+        assert float((d / (2.0 ** -7 * y[lo:lo + 30].double().abs() + 0.05)).max()) <= 1.0
