@@ -473,24 +473,8 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hip
         return hipSuccess;
     }
     const bool fits = tile_fits(fmt, a);
-    // Stream up to 16 rows, and more while its workgroups of 16 rows x 64 rows of
-    // W fit the GPU at once; a grouped bf16 product up to 9 rows for an expert on
-    // average, a grouped f32 one up to 8 in all.  us, stream and tiles:
-    // bf16, 64 x 4096 x 4096 10.8 and 15.4, 96 x 4096 x 4096 (384 workgroups) 20.4
-    // and 15.8; 32 x 7168 x 2048 8.7 and 20.5; 32 x 6144 x 12288 (384) 26.4 and
-    // 20.8; f32, 64 x 4096 x 4096 17.5 and 20.6, 64 x 14336 x 4096 48.2 and 47.7,
-    // 32 x 2048 x 6144 9.6 and 13.8.
-    // Grouped bf16, 7168 x 2048, 256 experts: 128 tokens of 8 (4 rows) 396 and
-    // 465, 256 (8) 531 and 557, 320 (10) 591 and 574, 512 (16) 789 and 622; 2048 x
-    // 1024, 32 experts: 8 rows 24.1 and 27.7, 10 rows 32.2 and 28.8.
-    // f32, 2048 x 4096, 8 experts: 2 rows in all 11.6 and 14.9, 8 rows 20.4 and
-    // 21.0, 16 rows 27.1 and 24.8; 7168 x 2048, 64 rows 200 and 154.
     const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
-    const bool few_rows =
-        !a.offsets ? rows <= 16 || (long long)((rows + 15) / 16) * ((a.O + 63) / 64) <= cu_count()
-        : a.dtype == QGEMV_BF16 ? rows <= 9
-                                : a.R <= 8;
-    const bool stream = few_rows && stream_fits(fmt, a);
+    const int stream = stream_rows(fmt, a);
     // The general kernel's tiles: 16 rows also where 64-row tiles would give a
     // CU less than two, thin ones where those of 16 x 64 would.  us, bf16 int4:
     // 512 x 3001 x 3001 (376 tiles of 64 rows) 141 in tiles of 16 rows, 160 of
@@ -505,7 +489,7 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hip
     int bm = shape == MANY ? GM : GM_FEW;
     bool narrow = false;
     if (stream) {
-        bm = 16;
+        bm = stream;
     } else if (fits) {
         pick_tile(a, oc, bm, narrow);
     }
@@ -520,7 +504,7 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hip
         if (e != hipSuccess) return e;
         ws = static_cast<char *>(ws) + align256((size_t)max_tiles(a.R, a.E, 16) * sizeof(RowTile));
     }
-    if (stream) return launch_stream(fmt, a, tiles, (int)mt, st);
+    if (stream) return launch_stream(fmt, a, stream, tiles, (int)mt, st);
     if (fits) return launch_tile(fmt, a, narrow, bm, tiles, (int)mt, ws, st);
     const int bn = shape == THIN ? GN_THIN : GN;
     const long long grid = mt * ((oc + bn - 1) / bn);

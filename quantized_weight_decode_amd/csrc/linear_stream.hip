@@ -1,4 +1,4 @@
-// linear_stream.hip -- up to 16 rows of x times packed weights, bound by the
+// linear_stream.hip -- few rows of x times packed weights, bound by the
 // weights' bytes, dense or grouped by expert, with the epilogue.
 #include "qg_device.h"
 #include "qg_launch.h"
@@ -212,7 +212,7 @@ struct StreamArgs {
     int ntn;
 };
 
-// Stream kernel.  A workgroup of 8 waves makes up to 16 rows of y x 16 NB
+// Stream kernel.  A workgroup of 8 waves makes up to ROWS rows of y x 16 NB
 // rows of W; the waves take blocks of P chunks of 128 columns in turn, and
 // their sums are joined through LDS in a fixed order.
 // v_mfma_f32_16x16x32_bf16, lane l: A row of x l % 16, B row of W l % 16, eight
@@ -231,7 +231,7 @@ struct StreamArgs {
 // instructions per weight: an outlier of x at a zero weight must not cost the
 // small elements their bits.
 //
-// ROWS = 16: x goes to LDS as it is in memory, and each fragment is turned into
+// ROWS = 16 or 32: x goes to LDS as it is in memory, and each fragment is turned into
 // bf16 parts as it is read; three parts of f32 take three matrix instructions.
 // ROWS = 4 (dense): the parts are made on the way to LDS, once per element
 // instead of once per lane of a fragment, and the three parts of four rows are
@@ -247,6 +247,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     typedef typename XT::raw raw;
     typedef XFrag<XT, FMT> Frag;
     constexpr bool FEW = ROWS == 4;
+    constexpr int MT = FEW ? 1 : ROWS / 16;              // row tiles
     constexpr int NP = FEW ? 1 : Frag::NP;               // matrix instructions per step
     constexpr int XQ = FEW ? Frag::NP : 1;               // parts of x beside each other
     constexpr bool OFFSET = FMT == FMT_I4G && Frag::NP == 1;
@@ -266,7 +267,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     constexpr int LDR = NB * 16 + 4;
     constexpr int WB = NB * 16 * WROW, SB = SL * 256;
     constexpr int WAVE_LDS = WB + SB + ROWS * XQ * XROW;
-    constexpr int RED = SW * 16 * LDR * 4;
+    constexpr int RED = SW * 16 * MT * LDR * 4;
     __shared__ __align__(16) char smem[SW * WAVE_LDS > RED ? SW * WAVE_LDS : RED];
     const LinearArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     float *const sl = reinterpret_cast<float *>(wl + WB);
     char *const xl = wl + WB + SB;
     if (!FEW)                                            // rows past the tile's: zero
-        for (int i = lane; i < 16 * XROW / 16; i += 64)
+        for (int i = lane; i < ROWS * XROW / 16; i += 64)
             reinterpret_cast<u32x4 *>(xl)[i] = u32x4{0, 0, 0, 0};
 
     u32x4 wr[WL], xr[P][XL];
@@ -381,9 +382,11 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
         }
     };
 
-    f32x4v acc[NB];
+    f32x4v acc[MT][NB];
 #pragma unroll
-    for (int n = 0; n < NB; n++) acc[n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+        for (int n = 0; n < NB; n++) acc[m][n] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
 
     auto multiply = [&](int q) {                         // chunk q of the block
         uint32_t wd[NB][WC];
@@ -400,30 +403,36 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
         }
 #pragma unroll
         for (int g = 0; g < NG; g++) {
-            bf16x8 xv[TPG][NP];
+            bf16x8 xv[MT][TPG][NP];
+            f32x4v z[MT];
 #pragma unroll
-            for (int s = 0; s < TPG; s++) {
-                const int st = g * TPG + s;
-                const int k = FMT == FMT_I4G ? 32 * st + 8 * lg
-                                             : 64 * (st >> 1) + 16 * lg + 8 * (st & 1);
-                if (FEW)                                 // rows behind the last repeat others
-                    xv[s][0] = *reinterpret_cast<const bf16x8 *>(
-                        xl + (li % (ROWS * XQ)) * XROW + (q * SC + k) * 2);
-                else
-                    Frag::parts(xl + li * XROW + k * sizeof(raw), xv[s]);
-            }
-            f32x4v z = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (OFFSET) {
-                const u32x4 m24 = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
+            for (int m = 0; m < MT; m++) {
 #pragma unroll
-                for (int s = 0; s < TPG; s++)
-                    z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        xv[s][0], __builtin_bit_cast(bf16x8, m24), z, 0, 0, 0);
+                for (int s = 0; s < TPG; s++) {
+                    const int st = g * TPG + s;
+                    const int k = FMT == FMT_I4G ? 32 * st + 8 * lg
+                                                 : 64 * (st >> 1) + 16 * lg + 8 * (st & 1);
+                    if (FEW)                             // rows behind the last repeat others
+                        xv[m][s][0] = *reinterpret_cast<const bf16x8 *>(
+                            xl + (li % (ROWS * XQ)) * XROW + (q * SC + k) * 2);
+                    else
+                        Frag::parts(xl + (16 * m + li) * XROW + k * sizeof(raw), xv[m][s]);
+                }
+                z[m] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+                if (OFFSET) {
+                    const u32x4 m24 = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
+#pragma unroll
+                    for (int s = 0; s < TPG; s++)
+                        z[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            xv[m][s][0], __builtin_bit_cast(bf16x8, m24), z[m], 0, 0, 0);
+                }
             }
 #pragma unroll
             for (int n = 0; n < NB; n++) {
                 const float sc = sl[(n * 16 + li) * NGB + q * NG + g];
-                f32x4v sum = z;
+                f32x4v sum[MT];
+#pragma unroll
+                for (int m = 0; m < MT; m++) sum[m] = z[m];
 #pragma unroll
                 for (int s = 0; s < TPG; s++) {
                     const int st = g * TPG + s;
@@ -436,11 +445,17 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
                         wv = join(cvt_lo<0>(p0), cvt_hi<0>(p0), cvt_lo<0>(p1), cvt_hi<0>(p1));
                     }
 #pragma unroll
-                    for (int q = NP - 1; q >= 0; q--)    // small parts first
-                        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[s][q], wv, sum, 0, 0, 0);
+                    for (int m = 0; m < MT; m++)
+#pragma unroll
+                        for (int q = NP - 1; q >= 0; q--)    // small parts first
+                            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[m][s][q], wv,
+                                                                             sum[m], 0, 0, 0);
                 }
 #pragma unroll
-                for (int r = 0; r < 4; r++) acc[n][r] = fmaf(sc, sum[r], acc[n][r]);
+                for (int m = 0; m < MT; m++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        acc[m][n][r] = fmaf(sc, sum[m][r], acc[m][n][r]);
             }
             if (NG == 4) __builtin_amdgcn_sched_barrier(0);    // keeps registers down
         }
@@ -467,11 +482,14 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     }
 
     __syncthreads();
-    float (*const red)[16][LDR] = reinterpret_cast<float (*)[16][LDR]>(smem);
+    float (*const red)[16 * MT][LDR] = reinterpret_cast<float (*)[16 * MT][LDR]>(smem);
 #pragma unroll
-    for (int n = 0; n < NB; n++)
+    for (int m = 0; m < MT; m++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) red[wave][4 * lg + r][n * 16 + li] = acc[n][r];
+        for (int n = 0; n < NB; n++)
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                red[wave][16 * m + 4 * lg + r][n * 16 + li] = acc[m][n][r];
     __syncthreads();
     finish<XT, 2>(a, t.expert, tid, SW * 64, t.n * YC,
                   [&](int i, int &row, int &col, float &v, float &up) {
@@ -493,10 +511,12 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
                   });
 }
 
-bool few_rows(const LinearArgs &a) { return !a.offsets && a.R <= 4; }
+// Row blocks that 32 rows leave registers for (int4, four blocks: 360 bytes of
+// them spilled, 32 x 4096 x 14336 21.2 us, the narrow kernel 16.9).
+constexpr int wide_blocks(int fmt) { return fmt == FMT_I4G ? 3 : 4; }
 
 template <int FMT, typename XT, int NB, bool GATED>
-void run_nb(const StreamArgs &p, unsigned grid, hipStream_t st)
+void run_nb(const StreamArgs &p, int rows, unsigned grid, hipStream_t st)
 {
     constexpr int P = FMT == FMT_I4G ? 2 : 1;
 #define QG_RUN_R(FG, ROWS)                                                                  \
@@ -504,8 +524,10 @@ void run_nb(const StreamArgs &p, unsigned grid, hipStream_t st)
                        dim3(SW * 64), 0, st, p)
 #define QG_RUN(FG)                                                                          \
     do {                                                                                    \
-        if (few_rows(p.a)) QG_RUN_R(FG, 4);                                                 \
-        else QG_RUN_R(FG, 16);                                                              \
+        if (rows == 4) QG_RUN_R(FG, 4);                                                     \
+        else if (rows == 16) QG_RUN_R(FG, 16);                                              \
+        else if constexpr (sizeof(typename XT::raw) == 2 && NB <= wide_blocks(FMT))         \
+            QG_RUN_R(FG, 32);                                                               \
     } while (0)
     if constexpr (FMT == FMT_FP8) {
         QG_RUN(128);
@@ -519,32 +541,55 @@ void run_nb(const StreamArgs &p, unsigned grid, hipStream_t st)
 }
 
 template <int FMT, typename XT>
-void run_stream(const StreamArgs &p, int nb, unsigned grid, hipStream_t st)
+void run_stream(const StreamArgs &p, int rows, int nb, unsigned grid, hipStream_t st)
 {
     if (p.a.gated) {
-        if (nb == 4) run_nb<FMT, XT, 4, true>(p, grid, st);
-        else run_nb<FMT, XT, 2, true>(p, grid, st);
+        if (nb == 4) run_nb<FMT, XT, 4, true>(p, rows, grid, st);
+        else run_nb<FMT, XT, 2, true>(p, rows, grid, st);
     } else if (nb == 4) {
-        run_nb<FMT, XT, 4, false>(p, grid, st);
+        run_nb<FMT, XT, 4, false>(p, rows, grid, st);
     } else if (nb == 3) {
-        run_nb<FMT, XT, 3, false>(p, grid, st);
+        run_nb<FMT, XT, 3, false>(p, rows, grid, st);
     } else if (nb == 2) {
-        run_nb<FMT, XT, 2, false>(p, grid, st);
+        run_nb<FMT, XT, 2, false>(p, rows, grid, st);
     } else {
-        run_nb<FMT, XT, 1, false>(p, grid, st);
+        run_nb<FMT, XT, 1, false>(p, rows, grid, st);
     }
 }
 
 }  // namespace
 
-bool stream_fits(WeightFormat fmt, const LinearArgs &a)
+// Up to 16 rows, and more while all workgroups fit the GPU at once, with 16 or
+// (bf16) 32 rows each; a grouped bf16 product up to 9 rows for an expert on
+// average, a grouped f32 one up to 8 in all.  us, this kernel and tiles:
+// 16 rows: bf16, 64 x 4096 x 4096 10.8 and 15.4, 96 x 4096 x 4096 (384 workgroups)
+// 20.4 and 15.8; 32 x 7168 x 2048 8.7 and 20.5; f32, 64 x 4096 x 4096 17.5 and 20.6,
+// 64 x 14336 x 4096 48.2 and 47.7, 32 x 2048 x 6144 9.6 and 13.8.
+// 32 rows: int4, 17 x 6144 x 12288 16.1 and 19.8, 32 x 6144 x 12288 18.7 and 20.8
+// (two of 16 rows 26.4), 64 x 2048 x 6144 9.4 and 11.6; fp8, 32 x 7168 x 16384 25.8
+// and 33.1, 64 x 16384 x 7168 44.8 and 52.0.
+// Grouped bf16, 7168 x 2048, 256 experts: 128 tokens of 8 (4 rows) 396 and 465,
+// 256 (8) 531 and 557, 320 (10) 591 and 574, 512 (16) 789 and 622; 2048 x 1024,
+// 32 experts: 8 rows 24.1 and 27.7, 10 rows 32.2 and 28.8.
+// Grouped f32, 2048 x 4096, 8 experts: 2 rows in all 11.6 and 14.9, 8 rows 20.4 and
+// 21.0, 16 rows 27.1 and 24.8; 7168 x 2048, 64 rows 200 and 154.
+int stream_rows(WeightFormat fmt, const LinearArgs &a)
 {
     const int el = a.dtype == QGEMV_BF16 ? 2 : 4;
-    return tile_fits(fmt, a) && (((uintptr_t)a.x | (uintptr_t)(a.ldx * el)) & 15) == 0;
+    if (!tile_fits(fmt, a) || (((uintptr_t)a.x | (uintptr_t)(a.ldx * el)) & 15) != 0) return 0;
+    if (a.offsets) {
+        const bool few = a.dtype == QGEMV_BF16 ? a.R <= 9 * (long long)a.E : a.R <= 8;
+        return few ? 16 : 0;
+    }
+    if (a.R <= 4) return 4;
+    const long long ncu = cu_count(), O = a.O;
+    if (a.R <= 16 || (a.R + 15) / 16 * ((O + 63) / 64) <= ncu) return 16;
+    const int cols = a.gated ? wide_blocks(fmt) / 2 * 32 : wide_blocks(fmt) * 16;
+    return a.dtype == QGEMV_BF16 && (a.R + 31) / 32 * ((O + cols - 1) / cols) <= ncu ? 32 : 0;
 }
 
-hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, const RowTile *tiles, int ntm,
-                         hipStream_t st)
+hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, int rows, const RowTile *tiles,
+                         int ntm, hipStream_t st)
 {
     // Row blocks per workgroup: the count that leaves the busiest CU the least to
     // do, a workgroup of 16 rows of x counted as its row blocks and 1.5 for its x
@@ -555,15 +600,15 @@ hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, const RowTile *t
     // blocks 13.0; f32 16.3 and 16.0; fp8 1 x 7168 x 16384: 22.7, four 21.4).
     const int oc = a.gated ? a.O / 2 : a.O;
     const long long ncu = cu_count();
-    const bool small = few_rows(a) && fmt == FMT_I4G && a.dtype == QGEMV_BF16;
+    const bool small = rows == 4 && fmt == FMT_I4G && a.dtype == QGEMV_BF16;
     int best = 0, ntn = 0;
     double cost = 0.0;
-    for (int nb = 4; nb >= 1; nb--) {
+    for (int nb = rows == 32 ? wide_blocks(fmt) : 4; nb >= 1; nb--) {
         if (a.gated && (nb & 1)) continue;
         const int yc = a.gated ? nb * 8 : nb * 16;
         const int n = (oc + yc - 1) / yc;
         const double c = (double)(((long long)n * ntm + ncu - 1) / ncu) *
-                         (nb + (few_rows(a) ? 0.0 : 1.5));
+                         (nb + (rows == 4 ? 0.0 : 1.5));
         if (!best || c < cost || (c == cost && small)) {
             best = nb;
             cost = c;
@@ -574,11 +619,11 @@ hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, const RowTile *t
     const long long grid = (long long)ntm * ntn;
     if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     if (fmt == FMT_I4G) {
-        if (a.dtype == QGEMV_BF16) run_stream<FMT_I4G, BF16>(p, best, (unsigned)grid, st);
-        else run_stream<FMT_I4G, F32>(p, best, (unsigned)grid, st);
+        if (a.dtype == QGEMV_BF16) run_stream<FMT_I4G, BF16>(p, rows, best, (unsigned)grid, st);
+        else run_stream<FMT_I4G, F32>(p, rows, best, (unsigned)grid, st);
     } else {
-        if (a.dtype == QGEMV_BF16) run_stream<FMT_FP8, BF16>(p, best, (unsigned)grid, st);
-        else run_stream<FMT_FP8, F32>(p, best, (unsigned)grid, st);
+        if (a.dtype == QGEMV_BF16) run_stream<FMT_FP8, BF16>(p, rows, best, (unsigned)grid, st);
+        else run_stream<FMT_FP8, F32>(p, rows, best, (unsigned)grid, st);
     }
     return hipGetLastError();
 }

@@ -44,10 +44,11 @@ int tile_rows(int I);                    // rows whose packed plane stays below 
 hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int bm,
                        const RowTile *tiles, int ntm, void *ws, hipStream_t st);
 
-// The stream kernels (linear_stream.hip): row tiles of 16.
-bool stream_fits(WeightFormat fmt, const LinearArgs &a);
-hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, const RowTile *tiles, int ntm,
-                         hipStream_t st);
+// The stream kernel (linear_stream.hip): the rows of its tiles for a product, 0
+// where others are better or it does not fit.
+int stream_rows(WeightFormat fmt, const LinearArgs &a);
+hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, int rows, const RowTile *tiles,
+                         int ntm, hipStream_t st);
 
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 

@@ -337,8 +337,10 @@ def test_two_streams_at_once(q):
         assert torch.equal(y, want[c])
 
 
-# more workgroups of 16 rows x 64 rows of W than CUs: the narrow kernel
-NARROW = [(20, 9000), (40, 6100), (100, 2500), (300, 1002)]
+# more workgroups of 16 rows x 64 rows of W than CUs: the stream kernel with 32
+# rows, and the narrow kernel
+NARROW = [(20, 9000), (40, 6100), (100, 2500), (300, 1002),
+          (20, 17000), (40, 8300), (100, 4200), (300, 1702)]
 
 
 @pytest.mark.parametrize("fmt", ["i4g", "fp8"])
