@@ -314,8 +314,8 @@ typedef struct {
  * bf16 x exactly (below 2^-28 of the row's largest within 2^-39 of that).  Few
  * bf16 rows times int4 are summed as (16 + q) x less 24 sum x: each f32 rounding
  * is relative to 24 sum |x| of a scale group, not to sum |(q - 8) x|.
- * Magnitudes of x below 2^120 and of the scales below 2^90 do not overflow on
- * the way.
+ * No finite x overflows on the way where the sum of |x w| of an output is in
+ * f32's range and the scales are below 2^80.
  * A row of x that holds an infinity or NaN gives a row of y without finite
  * sums (infinities may come out as NaN); other rows are not affected.
  * One or two f32 rows without an epilogue run faster through qgemv_i4g (1 x

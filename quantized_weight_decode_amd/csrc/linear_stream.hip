@@ -43,16 +43,26 @@ __device__ __forceinline__ bf16x8 join(bf16x2 a, bf16x2 b, bf16x2 c, bf16x2 d)
     return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-// Four E4M3 codes times 2^e in bf16, exactly.
+// Codes enter the matrix instructions times 2^-k, and a row's scales times 2^k,
+// so that a scale group's sum stays finite for every finite x: with group sums
+// of up to 128 columns in units of max |x|, fp8 448 * 128 < 2^16, int4 q - 8 8 *
+// 128 < 2^11, and int4 16 + q from -24 sum x on 31 * 128 < 2^12 (the partial
+// sums stay within it).  Powers of two: the codes stay exact, and sums below
+// 2^-126 are subnormal, which the matrix instructions keep (to 2^-149).
+constexpr int FP8_DOWN = 16, SIGNED_DOWN = 11, OFFSET_DOWN = 12;
+
+constexpr float pow2(int e) { return e < 0 ? 1.0f / (float)(1 << -e) : (float)(1 << e); }
+
+// Two E4M3 codes times 2^e in bf16, exactly.
 template <int E>
 __device__ __forceinline__ bf16x2 cvt_lo(uint32_t w)
 {
-    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, (float)(1 << E), false);
+    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, pow2(E), false);
 }
 template <int E>
 __device__ __forceinline__ bf16x2 cvt_hi(uint32_t w)
 {
-    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, (float)(1 << E), true);
+    return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, pow2(E), true);
 }
 
 // (w & mask) | bits in one instruction: it takes one scalar operand and no
@@ -66,16 +76,17 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
     return (w & mask) | bits;
 }
 
-// Eight nibbles as 16 + q in bf16 (0x4180 | 8 q), in the column order 0 4 1 5
-// 2 6 3 7.
+// Eight nibbles as (16 + q) 2^-OFFSET_DOWN in bf16 (0x4180 | 8 q is 16 + q), in
+// the column order 0 4 1 5 2 6 3 7; and -24 times the same.
+constexpr uint32_t bf16_pair(uint32_t bits) { return (bits - (OFFSET_DOWN << 7)) * 0x10001u; }
 __device__ __forceinline__ bf16x8 nib8_bf16(uint32_t w)
 {
-    constexpr uint32_t M = 0x00780078u, B = 0x41804180u;
+    constexpr uint32_t M = 0x00780078u, B = bf16_pair(0x4180u);
     const u32x4 o = {and_or(w << 3, M, B), and_or(w >> 1, M, B), and_or(w >> 5, M, B),
                      and_or(w >> 9, M, B)};
     return __builtin_bit_cast(bf16x8, o);
 }
-// Eight nibbles as q - 8, in the column order 0 2 4 6 1 3 5 7.  Read as E4M3
+// Eight nibbles as (q - 8) 2^-SIGNED_DOWN, in the column order 0 2 4 6 1 3 5 7.  Read as E4M3
 // codes, 0..15 are n 2^-9, so bytes of one nibble each convert two at a time.
 // t = the two's complement nibble; its code is t for t < 8,
 // else 0x90 - t (sign bit and 16 - t) = (t ^ 0x8F) + 1.
@@ -90,7 +101,8 @@ __device__ __forceinline__ bf16x8 nib8_bf16_signed(uint32_t w)
     const uint32_t x = w ^ 0x88888888u;
     const uint32_t lo = signed_codes(x & 0x0F0F0F0Fu);
     const uint32_t hi = signed_codes((x >> 4) & 0x0F0F0F0Fu);
-    return join(cvt_lo<9>(lo), cvt_hi<9>(lo), cvt_lo<9>(hi), cvt_hi<9>(hi));
+    constexpr int E = 9 - SIGNED_DOWN;
+    return join(cvt_lo<E>(lo), cvt_hi<E>(lo), cvt_lo<E>(hi), cvt_hi<E>(hi));
 }
 
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b)
@@ -251,6 +263,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
     constexpr int NP = FEW ? 1 : Frag::NP;               // matrix instructions per step
     constexpr int XQ = FEW ? Frag::NP : 1;               // parts of x beside each other
     constexpr bool OFFSET = FMT == FMT_I4G && Frag::NP == 1;
+    constexpr float UP = pow2(FMT == FMT_FP8 ? FP8_DOWN : OFFSET ? OFFSET_DOWN : SIGNED_DOWN);
     constexpr int NG = SC / FG;                          // scale groups of a chunk
     constexpr int TPG = 4 / NG;                          // 32-column steps of a group
     constexpr int WC = FMT == FMT_FP8 ? 8 : 4;           // 16-byte pieces of a row and chunk
@@ -364,7 +377,7 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
             *reinterpret_cast<u32x4 *>(wl + ((lane + 64 * i) / WP) * WROW + (lane % WP) * 16) =
                 wr[i];
 #pragma unroll
-        for (int i = 0; i < SL; i++) sl[lane + 64 * i] = sr[i];
+        for (int i = 0; i < SL; i++) sl[lane + 64 * i] = sr[i] * UP;
     };
     auto store_x = [&](int c, int q) {
 #pragma unroll
@@ -420,7 +433,8 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
                 }
                 z[m] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
                 if (OFFSET) {
-                    const u32x4 m24 = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};
+                    constexpr uint32_t M = bf16_pair(0xC1C0u);
+                    const u32x4 m24 = {M, M, M, M};
 #pragma unroll
                     for (int s = 0; s < TPG; s++)
                         z[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -442,7 +456,8 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
                     } else {
                         const uint32_t p0 = wd[n][(2 * st) % WC];
                         const uint32_t p1 = wd[n][(2 * st + 1) % WC];
-                        wv = join(cvt_lo<0>(p0), cvt_hi<0>(p0), cvt_lo<0>(p1), cvt_hi<0>(p1));
+                        constexpr int E = -FP8_DOWN;
+                        wv = join(cvt_lo<E>(p0), cvt_hi<E>(p0), cvt_lo<E>(p1), cvt_hi<E>(p1));
                     }
 #pragma unroll
                     for (int m = 0; m < MT; m++)
