@@ -318,11 +318,14 @@ def _out(out, S, O, like):
     return out
 
 
+_MAX_DIM = 1 << 24
+
+
 def _gs(gs):
     import operator
     gs = operator.index(gs)
-    if gs < 2 or gs % 2:
-        raise QgemvError("argument check", 3, "group size must be an even number >= 2")
+    if gs < 2 or gs % 2 or gs > _MAX_DIM:               # (above 2^31 the C call would wrap)
+        raise QgemvError("argument check", 3, "group size must be an even number in 2 .. 2^24")
     return gs
 
 
