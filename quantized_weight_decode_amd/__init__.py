@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import operator
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -322,7 +323,6 @@ _MAX_DIM = 1 << 24
 
 
 def _gs(gs):
-    import operator
     gs = operator.index(gs)
     if gs < 2 or gs % 2 or gs > _MAX_DIM:               # (above 2^31 the C call would wrap)
         raise QgemvError("argument check", 3, "group size must be an even number in 2 .. 2^24")
@@ -549,6 +549,12 @@ def moe_topk_error(workspace):
 _NO_GUARD = contextlib.nullcontext()
 
 
+def _sizes(fn, *sizes):
+    """Refuses sizes that no call takes, before a C int could wrap them."""
+    if max(sizes) > _MAX_DIM or min(sizes) < 0:
+        raise QgemvError(fn, 2, strerror(2))
+
+
 def _on(device):
     """Makes `device` current for a launch (nothing to do where it is)."""
     cuda = _torch().cuda
@@ -651,6 +657,7 @@ def _linear(fn, w, scales, x, gs, bias, act, gated, residual, workspace, out):
     S, I = x.shape
     O = _i4g_check(w, scales, x, gs, S, I) if gs is not None else _fp8_check(w, scales, I,
                                                                              "scale_inv")
+    _sizes(fn, S, I, O)
     _one_device(w, scales, x, bias, residual, workspace, out)
     xp, ldx = _rows(x, "x", x.dtype)
     epi, oc = _epilogue(x.dtype, O, bias, act, gated, residual, S)
@@ -698,9 +705,11 @@ def moe_group(ids, E, workspace=None):
     if ids.dim() != 2:
         raise ValueError("ids must be [T, K]")
     T, K = ids.shape
+    E = operator.index(E)
+    _sizes("qgemv_moe_group", T, K, E)
     _one_device(ids, workspace)
     ip = _dev(ids, "ids", torch.int32)
-    offsets = torch.empty(min(max(int(E), 0), 1024) + 1, dtype=torch.int32, device=ids.device)
+    offsets = torch.empty(min(E, 1024) + 1, dtype=torch.int32, device=ids.device)
     tokens = torch.empty(T * K, dtype=torch.int32, device=ids.device)
     pos = torch.empty((T, K), dtype=torch.int32, device=ids.device)
     with _on(ids.device):
@@ -733,6 +742,7 @@ def i4g_grouped(w, scales, x, offsets, gs, rows=None, bias=None, act=None, gated
     E, O = w.shape[0], w.shape[1]
     T, I = x.shape
     R = T if rows is None else rows.numel()
+    _sizes("qgemv_i4g_grouped", T, R, E, I, O)
     _shape(w, "w", (E, O, (I + 1) // 2))
     _shape(scales, "scales", (E, O, (I + gs - 1) // gs))
     _shape(offsets, "offsets", (E + 1,))
@@ -763,6 +773,7 @@ def moe_combine(h, pos, gates, residual=None, out=None):
         raise ValueError("h must be [R, O] and pos [T, K]")
     T, K = pos.shape
     R, O = h.shape
+    _sizes("qgemv_moe_combine", T, K, R, O)
     _shape(gates, "gates", (T, K))
     _one_device(h, pos, gates, residual, out)
     hp, ldh = _rows(h, "h", h.dtype)

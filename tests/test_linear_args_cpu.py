@@ -33,3 +33,30 @@ def test_group_size_that_a_c_int_would_wrap(q, gs):
     with pytest.raises(q.QgemvError):
         q.i4g(meta(8, 512), meta(8, 1, dtype=torch.float32),
               meta(3, 1024, dtype=torch.float32), gs)
+
+
+BIG = (1 << 32) + 3          # 3 as a C int
+
+
+def test_sizes_that_a_c_int_would_wrap(q):
+    """Refused by name; a call with the wrapped sizes would fill three rows of
+    the output, or sort by other experts."""
+    f32, i32 = {"dtype": torch.float32}, {"dtype": torch.int32}
+
+    def refused(f, *a, **k):
+        with pytest.raises(q.QgemvError) as e:
+            f(*a, **k)
+        assert e.value.status == 2
+    refused(q.i4g_linear, meta(8, 32), meta(8, 2, **f32), meta(BIG, 64, **f32), 32)
+    refused(q.fp8b128_linear, meta(8, 64), meta(1, 1, **f32), meta(BIG, 64, **f32))
+    refused(q.i4g_linear, meta(BIG, 32), meta(BIG, 2, **f32), meta(3, 64, **f32), 32)
+    refused(q.i4g_grouped, meta(2, 8, 32), meta(2, 8, 2, **f32), meta(BIG, 64, **f32),
+            meta(3, **i32), 32)
+    refused(q.i4g_grouped, meta(2, 8, 32), meta(2, 8, 2, **f32), meta(3, 64, **f32),
+            meta(3, **i32), 32, rows=meta(BIG, **i32))
+    refused(q.moe_group, meta(4, 2, **i32), BIG)
+    refused(q.moe_group, meta(4, 2, **i32), 3 - (1 << 32))
+    refused(q.moe_group, meta(BIG, 2, **i32), 8)
+    refused(q.moe_combine, meta(BIG, 8, **f32), meta(4, 2, **i32), meta(4, 2, **f32))
+    refused(q.moe_combine, meta(4, 8, **f32), meta(BIG, 2, **i32), meta(BIG, 2, **f32))
+    refused(q.moe_combine, meta(4, BIG, **f32), meta(4, 2, **i32), meta(4, 2, **f32))
