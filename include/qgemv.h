@@ -36,8 +36,10 @@ typedef enum {
     QGEMV_E_IDS = 6,       /* expert strides too small for one expert         */
     QGEMV_E_WORKSPACE = 7, /* workspace NULL or smaller than required         */
     QGEMV_E_HIP = 8,       /* the HIP runtime reported an error at launch     */
-    QGEMV_E_ARG = 9        /* unknown type or activation, or an epilogue term
+    QGEMV_E_ARG = 9,       /* unknown type or activation, or an epilogue term
                               that this call does not take                    */
+    QGEMV_E_OVERLAP = 10   /* an output or the workspace overlaps another
+                              operand (products with an epilogue, routing)    */
 } qgemv_status;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -301,7 +303,8 @@ typedef struct {
  * rows of x (S = 0 launches nothing and accepts any pointers).
  *   x  dtype [S] rows of I, ldx >= I elements apart;  y dtype [S] rows of O
  *   (gated: O/2), ldy elements apart; nothing between or behind the rows is
- *   read or written.  y must not overlap x, the weights or the bias.
+ *   read or written.  y must not overlap what the call reads (columns of one
+ *   buffer may be x and others y), but for the residual in place.
  *   x, y, bias and residual are aligned to their element, w to a byte.
  *   workspace  device scratch of qgemv_linear_workspace bytes, 256-byte
  *              aligned, overwritten; calls that may overlap in time (two
@@ -351,6 +354,7 @@ int qgemv_fp8b128_linear(const void *w, const float *scale_inv, const void *x, l
  *   1 <= E <= 1024, K >= 1, T * K <= 2^24; T = 0 gives all-zero offsets
  *   workspace  qgemv_moe_group_workspace bytes (may be 0: then it may be
  *              NULL), 4-byte aligned, overwritten
+ *   the buffers must not overlap each other
  */
 size_t qgemv_moe_group_workspace(int T, int K, int E);
 int qgemv_moe_group(const int32_t *ids, int T, int K, int E, int32_t *offsets, int32_t *tokens,
@@ -385,7 +389,8 @@ int qgemv_i4g_grouped(const void *w, const float *scales, long long w_stride, lo
  *   h        dtype [R] rows of O, ldh elements apart
  *   pos      int32 [T][K] as qgemv_moe_group gives; an index outside [0, R)
  *            makes row t of y NaN (it is never dereferenced)
- *   gates    f32 [T][K];  residual dtype rows ldr apart, or NULL (may be y)
+ *   gates    f32 [T][K];  residual dtype rows ldr apart, or NULL (may be y:
+ *            same pointer and stride); y must not overlap h, pos or gates
  *   T = 0 launches nothing; 1 <= K <= 64
  */
 int qgemv_moe_combine(const void *h, long long ldh, int R, const int32_t *pos,

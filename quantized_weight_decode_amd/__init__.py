@@ -544,8 +544,9 @@ def moe_topk_error(workspace):
 # -- products with an epilogue, routed slots -------------------------------
 # x, bias, residual and y of one call share a type, float32 or bfloat16.
 # x, residual, h and a caller's out may be row-strided views (columns
-# contiguous); everything else is contiguous.  The launch goes to the device
-# of the tensors, on its current stream.
+# contiguous); everything else is contiguous.  out must not share elements with
+# another argument, but for residual, which may be out itself.  The launch goes
+# to the device of the tensors, on its current stream.
 _NO_GUARD = contextlib.nullcontext()
 
 

@@ -136,6 +136,7 @@ const char *qgemv_strerror(int status)
     case QGEMV_E_WORKSPACE: return "workspace is NULL or too small";
     case QGEMV_E_HIP: return "the HIP runtime reported an error at launch";
     case QGEMV_E_ARG: return "unknown type or activation, or an epilogue term this call does not take";
+    case QGEMV_E_OVERLAP: return "an output or the workspace overlaps another operand";
     default: return "unknown status";
     }
 }

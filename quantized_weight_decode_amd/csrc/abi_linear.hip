@@ -4,8 +4,15 @@
 // As in abi.hip, validation looks at pointer values, dimensions and sizes
 // only, so a refused call is safe with any pointers.
 #include "qg_linear.h"
+#include "qg_rows.h"
 
 namespace {
+
+using qg::Rows;
+using qg::block;
+using qg::overlap;
+using qg::overlaps_any;
+using qg::rows_of;
 
 constexpr int MAX_DIM = 1 << 24;
 constexpr int MAX_EXPERTS = 1024;
@@ -21,6 +28,27 @@ int element(int dtype) { return dtype == QGEMV_BF16 ? 2 : 4; }
 bool bad_sizes(int rows, int I, int O)
 {
     return rows < 0 || rows > MAX_DIM || I < 1 || O < 1 || I > MAX_DIM || O > MAX_DIM;
+}
+
+// y against what a product reads (the residual may be y itself), and the
+// scratch against both.
+bool overlapping(const qg::LinearArgs &a, long long w_bytes, long long s_bytes,
+                 const void *workspace, size_t ws_bytes)
+{
+    const long long el = a.dtype == QGEMV_BF16 ? 2 : 4, oc = a.gated ? a.O / 2 : a.O;
+    const Rows y = rows_of(a.y, a.R, oc * el, a.ldy * el);
+    const Rows res = rows_of(a.residual, a.R, oc * el, a.ldr * el);
+    const Rows in[] = {rows_of(a.x, a.T, a.I * el, a.ldx * el),
+                       rows_of(a.w, a.E, w_bytes, a.offsets ? a.w_stride : w_bytes),
+                       rows_of(a.scales, a.E, s_bytes, a.offsets ? a.s_stride * 4 : s_bytes),
+                       block(a.bias, (long long)a.E * a.O * el),
+                       block(a.rows, (long long)a.R * 4),
+                       block(a.offsets, (long long)(a.E + 1) * 4)};
+    constexpr int N = sizeof(in) / sizeof(in[0]);
+    const Rows ws = block(workspace, (long long)ws_bytes);
+    const bool in_place = a.residual == a.y && (a.R == 1 || a.ldr == a.ldy);
+    return overlaps_any(y, in, N) || (!in_place && overlap(y, res)) || overlap(y, ws) ||
+           overlap(res, ws) || overlaps_any(ws, in, N);
 }
 
 // 16 x 16 tiles of y, the smallest of all kernels, must fit a launch
@@ -75,9 +103,12 @@ int dense(qg::WeightFormat fmt, const void *w, const float *scales, const void *
     if (int e = take(a, epilogue, true)) return e;
     if (S == 0) return QGEMV_OK;
     if (too_many_tiles((S + 15) / 16, O)) return QGEMV_E_DIMS;
-    if (!workspace || misaligned(workspace, 256) ||
-        ws_bytes < qg::linear_workspace(S, S, 0, I, O, dtype))
-        return QGEMV_E_WORKSPACE;
+    const size_t need = qg::linear_workspace(S, S, 0, I, O, dtype);
+    if (!workspace || misaligned(workspace, 256) || ws_bytes < need) return QGEMV_E_WORKSPACE;
+    const bool i4 = fmt == qg::FMT_I4G;
+    if (overlapping(a, (long long)O * (i4 ? (I + 1) / 2 : I),
+                    4LL * a.ng * (i4 ? O : (O + 127) / 128), workspace, need))
+        return QGEMV_E_OVERLAP;
     return launched(qg::launch_linear(fmt, a, workspace, (hipStream_t)stream));
 }
 
@@ -153,9 +184,9 @@ int qgemv_i4g_grouped(const void *w, const float *scales, long long w_stride, lo
     if (int e = take(a, epilogue, false)) return e;
     if (R == 0) return QGEMV_OK;
     if (too_many_tiles((long long)R / 16 + (E < R ? E : R), O)) return QGEMV_E_DIMS;
-    if (!workspace || misaligned(workspace, 256) ||
-        ws_bytes < qg::linear_workspace(T, R, E, I, O, dtype))
-        return QGEMV_E_WORKSPACE;
+    const size_t need = qg::linear_workspace(T, R, E, I, O, dtype);
+    if (!workspace || misaligned(workspace, 256) || ws_bytes < need) return QGEMV_E_WORKSPACE;
+    if (overlapping(a, O * rb, 4 * O * ng, workspace, need)) return QGEMV_E_OVERLAP;
     return launched(qg::launch_linear(qg::FMT_I4G, a, workspace, (hipStream_t)stream));
 }
 
@@ -177,6 +208,11 @@ int qgemv_moe_group(const int32_t *ids, int T, int K, int E, int32_t *offsets, i
     const size_t need = qg::moe_group_workspace(T, K, E);
     if (need > 0 && (!workspace || misaligned(workspace, 4) || ws_bytes < need))
         return QGEMV_E_WORKSPACE;
+    const long long n = 4LL * T * K;
+    const Rows all[] = {block(ids, n), block(offsets, 4LL * (E + 1)), block(tokens, n),
+                        block(pos, n), block(workspace, (long long)need)};
+    for (int i = 1; i < 5; i++)
+        if (overlaps_any(all[i], all, i)) return QGEMV_E_OVERLAP;
     return launched(qg::launch_moe_group(ids, T, K, E, offsets, tokens, pos, workspace,
                                          (hipStream_t)stream));
 }
@@ -195,6 +231,14 @@ int qgemv_moe_combine(const void *h, long long ldh, int R, const int32_t *pos,
         misaligned(pos, 4) || misaligned(gates, 4))
         return QGEMV_E_ALIGN;
     if (T == 0) return QGEMV_OK;
+    const long long n = 4LL * T * K;
+    const Rows yr = rows_of(y, T, O * (long long)el, ldy * (long long)el);
+    const Rows in[] = {rows_of(h, R, O * (long long)el, ldh * (long long)el), block(pos, n),
+                       block(gates, n)};
+    const bool in_place = residual == y && (T == 1 || ldr == ldy);
+    if (overlaps_any(yr, in, 3) ||
+        (!in_place && overlap(yr, rows_of(residual, T, O * (long long)el, ldr * (long long)el))))
+        return QGEMV_E_OVERLAP;
     return launched(qg::launch_moe_combine(h, ldh, R, pos, gates, T, K, O, residual, ldr, y, ldy,
                                            dtype, (hipStream_t)stream));
 }
