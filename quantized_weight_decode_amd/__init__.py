@@ -11,7 +11,8 @@ Two layers:
   ``i4g_linear``, ``fp8b128_linear``, ``moe_group``, ``i4g_grouped``,
   ``moe_combine`` -- take torch tensors on the current CUDA (HIP) device, allocate the output
   with ``torch.empty``, launch on ``torch.cuda.current_stream()`` and raise
-  ``QgemvError`` on a refusal.
+  ``QgemvError`` on a refusal.  No call records a gradient; the products with
+  an epilogue and ``moe_combine`` refuse arguments that ask for one.
 """
 from __future__ import annotations
 
@@ -546,7 +547,8 @@ def moe_topk_error(workspace):
 # x, residual, h and a caller's out may be row-strided views (columns
 # contiguous); everything else is contiguous.  out must not share elements with
 # another argument, but for residual, which may be out itself.  The launch goes
-# to the device of the tensors, on its current stream.
+# to the device of the tensors, on its current stream.  There is no backward pass: a call that
+# autograd would have to record is refused (torch.no_grad(), or detach()).
 _NO_GUARD = contextlib.nullcontext()
 
 
@@ -554,6 +556,14 @@ def _sizes(fn, *sizes):
     """Refuses sizes that no call takes, before a C int could wrap them."""
     if max(sizes) > _MAX_DIM or min(sizes) < 0:
         raise QgemvError(fn, 2, strerror(2))
+
+
+def _no_gradient(*ts):
+    if _torch().is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                raise ValueError("an argument requires a gradient, and this call has no backward "
+                                 "pass: detach it or use torch.no_grad()")
 
 
 def _on(device):
@@ -659,6 +669,7 @@ def _linear(fn, w, scales, x, gs, bias, act, gated, residual, workspace, out):
     O = _i4g_check(w, scales, x, gs, S, I) if gs is not None else _fp8_check(w, scales, I,
                                                                              "scale_inv")
     _sizes(fn, S, I, O)
+    _no_gradient(scales, x, bias, residual, out)
     _one_device(w, scales, x, bias, residual, workspace, out)
     xp, ldx = _rows(x, "x", x.dtype)
     epi, oc = _epilogue(x.dtype, O, bias, act, gated, residual, S)
@@ -749,6 +760,7 @@ def i4g_grouped(w, scales, x, offsets, gs, rows=None, bias=None, act=None, gated
     _shape(offsets, "offsets", (E + 1,))
     if rows is not None:
         _shape(rows, "rows", (R,))
+    _no_gradient(scales, x, bias, out)
     _one_device(w, scales, x, offsets, rows, bias, workspace, out)
     xp, ldx = _rows(x, "x", x.dtype)
     epi, oc = _epilogue(x.dtype, O, bias, act, gated, None, R, E)
@@ -776,6 +788,7 @@ def moe_combine(h, pos, gates, residual=None, out=None):
     R, O = h.shape
     _sizes("qgemv_moe_combine", T, K, R, O)
     _shape(gates, "gates", (T, K))
+    _no_gradient(h, gates, residual, out)
     _one_device(h, pos, gates, residual, out)
     hp, ldh = _rows(h, "h", h.dtype)
     rp, ldr = _rows(residual, "residual", h.dtype, (T, O)) if residual is not None else (None, 0)

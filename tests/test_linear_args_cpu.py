@@ -60,3 +60,32 @@ def test_sizes_that_a_c_int_would_wrap(q):
     refused(q.moe_combine, meta(BIG, 8, **f32), meta(4, 2, **i32), meta(4, 2, **f32))
     refused(q.moe_combine, meta(4, 8, **f32), meta(BIG, 2, **i32), meta(BIG, 2, **f32))
     refused(q.moe_combine, meta(4, BIG, **f32), meta(4, 2, **i32), meta(4, 2, **f32))
+
+
+def test_arguments_that_ask_for_a_gradient(q):
+    """There is no backward pass: refused in grad mode, not detached silently;
+    without it the call goes on (to the refusal of a tensor not on a GPU)."""
+    w, s, x = meta(8, 32), meta(8, 2, dtype=torch.float32), meta(3, 64, dtype=torch.float32)
+    sc, xs = meta(1, 1, dtype=torch.float32), {"dtype": torch.float32}
+    i32 = {"dtype": torch.int32}
+    h, pos, gates = meta(4, 8, **xs), meta(4, 2, **i32), meta(4, 2, **xs)
+
+    def asks(t):
+        return t.clone().requires_grad_()
+    calls = [lambda g: q.i4g_linear(w, s, g(x), 32),
+             lambda g: q.i4g_linear(w, g(s), x, 32),
+             lambda g: q.i4g_linear(w, s, x, 32, bias=g(meta(8, **xs))),
+             lambda g: q.i4g_linear(w, s, x, 32, residual=g(meta(3, 8, **xs))),
+             lambda g: q.i4g_linear(w, s, x, 32, out=g(meta(3, 8, **xs))),
+             lambda g: q.fp8b128_linear(meta(8, 64), sc, g(x)),
+             lambda g: q.i4g_grouped(meta(2, 8, 32), meta(2, 8, 2, **xs), g(x), meta(3, **i32),
+                                     32),
+             lambda g: q.moe_combine(g(h), pos, gates),
+             lambda g: q.moe_combine(h, pos, g(gates))]
+    for f in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            f(asks)
+        with torch.no_grad(), pytest.raises(TypeError, match="CUDA"):
+            f(asks)
+        with pytest.raises(TypeError, match="CUDA"):
+            f(lambda t: t)
