@@ -371,7 +371,8 @@ int qgemv_moe_group(const int32_t *ids, int T, int K, int E, int32_t *offsets, i
  *   x [T] rows (T >= R where rows is NULL);  y [R] rows; rows of y before
  *   offsets[0] and from offsets[E] on are left as they were
  *   1 <= E <= 1024; R = 0 launches nothing; the epilogue's residual must be
- *   NULL
+ *   NULL; sizes that need 2^32 work items are refused (QGEMV_E_DIMS; not below
+ *   (R / 16 + E) * O = 2^29)
  *   workspace  qgemv_grouped_workspace bytes, 256-byte aligned
  * Row counts per expert stay on the device.
  */

@@ -51,11 +51,8 @@ bool overlapping(const qg::LinearArgs &a, long long w_bytes, long long s_bytes,
            overlap(res, ws) || overlaps_any(ws, in, N);
 }
 
-// 16 x 16 tiles of y, the smallest of all kernels, must fit a launch
-bool too_many_tiles(long long row_tiles, int oc)
-{
-    return row_tiles * ((oc + 15) / 16) > 0x7FFFFFFFLL;
-}
+// more products than any memory holds outputs for
+bool too_large(long long rows, int O) { return rows * O > 1LL << 39; }
 
 // Fills a's type, strides and epilogue from the arguments and checks them.
 int take(qg::LinearArgs &a, const qgemv_epilogue *e, bool with_residual)
@@ -102,7 +99,7 @@ int dense(qg::WeightFormat fmt, const void *w, const float *scales, const void *
     a.dtype = dtype;
     if (int e = take(a, epilogue, true)) return e;
     if (S == 0) return QGEMV_OK;
-    if (too_many_tiles((S + 15) / 16, O)) return QGEMV_E_DIMS;
+    if (too_large(S, O)) return QGEMV_E_DIMS;
     const size_t need = qg::linear_workspace(S, S, 0, I, O, dtype);
     if (!workspace || misaligned(workspace, 256) || ws_bytes < need) return QGEMV_E_WORKSPACE;
     const bool i4 = fmt == qg::FMT_I4G;
@@ -183,7 +180,7 @@ int qgemv_i4g_grouped(const void *w, const float *scales, long long w_stride, lo
     a.dtype = dtype;
     if (int e = take(a, epilogue, false)) return e;
     if (R == 0) return QGEMV_OK;
-    if (too_many_tiles((long long)R / 16 + (E < R ? E : R), O)) return QGEMV_E_DIMS;
+    if (too_large(R, O) || !qg::linear_launchable(qg::FMT_I4G, a)) return QGEMV_E_DIMS;
     const size_t need = qg::linear_workspace(T, R, E, I, O, dtype);
     if (!workspace || misaligned(workspace, 256) || ws_bytes < need) return QGEMV_E_WORKSPACE;
     if (overlapping(a, O * rb, 4 * O * ng, workspace, need)) return QGEMV_E_OVERLAP;

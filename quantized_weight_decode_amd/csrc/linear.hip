@@ -453,28 +453,22 @@ size_t linear_workspace(int T, int R, int E, int I, int O, int dtype)
            tile_workspace(E > 0 || T < slice ? T : slice, I, dtype);
 }
 
-hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hipStream_t st)
+// The kernel of a product, its row tiles and its launch's work items.
+struct Choice {
+    int stream;                          // rows of the stream kernel's tiles, or 0
+    bool fits, narrow;                   // the packed kernels take it
+    Shape shape;                         // of the general kernel
+    int bm;
+    long long mt, items;
+};
+
+static Choice choose(WeightFormat fmt, const LinearArgs &a)
 {
-    LinearArgs a = args;
+    Choice c{};
     const int oc = a.gated ? a.O / 2 : a.O;
-    // a dense product's packed activations must lie within 4 GB: slices of rows
-    const int slice = tile_rows(a.I);
-    if (!a.offsets && a.R > slice) {
-        const size_t el = a.dtype == QGEMV_BF16 ? 2 : 4;
-        for (int r = 0; r < args.R; r += slice) {
-            a.T = a.R = args.R - r < slice ? args.R - r : slice;
-            a.x = static_cast<const char *>(args.x) + (size_t)r * a.ldx * el;
-            a.y = static_cast<char *>(args.y) + (size_t)r * a.ldy * el;
-            if (args.residual)
-                a.residual = static_cast<const char *>(args.residual) + (size_t)r * a.ldr * el;
-            const hipError_t e = launch_linear(fmt, a, ws, st);
-            if (e != hipSuccess) return e;
-        }
-        return hipSuccess;
-    }
-    const bool fits = tile_fits(fmt, a);
+    c.fits = tile_fits(fmt, a);
+    c.stream = stream_rows(fmt, a);
     const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
-    const int stream = stream_rows(fmt, a);
     // The general kernel's tiles: 16 rows also where 64-row tiles would give a
     // CU less than two, thin ones where those of 16 x 64 would.  us, bf16 int4:
     // 512 x 3001 x 3001 (376 tiles of 64 rows) 141 in tiles of 16 rows, 160 of
@@ -485,19 +479,65 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hip
     const long long ntn = (oc + GN - 1) / GN, most = cu_count() * 3 / 2;
     const long long tiles64 = ((a.R + GM - 1) / GM + shorts) * ntn;
     const long long tiles16 = ((a.R + GM_FEW - 1) / GM_FEW + shorts) * ntn;
-    const Shape shape = rows > GM_FEW && tiles64 > most ? MANY : tiles16 > most ? FEW : THIN;
-    int bm = shape == MANY ? GM : GM_FEW;
-    bool narrow = false;
-    if (stream) {
-        bm = stream;
-    } else if (fits) {
-        pick_tile(a, oc, bm, narrow);
+    c.shape = rows > GM_FEW && tiles64 > most ? MANY : tiles16 > most ? FEW : THIN;
+    c.bm = c.shape == MANY ? GM : GM_FEW;
+    if (c.stream) c.bm = c.stream;
+    else if (c.fits) pick_tile(a, oc, c.bm, c.narrow);
+    c.mt = a.offsets ? max_tiles(a.R, a.E, c.bm) : (a.R + c.bm - 1) / c.bm;
+    if (c.stream) {
+        c.items = stream_items(fmt, a, c.stream, (int)c.mt);
+    } else if (c.fits) {
+        c.items = tile_items(a, c.narrow, c.bm, (int)c.mt);
+    } else {
+        const int bn = c.shape == THIN ? GN_THIN : GN;
+        c.items = c.mt * ((oc + bn - 1) / bn) * (c.shape == THIN ? 1024 : 256);
     }
+    return c;
+}
+
+bool linear_launchable(WeightFormat fmt, const LinearArgs &a)
+{
+    return !a.offsets || choose(fmt, a).items <= MAX_ITEMS;
+}
+
+hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hipStream_t st)
+{
+    LinearArgs a = args;
+    const int oc = a.gated ? a.O / 2 : a.O;
+    Choice c;
+    if (a.offsets) {
+        c = choose(fmt, a);
+    } else {
+        // slices of rows: a dense product's packed activations must lie within
+        // 4 GB, its work items within a launch (128 rows of 2^24 outputs do)
+        int slice = tile_rows(a.I);
+        for (;; slice = (slice / 2 + 127) / 128 * 128) {
+            a.T = a.R = args.R < slice ? args.R : slice;
+            c = choose(fmt, a);
+            if (c.items <= MAX_ITEMS || slice <= 128) break;
+        }
+        if (args.R > slice) {
+            const size_t el = a.dtype == QGEMV_BF16 ? 2 : 4;
+            for (int r = 0; r < args.R; r += slice) {
+                a.T = a.R = args.R - r < slice ? args.R - r : slice;
+                a.x = static_cast<const char *>(args.x) + (size_t)r * a.ldx * el;
+                a.y = static_cast<char *>(args.y) + (size_t)r * a.ldy * el;
+                if (args.residual)
+                    a.residual = static_cast<const char *>(args.residual) + (size_t)r * a.ldr * el;
+                const hipError_t e = launch_linear(fmt, a, ws, st);
+                if (e != hipSuccess) return e;
+            }
+            return hipSuccess;
+        }
+    }
+    if (c.items > MAX_ITEMS) return hipErrorInvalidValue;
+    const bool fits = c.fits;
+    const int stream = c.stream, bm = c.bm;
+    const Shape shape = c.shape;
+    const long long mt = c.mt;
     RowTile *tiles = nullptr;
-    long long mt = (a.R + bm - 1) / bm;
     if (a.offsets) {
         tiles = static_cast<RowTile *>(ws);
-        mt = max_tiles(a.R, a.E, bm);
         hipLaunchKernelGGL(plan_tiles, dim3(1), dim3(1024), 0, st, a.offsets, a.E, a.R, bm, tiles,
                            (int)mt);
         hipError_t e = hipGetLastError();
@@ -505,10 +545,9 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hip
         ws = static_cast<char *>(ws) + align256((size_t)max_tiles(a.R, a.E, 16) * sizeof(RowTile));
     }
     if (stream) return launch_stream(fmt, a, stream, tiles, (int)mt, st);
-    if (fits) return launch_tile(fmt, a, narrow, bm, tiles, (int)mt, ws, st);
+    if (fits) return launch_tile(fmt, a, c.narrow, bm, tiles, (int)mt, ws, st);
     const int bn = shape == THIN ? GN_THIN : GN;
     const long long grid = mt * ((oc + bn - 1) / bn);
-    if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     if (fmt == FMT_I4G) {
         if (a.dtype == QGEMV_BF16) run_general<FMT_I4G, BF16>(a, shape, tiles, (unsigned)grid, st);
         else run_general<FMT_I4G, F32>(a, shape, tiles, (unsigned)grid, st);

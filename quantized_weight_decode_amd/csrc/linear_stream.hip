@@ -603,20 +603,20 @@ int stream_rows(WeightFormat fmt, const LinearArgs &a)
     return a.dtype == QGEMV_BF16 && (a.R + 31) / 32 * ((O + cols - 1) / cols) <= ncu ? 32 : 0;
 }
 
-hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, int rows, const RowTile *tiles,
-                         int ntm, hipStream_t st)
+// Row blocks per workgroup: the count that leaves the busiest CU the least to
+// do, a workgroup of 16 rows of x counted as its row blocks and 1.5 for its x
+// (48 x 4096 x 4096 f32: one workgroup of four blocks per CU 17.5 us, three of
+// one 27.7); among equals the largest, which shares each x fragment among
+// the most rows, but for up to four rows of bf16 by int4, where that is
+// cheap, the smallest (1 x 6144 x 12288: 12.4 us, three
+// blocks 13.0; f32 16.3 and 16.0; fp8 1 x 7168 x 16384: 22.7, four 21.4).
+static void pick_blocks(WeightFormat fmt, const LinearArgs &a, int rows, int ntm, int &best,
+                        int &ntn)
 {
-    // Row blocks per workgroup: the count that leaves the busiest CU the least to
-    // do, a workgroup of 16 rows of x counted as its row blocks and 1.5 for its x
-    // (48 x 4096 x 4096 f32: one workgroup of four blocks per CU 17.5 us, three of
-    // one 27.7); among equals the largest, which shares each x fragment among
-    // the most rows, but for up to four rows of bf16 by int4, where that is
-    // cheap, the smallest (1 x 6144 x 12288: 12.4 us, three
-    // blocks 13.0; f32 16.3 and 16.0; fp8 1 x 7168 x 16384: 22.7, four 21.4).
     const int oc = a.gated ? a.O / 2 : a.O;
     const long long ncu = cu_count();
     const bool small = rows == 4 && fmt == FMT_I4G && a.dtype == QGEMV_BF16;
-    int best = 0, ntn = 0;
+    best = ntn = 0;
     double cost = 0.0;
     for (int nb = rows == 32 ? wide_blocks(fmt) : 4; nb >= 1; nb--) {
         if (a.gated && (nb & 1)) continue;
@@ -630,9 +630,22 @@ hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, int rows, const 
             ntn = n;
         }
     }
+}
+
+long long stream_items(WeightFormat fmt, const LinearArgs &a, int rows, int ntm)
+{
+    int best, ntn;
+    pick_blocks(fmt, a, rows, ntm, best, ntn);
+    return (long long)ntm * ntn * (SW * 64);
+}
+
+hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, int rows, const RowTile *tiles,
+                         int ntm, hipStream_t st)
+{
+    int best, ntn;
+    pick_blocks(fmt, a, rows, ntm, best, ntn);
     StreamArgs p{a, tiles, ntn};
     const long long grid = (long long)ntm * ntn;
-    if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
     if (fmt == FMT_I4G) {
         if (a.dtype == QGEMV_BF16) run_stream<FMT_I4G, BF16>(p, rows, best, (unsigned)grid, st);
         else run_stream<FMT_I4G, F32>(p, rows, best, (unsigned)grid, st);

@@ -785,12 +785,15 @@ hipError_t run_tile(const TileArgs &p, unsigned grid, hipStream_t st)
     return hipGetLastError();
 }
 
+// Waves of a narrow workgroup with planes x row blocks of packed x: 8 where
+// their stages fit the 160 KB of LDS, else 6.
+constexpr int narrow_waves(int planes) { return planes <= 2 ? 8 : 6; }
+
 template <int FMT, typename XT, int MB>
 hipError_t run_narrow(const TileArgs &p, unsigned grid, hipStream_t st)
 {
-    // 8 waves where their stages fit the 160 KB of LDS, else 6
     constexpr int NP = sizeof(typename XT::raw) == 4 ? 2 : 1;
-    constexpr int KW = NP * MB <= 2 ? 8 : 6, AST = 2;
+    constexpr int KW = narrow_waves(NP * MB), AST = 2;
 #define QG_RUN2(FG, G, R)                                                                   \
     hipLaunchKernelGGL((linear_narrow<FMT, XT, NP, MB, G, FG, R, KW, AST>), dim3(grid),     \
                        dim3(KW * 64), 0, st, p)
@@ -844,6 +847,23 @@ bool tile_fits(WeightFormat fmt, const LinearArgs &a)
            (size_t)a.ng * a.O * 4 < (1ull << 32) && (size_t)a.T * plane_stride(a.I) * 2 < (1ull << 32);
 }
 
+// Workgroups of a launch, and tiles across y.
+static long long tile_grid(const LinearArgs &a, bool narrow, int ntm, int &ntn)
+{
+    const int tn = narrow ? 64 : TN;
+    const int cols = a.gated ? tn / 2 : tn, oc = a.gated ? a.O / 2 : a.O;
+    ntn = (oc + cols - 1) / cols;
+    // the grouped tile kernel deals row tiles by eights
+    return (long long)(a.offsets && !narrow ? (ntm + 7) / 8 * 8 : ntm) * ntn;
+}
+
+long long tile_items(const LinearArgs &a, bool narrow, int bm, int ntm)
+{
+    const int planes = (a.dtype == QGEMV_BF16 ? 1 : 2) * bm / 16;
+    int ntn;
+    return tile_grid(a, narrow, ntm, ntn) * (narrow ? narrow_waves(planes) * 64 : 256);
+}
+
 hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int bm,
                        const RowTile *tiles, int ntm, void *ws, hipStream_t st)
 {
@@ -864,12 +884,7 @@ hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int b
     p.rexp = rexp;
     p.tiles = tiles;
     p.ntm = ntm;
-    const int tn = narrow ? 64 : TN;
-    const int cols = a.gated ? tn / 2 : tn, oc = a.gated ? a.O / 2 : a.O;
-    p.ntn = (oc + cols - 1) / cols;
-    // the grouped tile kernel deals row tiles by eights
-    const long long grid = (long long)(tiles && !narrow ? (ntm + 7) / 8 * 8 : ntm) * p.ntn;
-    if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+    const long long grid = tile_grid(a, narrow, ntm, p.ntn);
     const hipError_t e = a.dtype == QGEMV_BF16 ? pack<BF16>(fmt, a, p.Ip, p.ldp, hi, lo, rexp, st)
                                                : pack<F32>(fmt, a, p.Ip, p.ldp, hi, lo, rexp, st);
     if (e != hipSuccess) return e;

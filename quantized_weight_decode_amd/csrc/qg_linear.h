@@ -32,6 +32,9 @@ struct LinearArgs {
 // Workspace bytes of a product (an upper bound over its kernels; a function
 // of these sizes only).  E = 0: dense.
 size_t linear_workspace(int T, int R, int E, int I, int O, int dtype);
+// Whether the kernel chosen for a product fits a launch (dense ones always: they
+// are cut into slices of rows).
+bool linear_launchable(WeightFormat fmt, const LinearArgs &a);
 hipError_t launch_linear(WeightFormat fmt, const LinearArgs &a, void *ws, hipStream_t st);
 
 // The f16 tile kernels (linear_tile.hip): shapes they take, workspace, launch
@@ -41,14 +44,19 @@ struct RowTile;
 bool tile_fits(WeightFormat fmt, const LinearArgs &a);
 size_t tile_workspace(int T, int I, int dtype);
 int tile_rows(int I);                    // rows whose packed plane stays below 4 GB
+long long tile_items(const LinearArgs &a, bool narrow, int bm, int ntm);   // work items
 hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int bm,
                        const RowTile *tiles, int ntm, void *ws, hipStream_t st);
 
 // The stream kernel (linear_stream.hip): the rows of its tiles for a product, 0
 // where others are better or it does not fit.
 int stream_rows(WeightFormat fmt, const LinearArgs &a);
+long long stream_items(WeightFormat fmt, const LinearArgs &a, int rows, int ntm);
 hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, int rows, const RowTile *tiles,
                          int ntm, hipStream_t st);
+
+// A dimension of a launch holds fewer than 2^32 work items.
+constexpr long long MAX_ITEMS = 0xFFFFFFFFLL;
 
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 

@@ -251,12 +251,19 @@ hipError_t run_combine(const void *h, long long ldh, int R, const int32_t *pos,
     const int bx = nch > 192 ? 256 : nch > 64 ? 128 : 64;
     const int by = 256 / bx;
     const int ncb = (nch + bx - 1) / bx;
-    const long long grid = (long long)((T + by - 1) / by) * ncb;
-    if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((combine<XT, VEC>), dim3((unsigned)grid), dim3(bx, by), 0, st,
-                       static_cast<const raw *>(h), ldh, R, pos, gates, T, K, O,
-                       static_cast<const raw *>(residual), ldr, static_cast<raw *>(y), ldy, ncb);
-    return hipGetLastError();
+    // as many tokens per launch as its work items allow
+    const long long most = MAX_ITEMS / bx / ncb * by;
+    for (long long t = 0; t < T; t += most) {
+        const int n = (int)(T - t < most ? T - t : most);
+        hipLaunchKernelGGL((combine<XT, VEC>), dim3((unsigned)((n + by - 1) / by * ncb)),
+                           dim3(bx, by), 0, st, static_cast<const raw *>(h), ldh, R, pos + t * K,
+                           gates + t * K, n, K, O,
+                           residual ? static_cast<const raw *>(residual) + t * ldr : nullptr, ldr,
+                           static_cast<raw *>(y) + t * ldy, ldy, ncb);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

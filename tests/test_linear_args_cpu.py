@@ -89,3 +89,13 @@ def test_arguments_that_ask_for_a_gradient(q):
             f(asks)
         with pytest.raises(TypeError, match="CUDA"):
             f(lambda t: t)
+
+
+@pytest.mark.parametrize("I,gs,dtype", [(32, 32, 0), (32, 32, 1), (30, 2, 0), (31, 6, 1)])
+@pytest.mark.parametrize("E,R", [(1024, 2048), (1024, 1 << 15), (1, 1 << 15)])
+def test_grouped_sizes_beyond_a_launch(q, E, R, I, gs, dtype):
+    """A launch holds fewer than 2^32 work items: refused before anything runs."""
+    a, O = 1 << 46, 1 << 24
+    st = q.qgemv_i4g_grouped(a, 2 * a, O * 16, O * 16, E, 3 * a, None, 4 * a, 32, R, 5 * a, O, R,
+                             I, O, gs, dtype, None, 6 * a, 1 << 45, 0)
+    assert st == 2
