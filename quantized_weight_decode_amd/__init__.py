@@ -304,9 +304,9 @@ def _shape(t, name, shape):
 
 
 def _one_device(*ts):
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"tensors are on different devices: {sorted(map(str, devs))}")
+    devs = [t.device for t in ts if t is not None]
+    if devs.count(devs[0]) != len(devs):
+        raise ValueError(f"tensors are on different devices: {sorted(set(map(str, devs)))}")
 
 
 def _out(out, S, O, like):
@@ -554,16 +554,16 @@ _NO_GUARD = contextlib.nullcontext()
 
 def _sizes(fn, *sizes):
     """Refuses sizes that no call takes, before a C int could wrap them."""
-    if max(sizes) > _MAX_DIM or min(sizes) < 0:
-        raise QgemvError(fn, 2, strerror(2))
+    for n in sizes:
+        if not 0 <= n <= _MAX_DIM:
+            raise QgemvError(fn, 2, strerror(2))
 
 
 def _no_gradient(*ts):
-    if _torch().is_grad_enabled():
-        for t in ts:
-            if t is not None and t.requires_grad:
-                raise ValueError("an argument requires a gradient, and this call has no backward "
-                                 "pass: detach it or use torch.no_grad()")
+    for t in ts:
+        if t is not None and t.requires_grad and _torch().is_grad_enabled():
+            raise ValueError("an argument requires a gradient, and this call has no backward "
+                             "pass: detach it or use torch.no_grad()")
 
 
 def _on(device):
