@@ -306,8 +306,8 @@ typedef struct {
  *   read or written.  y must not overlap what the call reads (columns of one
  *   buffer may be x and others y), but for the residual in place.
  *   x, y, bias and residual are aligned to their element, w to a byte.
- *   workspace  device scratch of qgemv_linear_workspace bytes, 256-byte
- *              aligned, overwritten; calls that may overlap in time (two
+ *   workspace  device scratch of qgemv_linear_workspace bytes (where that is 0,
+ *              it may be NULL), 256-byte aligned, overwritten; calls that may overlap in time (two
  *              streams, two captured graphs) need one each.
  * Any I >= 1 and any even gs.  gs % 32 == 0 with I % 32 == 0 and 16-byte
  * aligned w takes the fast kernels; every other valid shape a slower general

@@ -100,8 +100,9 @@ int dense(qg::WeightFormat fmt, const void *w, const float *scales, const void *
     if (int e = take(a, epilogue, true)) return e;
     if (S == 0) return QGEMV_OK;
     if (too_large(S, O)) return QGEMV_E_DIMS;
-    const size_t need = qg::linear_workspace(S, S, 0, I, O, dtype);
-    if (!workspace || misaligned(workspace, 256) || ws_bytes < need) return QGEMV_E_WORKSPACE;
+    const size_t need = qg::linear_workspace(S, S, 0, I, dtype);
+    if (need > 0 && (!workspace || misaligned(workspace, 256) || ws_bytes < need))
+        return QGEMV_E_WORKSPACE;
     const bool i4 = fmt == qg::FMT_I4G;
     if (overlapping(a, (long long)O * (i4 ? (I + 1) / 2 : I),
                     4LL * a.ng * (i4 ? O : (O + 127) / 128), workspace, need))
@@ -116,7 +117,7 @@ extern "C" {
 size_t qgemv_linear_workspace(int S, int I, int O, int dtype)
 {
     if (bad_sizes(S, I, O) || bad_dtype(dtype)) return 0;
-    return qg::linear_workspace(S, S, 0, I, O, dtype);
+    return qg::linear_workspace(S, S, 0, I, dtype);
 }
 
 int qgemv_i4g_linear(const void *w, const float *scales, const void *x, long long ldx, void *y,
@@ -142,7 +143,7 @@ size_t qgemv_grouped_workspace(int T, int R, int E, int I, int O, int dtype)
     if (bad_sizes(R, I, O) || T < 0 || T > MAX_DIM || E < 1 || E > MAX_EXPERTS ||
         bad_dtype(dtype))
         return 0;
-    return qg::linear_workspace(T, R, E, I, O, dtype);
+    return qg::linear_workspace(T, R, E, I, dtype);
 }
 
 int qgemv_i4g_grouped(const void *w, const float *scales, long long w_stride, long long s_stride,
@@ -181,7 +182,7 @@ int qgemv_i4g_grouped(const void *w, const float *scales, long long w_stride, lo
     if (int e = take(a, epilogue, false)) return e;
     if (R == 0) return QGEMV_OK;
     if (too_large(R, O) || !qg::linear_launchable(qg::FMT_I4G, a)) return QGEMV_E_DIMS;
-    const size_t need = qg::linear_workspace(T, R, E, I, O, dtype);
+    const size_t need = qg::linear_workspace(T, R, E, I, dtype);
     if (!workspace || misaligned(workspace, 256) || ws_bytes < need) return QGEMV_E_WORKSPACE;
     if (overlapping(a, O * rb, 4 * O * ng, workspace, need)) return QGEMV_E_OVERLAP;
     return launched(qg::launch_linear(qg::FMT_I4G, a, workspace, (hipStream_t)stream));

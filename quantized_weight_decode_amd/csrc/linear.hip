@@ -445,12 +445,12 @@ void run_general(const LinearArgs &a, Shape shape, const RowTile *tiles, unsigne
 
 }  // namespace
 
-size_t linear_workspace(int T, int R, int E, int I, int O, int dtype)
+size_t linear_workspace(int T, int R, int E, int I, int dtype)
 {
-    (void)O;
     const int slice = tile_rows(I);
+    const int rows = E > 0 || T < slice ? T : slice;
     return (E > 0 ? align256((size_t)max_tiles(R, E, 16) * sizeof(RowTile)) : 0) +
-           tile_workspace(E > 0 || T < slice ? T : slice, I, dtype);
+           (planes_fit(rows, I) ? tile_workspace(rows, I, dtype) : 0);
 }
 
 // The kernel of a product, its row tiles and its launch's work items.

@@ -839,12 +839,14 @@ int tile_rows(int I)
     return n > (1 << 24) ? 1 << 24 : n < 128 ? 128 : (int)n;
 }
 
+bool planes_fit(int T, int I) { return (size_t)T * plane_stride(I) * 2 < (1ull << 32); }
+
 bool tile_fits(WeightFormat fmt, const LinearArgs &a)
 {
     const size_t rb = fmt == FMT_I4G ? (size_t)a.I / 2 : (size_t)a.I;
     return a.I % 32 == 0 && (fmt == FMT_FP8 || a.gs % 32 == 0) && ((uintptr_t)a.w & 15) == 0 &&
            (!a.offsets || a.w_stride % 16 == 0) && rb * a.O < (1ull << 32) &&
-           (size_t)a.ng * a.O * 4 < (1ull << 32) && (size_t)a.T * plane_stride(a.I) * 2 < (1ull << 32);
+           (size_t)a.ng * a.O * 4 < (1ull << 32) && planes_fit(a.T, a.I);
 }
 
 // Workgroups of a launch, and tiles across y.

@@ -31,7 +31,7 @@ struct LinearArgs {
 
 // Workspace bytes of a product (an upper bound over its kernels; a function
 // of these sizes only).  E = 0: dense.
-size_t linear_workspace(int T, int R, int E, int I, int O, int dtype);
+size_t linear_workspace(int T, int R, int E, int I, int dtype);
 // Whether the kernel chosen for a product fits a launch (dense ones always: they
 // are cut into slices of rows).
 bool linear_launchable(WeightFormat fmt, const LinearArgs &a);
@@ -44,6 +44,7 @@ struct RowTile;
 bool tile_fits(WeightFormat fmt, const LinearArgs &a);
 size_t tile_workspace(int T, int I, int dtype);
 int tile_rows(int I);                    // rows whose packed plane stays below 4 GB
+bool planes_fit(int T, int I);           // those of T rows do
 long long tile_items(const LinearArgs &a, bool narrow, int bm, int ntm);   // work items
 hipError_t launch_tile(WeightFormat fmt, const LinearArgs &a, bool narrow, int bm,
                        const RowTile *tiles, int ntm, void *ws, hipStream_t st);

@@ -99,3 +99,14 @@ def test_grouped_sizes_beyond_a_launch(q, E, R, I, gs, dtype):
     st = q.qgemv_i4g_grouped(a, 2 * a, O * 16, O * 16, E, 3 * a, None, 4 * a, 32, R, 5 * a, O, R,
                              I, O, gs, dtype, None, 6 * a, 1 << 45, 0)
     assert st == 2
+
+
+def test_no_scratch_for_planes_that_no_kernel_packs(q):
+    """Packed activations of 4 GB and more are never made: dense rows are cut
+    into slices, grouped ones take the general kernel."""
+    for dtype in (0, 1):
+        T, I, E = 1 << 20, 7168, 64
+        assert q.qgemv_grouped_workspace(T, T, E, I, 64, dtype) < 1 << 24
+        assert q.qgemv_grouped_workspace(1 << 18, T, E, I, 64, dtype) > 1 << 31
+        assert 1 << 31 < q.qgemv_linear_workspace(T, I, 64, dtype) < 9 << 30
+        assert q.qgemv_linear_workspace(128, 1 << 24, 64, dtype) == 0
