@@ -264,7 +264,8 @@ int qgemv_moe_topk_noalloc(const void *w, const float *scales, long long w_strid
  *
  * Type of x, bias, residual and y of one call; sums are f32 (of exact
  * products of the decoded integer or fp8 values with x, the scales applied to
- * each scale group's f32 sum) and y is rounded once.
+ * each scale group's f32 sum; the general kernel's are of x with weights
+ * rounded to f32) and y is rounded once.
  */
 typedef enum { QGEMV_F32 = 0, QGEMV_BF16 = 1 } qgemv_dtype;
 
@@ -312,11 +313,16 @@ typedef struct {
  * Any I >= 1 and any even gs.  gs % 32 == 0 with I % 32 == 0 and 16-byte
  * aligned w takes the fast kernels; every other valid shape a slower general
  * kernel with the same result definition.
- * Accuracy: f32 x enters the sums within 2^-22 of itself (many rows; elements
- * below 2^-18 of their row's largest within 2^-40 of that) or exactly (few),
- * bf16 x exactly (below 2^-28 of the row's largest within 2^-39 of that).  Few
- * bf16 rows times int4 are summed as (16 + q) x less 24 sum x: each f32 rounding
- * is relative to 24 sum |x| of a scale group, not to sum |(q - 8) x|.
+ * Accuracy of the fast kernels: many rows of f32 x enter the sums within 2^-22
+ * of themselves (elements below 2^-17 of their row's largest within 2^-39 of
+ * that), of bf16 x exactly (below 2^-28 of the row's largest within 2^-39 of
+ * that).  Few rows enter exactly, f32 below 2^-109 to 2^-133, and a scale group's
+ * sum of x times codes is exact to 2^-133; bf16 times int4 is summed as (16 + q) x
+ * less 24 sum x, whose f32 roundings are relative to sum (16 + q) |x| + 24 sum
+ * |x| of a scale group, not to sum |(q - 8) x|.  Few rows are up to 16, and more
+ * where the workgroups of 16 (bf16: 16 or 32) rows times 64 rows of w (32 rows:
+ * 48 or 64) are no more than the CUs, thus up to 4096 rows for O <= 64 on 256
+ * CUs; grouped, up to 9 rows per expert on average (bf16), 8 in all (f32).
  * No finite x overflows on the way where the sum of |x w| of an output is in
  * f32's range and the scales are below 2^80.
  * A row of x that holds an infinity or NaN gives a row of y without finite

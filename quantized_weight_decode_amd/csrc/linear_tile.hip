@@ -18,8 +18,9 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 // [2^(E-1), 2^E) over its finite values, so that 2^14 <= max|x'| < 2^15, and
 // stored as f16: bf16 values exactly down to 2^-28 of the maximum (below it
 // to 2^-39 of the maximum); f32 values as two planes, hi = f16(x') and lo =
-// f16(x' - hi), together within 2^-22 of themselves (2^-40 of the maximum
-// where lo is subnormal), the size of f32's own rounding of a product.
+// f16(x' - hi), together within 2^-22 of themselves down to 2^-17 of the
+// maximum and within 2^-39 of it below, where lo is subnormal (an f32 sum's own
+// roundings are of that size).
 // The exponent E - 15 is undone on the f32 sum.  int4 weights unpack in the
 // column order 0 4 1 5 2 6 3 7 of each eight; x is stored in that order.
 // Rows are padded with zeros to whole K steps.
