@@ -236,12 +236,14 @@ struct StreamArgs {
 // part of LDS to get the fragments' order, and as soon as the weights are in
 // LDS asks for its next block, so that one block per wave is always in flight.
 //
-// bf16 activations multiply the nibbles q themselves, and the group's sum
-// starts from -8 sum(x), one more matrix instruction per group: |error| <=
-// 2^-24 (sum q|x| + 8 sum |x|) per rounding, far inside bf16's own.  f32
-// activations multiply q - 8, whose unpacking costs 2.5 instead of 0.9
-// instructions per weight: an outlier of x at a zero weight must not cost the
-// small elements their bits.
+// bf16 activations multiply 16 + q, and the group's sum starts from -24 sum(x),
+// one more matrix instruction per group: a rounding is up to 2^-24 (sum (16 + q)
+// |x| + 24 sum |x|) of the group.  With all of x of one size that is 48 / 4 times
+// 2^-24 of the sum of |(q - 8) x|, far below bf16's 2^-9; one element 10^4 times
+// the others at a zero weight adds 2^-24 * 48 * 10^4 = 0.03 of them, still below
+// the rounding of an output of 2000 columns (2^-9 of 4 sqrt(2000)), one of 10^6
+// no longer.  f32 activations multiply q - 8, whose unpacking costs 2.5 instead
+// of 0.9 instructions per weight: their outputs would show it much sooner.
 //
 // ROWS = 16 or 32: x goes to LDS as it is in memory, and each fragment is turned into
 // bf16 parts as it is read; three parts of f32 take three matrix instructions.
