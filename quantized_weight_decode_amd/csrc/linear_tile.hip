@@ -204,17 +204,23 @@ __device__ __forceinline__ f16x8 fp8x8_f16(uint32_t a, uint32_t b)
 // Memory to LDS without registers: lane i's 16 (4) bytes from base + off go to
 // LDS bytes lds + 16 i (4 i); lds is uniform over the wave.  The compiler does
 // not count these loads: the K loop waits for them itself (wait_loads), and
-// holds no other vector-memory loads.
+// holds no other vector-memory loads.  m0 is reserved, so that no value of the
+// compiler's lives there; that it is named keeps its own uses of it, which set
+// it first, on one side of these.  (The warning says that it is reserved.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds16(const void *base, uint32_t off, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(lds), "v"(off), "s"(base) : "memory");
+                 :: "s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds4(const void *base, uint32_t off, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-                 :: "s"(lds), "v"(off), "s"(base) : "memory");
+                 :: "s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
+#pragma clang diagnostic pop
+
 // All but the wave's last n loads have arrived, for every wave of the group.
 template <int N>
 __device__ __forceinline__ void wait_loads()
