@@ -630,14 +630,14 @@ __device__ __forceinline__ void wait_own_loads()
 // LDS in a fixed order.  Bound by the loads in flight, which LDS limits: 64 x
 // 6144 x 12288 bf16 31 us, 40 MB of weights; the tile kernel's 48 workgroups
 // take 89 us.
-template <int FMT, typename XT, int NP, int MB, bool GATED, int FG, bool RAGGED, int KW, int AST>
+template <int FMT, typename XT, int NP, int MB, bool GATED, int FG, bool RAGGED, int KW>
 __global__ __launch_bounds__(KW * 64, (KW + 3) / 4) void linear_narrow(TileArgs p)
 {
     typedef Weights<FMT, FG, 64> W;
     constexpr int NB = 4, NS = TK / FG;
     constexpr int AL = MB * 2;                           // loads of x per plane and step
     constexpr int CH = MB * 16 * 8;                      // 16-byte chunks of a plane
-    constexpr uint32_t XB = NP * CH * 16, WO = AST * XB, OWN = WO + 2 * W::BYTES;
+    constexpr uint32_t XB = NP * CH * 16, WO = 2 * XB, OWN = WO + 2 * W::BYTES;   // two stages
     constexpr int LDR = NB * 16 + 4;
     constexpr uint32_t RED = KW * MB * 16 * LDR * 4;
     __shared__ __align__(16) char smem[KW * OWN > RED ? KW * OWN : RED];
@@ -710,7 +710,6 @@ __global__ __launch_bounds__(KW * 64, (KW + 3) / 4) void linear_narrow(TileArgs 
     __builtin_amdgcn_s_waitcnt(QG_WAIT_VM0);             // earlier loads are done
     load_x(0, 0);
     load_w(0);
-    if (AST == 3) load_x(1, 1);
     // a stage behind the last step of a last half stage has zero steps
     const int mine = wave < stages ? (stages - 1 - wave) / KW + 1 : 0;
     const int last = (stages - 1) % KW == wave ? steps - (stages - 1) * W::WS : W::WS;
@@ -719,17 +718,16 @@ __global__ __launch_bounds__(KW * 64, (KW + 3) / 4) void linear_narrow(TileArgs 
     for (int i = 0; i < count; i++) {
         // as the tile kernel's
         const int half = i % W::WS;
-        constexpr int XLATER = AST == 3 ? NP * AL : 0;
-        if (half) wait_own_loads<XLATER + W::LOADS>();
-        else wait_own_loads<XLATER>();
+        if (half) wait_own_loads<W::LOADS>();
+        else wait_own_loads<0>();
         if (W::WS == 1) load_w(i + 1);
-        load_x(i + AST - 1, stage == 0 ? AST - 1 : stage - 1);
+        load_x(i + 1, stage ^ 1);
         if (W::WS == 2 && half == 0) load_w(i / 2 + 1);
         f16x8 bv[NB][2];
         float sc[NB][NS];
         W::unpack(own + WO + ((i / W::WS) & 1) * W::BYTES, half, lane, bv, sc);
         multiply_step<NP, MB, NB, FG, RAGGED>(acc, bv, sc, own + stage * XB, lane, mf);
-        stage = stage == AST - 1 ? 0 : stage + 1;
+        stage ^= 1;
     }
     wait_own_loads<0>();                                 // loads past the last step
     __syncthreads();
@@ -800,9 +798,9 @@ template <int FMT, typename XT, int MB>
 hipError_t run_narrow(const TileArgs &p, unsigned grid, hipStream_t st)
 {
     constexpr int NP = sizeof(typename XT::raw) == 4 ? 2 : 1;
-    constexpr int KW = narrow_waves(NP * MB), AST = 2;
+    constexpr int KW = narrow_waves(NP * MB);
 #define QG_RUN2(FG, G, R)                                                                   \
-    hipLaunchKernelGGL((linear_narrow<FMT, XT, NP, MB, G, FG, R, KW, AST>), dim3(grid),     \
+    hipLaunchKernelGGL((linear_narrow<FMT, XT, NP, MB, G, FG, R, KW>), dim3(grid),     \
                        dim3(KW * 64), 0, st, p)
 #define QG_RUN3(FG)                                                                         \
     do {                                                                                    \
