@@ -65,17 +65,6 @@ __device__ __forceinline__ bf16x2 cvt_hi(uint32_t w)
     return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, pow2(E), true);
 }
 
-// (w & mask) | bits in one instruction: it takes one scalar operand and no
-// literal here, so the constants are shown to the compiler as values in a
-// scalar and a vector register.  (The instruction itself stays the compiler's,
-// which keeps its distance to a matrix instruction that reads the result.)
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits)
-{
-    asm("" : "+s"(mask));
-    asm("" : "+v"(bits));
-    return (w & mask) | bits;
-}
-
 // Eight nibbles as (16 + q) 2^-OFFSET_DOWN in bf16 (0x4180 | 8 q is 16 + q), in
 // the column order 0 4 1 5 2 6 3 7; and -24 times the same.
 constexpr uint32_t bf16_pair(uint32_t bits) { return (bits - (OFFSET_DOWN << 7)) * 0x10001u; }

@@ -161,17 +161,6 @@ hipError_t pack(WeightFormat fmt, const LinearArgs &a, int Ip, int ldp, _Float16
     return hipGetLastError();
 }
 
-// (w & mask) | bits in one instruction: it takes one scalar operand and no
-// literal here, so the constants are shown to the compiler as values in a
-// scalar and a vector register.  (The instruction itself stays the compiler's,
-// which keeps its distance to a matrix instruction that reads the result.)
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits)
-{
-    asm("" : "+s"(mask));
-    asm("" : "+v"(bits));
-    return (w & mask) | bits;
-}
-
 // Eight nibbles of a dword as q - 8 in f16, exactly, in the column order 0 4
 // 1 5 2 6 3 7: 0x6400 | q is 1024 + q, and 0x6400 | 16 q is 1024 + 16 q =
 // 16 (q - 8) + 1152.

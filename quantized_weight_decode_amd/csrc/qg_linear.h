@@ -92,6 +92,17 @@ struct BF16 {
     }
 };
 
+// (w & mask) | bits in one instruction: it takes one scalar operand and no
+// literal here, so the constants are shown to the compiler as values in a
+// scalar and a vector register.  (The instruction itself stays the compiler's,
+// which keeps its distance to a matrix instruction that reads the result.)
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits)
+{
+    asm("" : "+s"(mask));
+    asm("" : "+v"(bits));
+    return (w & mask) | bits;
+}
+
 // -- epilogue ----------------------------------------------------------------
 // act(a) in f32.  silu a / (1 + e^-a); gelu a/2 (1 + erf(a / sqrt 2)), written
 // with erfc for negative a, where 1 + erf cancels; gelu_tanh the tanh form,
