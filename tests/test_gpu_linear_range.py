@@ -120,3 +120,21 @@ def test_grouped_large_activations(q, counts, dtype):
         if hi > lo:
             ref, bound = L.reference(L.decode_int4(w[e], s[e], I, gs), x[lo:hi], dtype)
             L.assert_within(y[lo:hi], ref, bound, f"expert {e}")
+
+
+@pytest.mark.parametrize("fmt", ["i4g", "fp8"])
+@pytest.mark.parametrize("S,O", [(1000, 4000), (500, 4000), (300, 1702), (100, 4200)])
+@pytest.mark.parametrize("I,gs", [(160, 32), (256, 64), (96, 96), (448, 64)])
+def test_f32_precision_of_the_packed_kernels(q, fmt, S, O, I, gs):
+    """f32 x is packed to 22 bits at least.  Relative L2 over all outputs: the
+    packing's errors, at most 2^-22 of an element and of either sign, give at
+    most 2^-22; the sums' roundings, each at most 2^-24 of a partial sum of the
+    output's size and of either sign, of N = I / 32 * 2 * 8 + I / 32 < 240 (two
+    planes, each matrix instruction eight additions, one FMA per scale group)
+    give sqrt(240) 2^-24 / sqrt(3) < 2^-20.8.  Together below 2^-20; twice that
+    is asked.  x rounded to 16 bits would give 2^-16 sqrt(1/3) 0.7 = 2^-17.3.
+    """
+    w, s, decode = _weights(fmt, O, I, gs, 90)
+    x = L.acts(S, I, torch.float32, 91)
+    ref, _ = L.reference(decode(s), x, torch.float32)
+    assert L.rel_l2(_call(q, fmt, w, s, x, gs), ref) <= 2.0 ** -19
