@@ -517,9 +517,20 @@ __global__ __launch_bounds__(512, 2) void linear_stream(StreamArgs p)
                   });
 }
 
-// Row blocks that 32 rows leave registers for (int4, four blocks: 360 bytes of
-// them spilled, 32 x 4096 x 14336 21.2 us, the narrow kernel 16.9).
-constexpr int wide_blocks(int fmt) { return fmt == FMT_I4G ? 3 : 4; }
+// Most row blocks that 32 rows of x leave registers for, 0: none worth it.  int4:
+// three; four spill 360 bytes per lane (32 x 4096 x 14336 21.2 us, the narrow
+// kernel 16.9), and three 128 with a scale per 32 columns (32 x 6144 x 12288 35.9
+// us, the narrow kernel 22.3).  Two (and with them int4's gated products, whose
+// blocks come in pairs) cover no more rows of W than two workgroups of 16 rows.
+constexpr int wide_blocks(int fmt, int fg, bool gated)
+{
+    return fmt == FMT_FP8 ? 4 : gated || fg == 32 ? 0 : 3;
+}
+// Columns of a scale group that the kernel is built for.
+int group_columns(WeightFormat fmt, int gs)
+{
+    return fmt == FMT_FP8 || gs % 128 == 0 ? 128 : gs % 64 == 0 ? 64 : 32;
+}
 
 template <int FMT, typename XT, int NB, bool GATED>
 void run_nb(const StreamArgs &p, int rows, unsigned grid, hipStream_t st)
@@ -532,14 +543,16 @@ void run_nb(const StreamArgs &p, int rows, unsigned grid, hipStream_t st)
     do {                                                                                    \
         if (rows == 4) QG_RUN_R(FG, 4);                                                     \
         else if (rows == 16) QG_RUN_R(FG, 16);                                              \
-        else if constexpr (sizeof(typename XT::raw) == 2 && NB <= wide_blocks(FMT))         \
+        else if constexpr (sizeof(typename XT::raw) == 2 && NB > 2 &&                       \
+                           NB <= wide_blocks(FMT, FG, GATED))                               \
             QG_RUN_R(FG, 32);                                                               \
     } while (0)
     if constexpr (FMT == FMT_FP8) {
         QG_RUN(128);
     } else {
-        if (p.a.gs % 128 == 0) QG_RUN(128);
-        else if (p.a.gs % 64 == 0) QG_RUN(64);
+        const int fg = group_columns(FMT_I4G, p.a.gs);
+        if (fg == 128) QG_RUN(128);
+        else if (fg == 64) QG_RUN(64);
         else QG_RUN(32);
     }
 #undef QG_RUN
@@ -590,8 +603,9 @@ int stream_rows(WeightFormat fmt, const LinearArgs &a)
     if (a.R <= 4) return 4;
     const long long ncu = cu_count(), O = a.O;
     if (a.R <= 16 || (a.R + 15) / 16 * ((O + 63) / 64) <= ncu) return 16;
-    const int cols = a.gated ? wide_blocks(fmt) / 2 * 32 : wide_blocks(fmt) * 16;
-    return a.dtype == QGEMV_BF16 && (a.R + 31) / 32 * ((O + cols - 1) / cols) <= ncu ? 32 : 0;
+    const int cols = 16 * wide_blocks(fmt, group_columns(fmt, a.gs), a.gated);
+    return a.dtype == QGEMV_BF16 && cols && (a.R + 31) / 32 * ((O + cols - 1) / cols) <= ncu ? 32
+                                                                                          : 0;
 }
 
 // Row blocks per workgroup: the count that leaves the busiest CU the least to
@@ -601,6 +615,9 @@ int stream_rows(WeightFormat fmt, const LinearArgs &a)
 // the most rows, but for up to four rows of bf16 by int4, where that is
 // cheap, the smallest (1 x 6144 x 12288: 12.4 us, three
 // blocks 13.0; f32 16.3 and 16.0; fp8 1 x 7168 x 16384: 22.7, four 21.4).
+// Four blocks of 16 f32 rows with a scale per 32 columns spill 84 bytes per lane,
+// three none, within 1 % of each other: 16 x 6144 x 12288 25.3 and 25.1, 5 x
+// 16384 x 7168 36.6 and 36.6.
 static void pick_blocks(WeightFormat fmt, const LinearArgs &a, int rows, int ntm, int &best,
                         int &ntn)
 {
@@ -609,7 +626,9 @@ static void pick_blocks(WeightFormat fmt, const LinearArgs &a, int rows, int ntm
     const bool small = rows == 4 && fmt == FMT_I4G && a.dtype == QGEMV_BF16;
     best = ntn = 0;
     double cost = 0.0;
-    for (int nb = rows == 32 ? wide_blocks(fmt) : 4; nb >= 1; nb--) {
+    // (32 rows: three or four, in one round of the CUs)
+    const int most = rows == 32 ? wide_blocks(fmt, group_columns(fmt, a.gs), a.gated) : 4;
+    for (int nb = most; nb >= (rows == 32 ? 3 : 1); nb--) {
         if (a.gated && (nb & 1)) continue;
         const int yc = a.gated ? nb * 8 : nb * 16;
         const int n = (oc + yc - 1) / yc;
