@@ -82,7 +82,9 @@ int qgemv_i4g(const void *w, const float *scales, const float *x, float *y,
  * separate matrix-unit GEMM path from a token-count threshold.
  *   w, scales, gs  as qgemv_i4g;  x f32 [S][I], y f32 [S][O] (overwritten)
  * Fast path: I % 32 == 0, gs % 32 == 0, w 4-byte and x 16-byte aligned;
- * other shapes run the GEMV eight tokens per launch.
+ * other shapes run the GEMV eight tokens per launch.  qgemv_i4g_linear is the
+ * same product on 16-bit matrix instructions, several times faster for many
+ * tokens, with x within 2^-22 of itself and a workspace.
  */
 int qgemv_i4g_prefill(const void *w, const float *scales, const float *x, float *y, int S,
                       int I, int O, int gs, void *stream);

@@ -361,7 +361,10 @@ def i4g(w, scales, x, gs, out=None):
 
 
 def i4g_prefill(w, scales, x, gs, out=None):
-    """Grouped-int4 product for many tokens (MFMA): x f32 [S][I] -> y f32 [S][O]."""
+    """Grouped-int4 product for many tokens (MFMA): x f32 [S][I] -> y f32 [S][O].
+
+    Decodes and multiplies in f32; ``i4g_linear`` is the faster product for many
+    tokens."""
     torch = _torch()
     I = x.shape[-1]
     S = x.reshape(-1, I).shape[0]
@@ -697,7 +700,8 @@ def i4g_linear(w, scales, x, gs, bias=None, act=None, gated=False, residual=None
     w u8 [O][(I+1)//2], scales f32 [O][ng], x [S][I] (or [I]) f32 or bf16, bias
     [O], residual and y [S][O] of x's type.  gated: w holds the gate rows, then
     the up rows, y = act(gate) * up (+ residual) has O/2 columns.  act: None,
-    "relu", "silu", "gelu" or "gelu_tanh".
+    "relu", "silu", "gelu" or "gelu_tanh".  One or two plain f32 vectors run
+    faster through ``i4g``.
     """
     return _linear("qgemv_i4g_linear", w, scales, x, _gs(gs), bias, act, gated, residual,
                    workspace, out)
