@@ -330,7 +330,7 @@ typedef struct {
  * A row of x that holds an infinity or NaN gives a row of y without finite
  * sums (infinities may come out as NaN); other rows are not affected.
  * One or two f32 rows without an epilogue run faster through qgemv_i4g (1 x
- * 6144 x 12288: 9.1 us, here 15.7), whose activations are fixed-point.
+ * 6144 x 12288: 9.1 us, here 14.5), whose activations are fixed-point.
  */
 size_t qgemv_linear_workspace(int S, int I, int O, int dtype);
 int qgemv_i4g_linear(const void *w, const float *scales, const void *x, long long ldx, void *y,

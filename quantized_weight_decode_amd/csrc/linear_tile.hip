@@ -226,8 +226,10 @@ constexpr int TN = 256;         // rows of W per workgroup tile
 // swizzle(row).  A 16-byte LDS read of a wave is served in four passes, lanes
 // 0-3, 12-15, 20-27, then 4-11, 16-19, 28-31, then the same of the upper half;
 // with this key the 16 lanes of each pass touch all 64 banks once, for both
-// column orders (bank conflicts measured: none; with row % 8 or row / 2 % 8
-// as key each read took twice as long).
+// column orders (counted in the fp8 tile kernel, whose weights are read the same
+// way: no conflict; with row % 8 or row / 2 % 8 as key each read took twice as
+// long.  int4's weights, read 4 or 8 bytes at a time, spend 15 % of the LDS
+// cycles on conflicts).
 __device__ __forceinline__ int swizzle(int row)
 {
     const int j = row >> 1;
@@ -421,9 +423,13 @@ __device__ __forceinline__ void multiply_step(f32x4v (&acc)[MF][NB], const f16x8
 // instructions.  RAGGED (grouped): row blocks of 16 behind the tile's rows are
 // neither loaded nor multiplied; a dense product does without those branches
 // (5 % faster at 2048 rows).
-// Bound by the matrix cores: int4 2048 x 6144 x 12288 bf16, packing included,
-// 318 us (972 TFLOP/s); the library's bf16 product of the same size takes 289
-// us (1069 TFLOP/s), of 8192^3 1364 TFLOP/s.
+// Bound by the matrix cores and the unpacking beside them: int4 2048 x 6144 x
+// 12288 bf16 gated, packing included, 309 us (1000 TFLOP/s), matrix cores busy
+// 48 % of the CUs' busy cycles, five vector instructions per matrix instruction;
+// the library's bf16 product of the same size takes 289 us (1069 TFLOP/s), of
+// 8192^3 1364 TFLOP/s.  Routed prompts (4096 tokens of 8 of 256 experts, 7168 x
+// 2048) fetch 7.8 GB in 1450 us, 3.6 times their bytes: 3.5 GB of weights, once
+// per row tile, the rest x by the column blocks; matrix cores busy 36 %.
 template <int FMT, typename XT, int NP, int MF, bool GATED, int FG, bool RAGGED>
 __global__ __launch_bounds__(256, 2) void linear_tile(TileArgs p)
 {
