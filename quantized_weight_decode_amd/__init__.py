@@ -277,9 +277,16 @@ def qgemv_dequant_mq4c(w, W, I, O, stream):
 
 
 # -- torch-tensor layer ----------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported by the first call that needs it."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream():
