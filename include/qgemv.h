@@ -407,6 +407,92 @@ int qgemv_moe_combine(const void *h, long long ldh, int R, const int32_t *pos,
                       long long ldr, void *y, long long ldy, int dtype, void *stream);
 
 /*
+ * Activations in 8 bits, for the products below: each row of x in blocks of 128
+ * columns (the last may be shorter),
+ *     scale = max|x| / 448, at least 2^-126;   code = e4m3(x / scale)
+ * (f32 quotients and e4m3 codes rounded to nearest, ties to even; 448 is e4m3's
+ * largest value), so x is codes * scale within 2^-4 of itself, or within 2^-10
+ * scale where that is more.
+ *   x       dtype [S] rows of I, ldx elements apart
+ *   codes   u8 [S] rows of I, ldc bytes apart (OCP E4M3-FN, as qgemv_fp8b128)
+ *   scales  f32 [S] rows of ceil(I/128), lds elements apart
+ * A block that holds an infinity or NaN gets the scale NaN and codes 0x7F.
+ * S = 0 launches nothing; the buffers must not overlap each other.
+ */
+int qgemv_fp8_quantize(const void *x, long long ldx, int S, int I, int dtype, void *codes,
+                       long long ldc, float *scales, long long lds, void *stream);
+
+/*
+ * y = epilogue(x . W^T), both operands in 8 bits, for S >= 0 rows:
+ *     a[s][o] = sum_b x_scale[s][b] scale_inv[o/128][b] sum_{i in b} x[s][i] w[o][i]
+ * over the blocks b of 128 columns, with the epilogue of qgemv_fp8b128_linear.
+ *   w, scale_inv  as qgemv_fp8b128;  x, x_scale  as qgemv_fp8_quantize's codes
+ *   (rows ldx bytes apart) and scales (rows lds elements apart)
+ *   dtype  of y, bias and residual;  any I >= 1, O >= 1, any alignment of w and x
+ *   no workspace; y must not overlap what the call reads, but for the residual
+ *   in place
+ * Products of two codes are exact, a block's sums and the sum over blocks are
+ * f32 and y is rounded once.
+ * The transpose of W's codes with the transpose of its scales is W^T in the same
+ * format, so the gradient of x is the same call on those and on the quantized
+ * gradient of y.
+ * A NaN code or scale makes what it meets NaN.  The product of two scales that
+ * meet must be in f32's range.
+ */
+int qgemv_fp8b128_matmul(const void *w, const float *scale_inv, const void *x, long long ldx,
+                         const float *x_scale, long long lds, void *y, long long ldy, int S, int I,
+                         int O, int dtype, const qgemv_epilogue *epilogue, void *stream);
+
+/*
+ * The same grouped by expert, as qgemv_i4g_grouped: rows offsets[e] ..
+ * offsets[e + 1] - 1 of y are epilogue(x[rows[r]] . W_e^T) (x[r] where rows is
+ * NULL) with expert e's codes at byte e * w_stride and scales at element e *
+ * s_stride.  offsets, rows, T, R, y, the rows that are left, the epilogue and
+ * refusals as there (sizes that need 2^32 work items are refused).
+ *   workspace  qgemv_matmul_grouped_workspace(R, E) bytes, 256-byte aligned
+ */
+size_t qgemv_matmul_grouped_workspace(int R, int E);
+int qgemv_fp8b128_matmul_grouped(const void *w, const float *scale_inv, long long w_stride,
+                                 long long s_stride, int E, const int32_t *offsets,
+                                 const int32_t *rows, const void *x, long long ldx,
+                                 const float *x_scale, long long lds, int T, void *y,
+                                 long long ldy, int R, int I, int O, int dtype,
+                                 const qgemv_epilogue *epilogue, void *workspace, size_t ws_bytes,
+                                 void *stream);
+
+/*
+ * Token rows in expert order, y[r] = x[tokens[r]] (dtype, bit for bit), and the
+ * gradient of that, dx[t] = sum_k dy[pos[t][k]] (f32 sums, k ascending, no
+ * atomics, rounded once).
+ *   tokens  int32 [R] as qgemv_moe_group gives; a row of index -1 is left as it
+ *           was, any other index outside [0, T) makes its row of y NaN
+ *   pos     int32 [T][K] as qgemv_moe_group gives; a slot of index -1 had no row
+ *           and adds nothing, any other index outside [0, R) makes row t of dx NaN
+ *   rows of x, y, dy, dx are ld elements apart; outputs overlap nothing
+ *   R = 0 (dispatch) and T = 0 (gradient) launch nothing; 1 <= K <= 64
+ */
+int qgemv_moe_dispatch(const void *x, long long ldx, int T, const int32_t *tokens, int R, int I,
+                       void *y, long long ldy, int dtype, void *stream);
+int qgemv_moe_dispatch_grad(const void *dy, long long lddy, int R, const int32_t *pos, int T,
+                            int K, int I, void *dx, long long lddx, int dtype, void *stream);
+
+/*
+ * The gradients of qgemv_moe_combine from that of y (the residual's is dy):
+ *     dh[r] = gates[t][k] * dy[t]  for the slot (t, k) of row r
+ *     dgates[t][k] = sum over columns of h[pos[t][k]] * dy[t]
+ * (f32 products and sums in a fixed order, no atomics, dh rounded once).
+ *   tokens, pos  one qgemv_moe_group's.  A row belongs to the token that tokens
+ *   names; slots of that token that name it twice add their gates.  Rows that no
+ *   slot of their token names are left as they were in dh.  A slot that names a
+ *   row outside [0, R) or of another token gets a NaN in dgates and no row.
+ *   T = 0 launches nothing; 1 <= K <= 64; outputs overlap nothing
+ */
+int qgemv_moe_combine_grad(const void *dy, long long lddy, const void *h, long long ldh, int R,
+                           const int32_t *tokens, const int32_t *pos, const float *gates, int T,
+                           int K, int O, void *dh, long long lddh, float *dgates, int dtype,
+                           void *stream);
+
+/*
  * Decode-only entry points: write the decoded f32 weights W[O][I], each the
  * format's definition rounded once to f32 -- grouped int4 (q - 8) * s
  * (colibri PR #457, section 3), fp8 e4m3 * block scale (colibri PR #528,

@@ -90,6 +90,28 @@ _SIGS = {
     "qgemv_moe_combine": (C.c_int, [C.c_void_p, C.c_longlong, C.c_int, C.c_void_p, C.c_void_p,
                                     C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_longlong,
                                     C.c_void_p, C.c_longlong, C.c_int, C.c_void_p]),
+    "qgemv_fp8_quantize": (C.c_int, [C.c_void_p, C.c_longlong, C.c_int, C.c_int, C.c_int,
+                                     C.c_void_p, C.c_longlong, C.c_void_p, C.c_longlong,
+                                     C.c_void_p]),
+    "qgemv_fp8b128_matmul": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_longlong,
+                                       C.c_void_p, C.c_longlong, C.c_void_p, C.c_longlong, C.c_int,
+                                       C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p]),
+    "qgemv_matmul_grouped_workspace": (C.c_size_t, [C.c_int, C.c_int]),
+    "qgemv_fp8b128_matmul_grouped": (C.c_int, [C.c_void_p, C.c_void_p, C.c_longlong, C.c_longlong,
+                                               C.c_int, C.c_void_p, C.c_void_p, C.c_void_p,
+                                               C.c_longlong, C.c_void_p, C.c_longlong, C.c_int,
+                                               C.c_void_p, C.c_longlong, C.c_int, C.c_int, C.c_int,
+                                               C.c_int, C.c_void_p, C.c_void_p, C.c_size_t,
+                                               C.c_void_p]),
+    "qgemv_moe_dispatch": (C.c_int, [C.c_void_p, C.c_longlong, C.c_int, C.c_void_p, C.c_int,
+                                     C.c_int, C.c_void_p, C.c_longlong, C.c_int, C.c_void_p]),
+    "qgemv_moe_dispatch_grad": (C.c_int, [C.c_void_p, C.c_longlong, C.c_int, C.c_void_p, C.c_int,
+                                          C.c_int, C.c_int, C.c_void_p, C.c_longlong, C.c_int,
+                                          C.c_void_p]),
+    "qgemv_moe_combine_grad": (C.c_int, [C.c_void_p, C.c_longlong, C.c_void_p, C.c_longlong,
+                                         C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int,
+                                         C.c_int, C.c_int, C.c_void_p, C.c_longlong, C.c_void_p,
+                                         C.c_int, C.c_void_p]),
     "qgemv_dequant_i4g": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p,
                                     C.c_int, C.c_int, C.c_int, C.c_void_p]),
     "qgemv_dequant_fp8b128": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p,
@@ -250,6 +272,42 @@ def qgemv_i4g_grouped(w, scales, w_stride, s_stride, E, offsets, rows, x, ldx, T
 def qgemv_moe_combine(h, ldh, R, pos, gates, T, K, O, residual, ldr, y, ldy, dtype, stream):
     return lib().qgemv_moe_combine(h, ldh, R, pos, gates, T, K, O, residual, ldr, y, ldy, dtype,
                                    stream)
+
+
+def qgemv_fp8_quantize(x, ldx, S, I, dtype, codes, ldc, scales, lds, stream):
+    return lib().qgemv_fp8_quantize(x, ldx, S, I, dtype, codes, ldc, scales, lds, stream)
+
+
+def qgemv_fp8b128_matmul(w, scale_inv, x, ldx, x_scale, lds, y, ldy, S, I, O, dtype, epilogue,
+                         stream):
+    return lib().qgemv_fp8b128_matmul(w, scale_inv, x, ldx, x_scale, lds, y, ldy, S, I, O, dtype,
+                                      epilogue, stream)
+
+
+def qgemv_matmul_grouped_workspace(R, E):
+    return lib().qgemv_matmul_grouped_workspace(R, E)
+
+
+def qgemv_fp8b128_matmul_grouped(w, scale_inv, w_stride, s_stride, E, offsets, rows, x, ldx,
+                                 x_scale, lds, T, y, ldy, R, I, O, dtype, epilogue, workspace,
+                                 ws_bytes, stream):
+    return lib().qgemv_fp8b128_matmul_grouped(w, scale_inv, w_stride, s_stride, E, offsets, rows,
+                                              x, ldx, x_scale, lds, T, y, ldy, R, I, O, dtype,
+                                              epilogue, workspace, ws_bytes, stream)
+
+
+def qgemv_moe_dispatch(x, ldx, T, tokens, R, I, y, ldy, dtype, stream):
+    return lib().qgemv_moe_dispatch(x, ldx, T, tokens, R, I, y, ldy, dtype, stream)
+
+
+def qgemv_moe_dispatch_grad(dy, lddy, R, pos, T, K, I, dx, lddx, dtype, stream):
+    return lib().qgemv_moe_dispatch_grad(dy, lddy, R, pos, T, K, I, dx, lddx, dtype, stream)
+
+
+def qgemv_moe_combine_grad(dy, lddy, h, ldh, R, tokens, pos, gates, T, K, O, dh, lddh, dgates,
+                           dtype, stream):
+    return lib().qgemv_moe_combine_grad(dy, lddy, h, ldh, R, tokens, pos, gates, T, K, O, dh, lddh,
+                                        dgates, dtype, stream)
 
 
 def qgemv_dequant_i4g(w, scales, W, I, O, gs, stream):
@@ -809,6 +867,219 @@ def moe_combine(h, pos, gates, residual=None, out=None):
               _dev(gates, "gates", torch.float32), T, K, O, rp, ldr, yp, ldy, code,
               _raw_stream(h.device))
     return y
+
+
+# -- products of two 8-bit operands, gradients of routed rows ----------------
+# Codes are uint8 (or float8_e4m3fn, whose bytes they are).  x and its scales, and
+# the rows of routed tensors, may be row-strided views.
+def _codes(t, name):
+    """t's bytes, uint8."""
+    torch = _torch()
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
+        return t.view(torch.uint8)
+    return t
+
+
+def fp8_quantize(x, out=None, scales=None):
+    """x [S][I] (or [I]) f32 or bf16 -> (codes uint8 [S][I], scales f32
+    [S][ceil(I/128)]): e4m3 codes of x over its blocks' scales, max|x| / 448 of
+    each row and 128 columns.  out, scales: where to write them."""
+    torch = _torch()
+    code = _dtype_code(x, "x")
+    if x.dim() not in (1, 2):
+        raise ValueError("x must be [I] or [S, I]")
+    one = x.dim() == 1
+    if one:
+        x = x.unsqueeze(0)
+        out = out.unsqueeze(0) if out is not None and out.dim() == 1 else out
+        scales = scales.unsqueeze(0) if scales is not None and scales.dim() == 1 else scales
+    S, I = x.shape
+    _sizes("qgemv_fp8_quantize", S, I)
+    _no_gradient(x, scales)
+    _one_device(x, out, scales)
+    xp, ldx = _rows(x, "x", x.dtype)
+    ng = -(-I // 128)
+    if out is None:
+        out = torch.empty((S, I), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((S, ng), dtype=torch.float32, device=x.device)
+    cp, ldc = _rows(_codes(out, "out"), "out", torch.uint8, (S, I))
+    sp, lds = _rows(scales, "scales", torch.float32, (S, ng))
+    with _on(x.device):
+        _call("qgemv_fp8_quantize", xp, ldx, S, I, code, cp, ldc, sp, lds, _raw_stream(x.device))
+    return (out[0], scales[0]) if one else (out, scales)
+
+
+def _result_type(dtype, *ts):
+    """The type of y: as asked for, else that of a given tensor, else bfloat16."""
+    torch = _torch()
+    for t in ts:
+        if dtype is None and t is not None:
+            dtype = t.dtype
+    if dtype is None or dtype == torch.bfloat16:
+        return torch.bfloat16, 1
+    if dtype == torch.float32:
+        return dtype, 0
+    raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+
+
+def _result(out, R, oc, dtype, device):
+    if out is None:
+        out = _torch().empty((R, oc), dtype=dtype, device=device)
+        return out, out.data_ptr(), oc
+    return (out, *_rows(out, "out", dtype, (R, oc)))
+
+
+def fp8b128_matmul(w, scale_inv, x, x_scale, bias=None, act=None, gated=False, residual=None,
+                   dtype=None, out=None):
+    """fp8b128_linear's product with 8-bit activations: w codes [O][I], scale_inv
+    f32 [ceil(O/128)][ceil(I/128)], x and x_scale as ``fp8_quantize`` gives them
+    ([S][I], or [I]).  y [S][O] (gated: O/2 columns) of ``dtype``, float32 or
+    bfloat16: by default the type of out, residual or bias, else bfloat16.
+    The gradient of x is the product with w.t().contiguous() and
+    scale_inv.t().contiguous(), which are W^T in the same format."""
+    torch = _torch()
+    w, x = _codes(w, "w"), _codes(x, "x")
+    one = x.dim() == 1
+    if one:
+        x, x_scale = x.unsqueeze(0), x_scale.reshape(1, -1)
+        residual = residual.unsqueeze(0) if residual is not None and residual.dim() == 1 \
+            else residual
+        out = out.unsqueeze(0) if out is not None and out.dim() == 1 else out
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("w must be [O, I] and x [I] or [S, I]")
+    S, I = x.shape
+    O = w.shape[0]
+    _sizes("qgemv_fp8b128_matmul", S, I, O)
+    _shape(w, "w", (O, I))
+    _shape(scale_inv, "scale_inv", (-(-O // 128), -(-I // 128)))
+    dtype, code = _result_type(dtype, out, residual, bias)
+    _no_gradient(scale_inv, x_scale, bias, residual, out)
+    _one_device(w, scale_inv, x, x_scale, bias, residual, out)
+    xp, ldx = _rows(x, "x", torch.uint8)
+    xsp, lds = _rows(x_scale, "x_scale", torch.float32, (S, -(-I // 128)))
+    epi, oc = _epilogue(dtype, O, bias, act, gated, residual, S)
+    y, yp, ldy = _result(out, S, oc, dtype, x.device)
+    wp, sp = _dev(w, "w", torch.uint8), _dev(scale_inv, "scale_inv", torch.float32)
+    with _on(x.device):
+        _call("qgemv_fp8b128_matmul", wp, sp, xp, ldx, xsp, lds, yp, ldy, S, I, O, code, _ref(epi),
+              _raw_stream(x.device))
+    return y[0] if one else y
+
+
+def matmul_grouped_workspace(R, E, device):
+    """Scratch for one fp8b128_matmul_grouped call of these sizes."""
+    return _torch().empty(max(int(qgemv_matmul_grouped_workspace(R, E)), 1),
+                          dtype=_torch().uint8, device=device)
+
+
+def fp8b128_matmul_grouped(w, scale_inv, x, x_scale, offsets, rows=None, bias=None, act=None,
+                           gated=False, dtype=None, workspace=None, out=None):
+    """Each expert's rows times its fp8 matrix, ``i4g_grouped`` with both operands
+    in 8 bits: w codes [E][O][I], scale_inv f32 [E][ceil(O/128)][ceil(I/128)], x
+    and x_scale as ``fp8_quantize`` gives them, offsets int32 [E+1], bias [E][O].
+    Row r of y reads x[rows[r]] (x[r] without rows); rows of no expert are left as
+    they are in ``out``.  dtype as in ``fp8b128_matmul``."""
+    torch = _torch()
+    w, x = _codes(w, "w"), _codes(x, "x")
+    if w.dim() != 3 or x.dim() != 2:
+        raise ValueError("w must be [E, O, I] and x [T, I]")
+    E, O = w.shape[0], w.shape[1]
+    T, I = x.shape
+    R = T if rows is None else rows.numel()
+    _sizes("qgemv_fp8b128_matmul_grouped", T, R, E, I, O)
+    _shape(w, "w", (E, O, I))
+    _shape(scale_inv, "scale_inv", (E, -(-O // 128), -(-I // 128)))
+    _shape(offsets, "offsets", (E + 1,))
+    if rows is not None:
+        _shape(rows, "rows", (R,))
+    dtype, code = _result_type(dtype, out, bias)
+    _no_gradient(scale_inv, x_scale, bias, out)
+    _one_device(w, scale_inv, x, x_scale, offsets, rows, bias, workspace, out)
+    xp, ldx = _rows(x, "x", torch.uint8)
+    xsp, lds = _rows(x_scale, "x_scale", torch.float32, (T, -(-I // 128)))
+    epi, oc = _epilogue(dtype, O, bias, act, gated, None, R, E)
+    y, yp, ldy = _result(out, R, oc, dtype, x.device)
+    wp, sp = _dev(w, "w", torch.uint8), _dev(scale_inv, "scale_inv", torch.float32)
+    op = _dev(offsets, "offsets", torch.int32)
+    rp = _dev(rows, "rows", torch.int32) if rows is not None else None
+    with _on(x.device):
+        ws, wsp, nbytes = _scratch(workspace, qgemv_matmul_grouped_workspace(R, E), x.device)
+        _call("qgemv_fp8b128_matmul_grouped", wp, sp, O * I, scale_inv.shape[1] * scale_inv.shape[2], E, op,
+              rp, xp, ldx, xsp, lds, T, yp, ldy, R, I, O, code, _ref(epi), wsp, nbytes,
+              _raw_stream(x.device))
+    return y
+
+
+def moe_dispatch(x, tokens, out=None):
+    """Token rows in expert order: y[r] = x[tokens[r]], x [T][I] f32 or bf16, tokens
+    int32 [R] as ``moe_group`` gives; rows of index -1 are left as they are in
+    ``out``."""
+    torch = _torch()
+    code = _dtype_code(x, "x")
+    if x.dim() != 2 or tokens.dim() != 1:
+        raise ValueError("x must be [T, I] and tokens [R]")
+    T, I = x.shape
+    R = tokens.shape[0]
+    _sizes("qgemv_moe_dispatch", T, I, R)
+    _no_gradient(x, out)
+    _one_device(x, tokens, out)
+    xp, ldx = _rows(x, "x", x.dtype)
+    tp = _dev(tokens, "tokens", torch.int32)
+    y, yp, ldy = _new_rows(out, "out", R, I, x)
+    with _on(x.device):
+        _call("qgemv_moe_dispatch", xp, ldx, T, tp, R, I, yp, ldy, code, _raw_stream(x.device))
+    return y
+
+
+def moe_dispatch_grad(dy, pos, out=None):
+    """The gradient of ``moe_dispatch``: dx[t] = sum_k dy[pos[t][k]], dy [R][I] f32 or
+    bf16, pos int32 [T][K]; slots of index -1 add nothing."""
+    torch = _torch()
+    code = _dtype_code(dy, "dy")
+    if dy.dim() != 2 or pos.dim() != 2:
+        raise ValueError("dy must be [R, I] and pos [T, K]")
+    R, I = dy.shape
+    T, K = pos.shape
+    _sizes("qgemv_moe_dispatch_grad", R, I, T, K)
+    _no_gradient(dy, out)
+    _one_device(dy, pos, out)
+    dyp, lddy = _rows(dy, "dy", dy.dtype)
+    pp = _dev(pos, "pos", torch.int32)
+    dx, dxp, lddx = _new_rows(out, "out", T, I, dy)
+    with _on(dy.device):
+        _call("qgemv_moe_dispatch_grad", dyp, lddy, R, pp, T, K, I, dxp, lddx, code,
+              _raw_stream(dy.device))
+    return dx
+
+
+def moe_combine_grad(dy, h, tokens, pos, gates, out=None):
+    """The gradients of ``moe_combine``, (dh [R][O], dgates f32 [T][K]), from that of
+    its y: dh[r] = gates[t][k] dy[t] for the slot (t, k) of row r, dgates[t][k] =
+    <h[pos[t][k]], dy[t]>.  dy [T][O] and h of one type, f32 or bf16, tokens int32
+    [R] and pos int32 [T][K] of one ``moe_group``; rows of no slot are left as they
+    are in ``out``.  The gradient of the residual is dy itself."""
+    torch = _torch()
+    code = _dtype_code(h, "h")
+    if h.dim() != 2 or pos.dim() != 2:
+        raise ValueError("h must be [R, O] and pos [T, K]")
+    R, O = h.shape
+    T, K = pos.shape
+    _sizes("qgemv_moe_combine_grad", R, O, T, K)
+    _shape(tokens, "tokens", (R,))
+    _shape(gates, "gates", (T, K))
+    _no_gradient(dy, h, gates, out)
+    _one_device(dy, h, tokens, pos, gates, out)
+    dyp, lddy = _rows(dy, "dy", h.dtype, (T, O))
+    hp, ldh = _rows(h, "h", h.dtype)
+    tp, pp = _dev(tokens, "tokens", torch.int32), _dev(pos, "pos", torch.int32)
+    gp = _dev(gates, "gates", torch.float32)
+    dh, dhp, lddh = _new_rows(out, "out", R, O, h)
+    dgates = torch.empty((T, K), dtype=torch.float32, device=h.device)
+    with _on(h.device):
+        _call("qgemv_moe_combine_grad", dyp, lddy, hp, ldh, R, tp, pp, gp, T, K, O, dhp, lddh,
+              dgates.data_ptr(), code, _raw_stream(h.device))
+    return dh, dgates
 
 
 def dequant_i4g(w, scales, I, gs):

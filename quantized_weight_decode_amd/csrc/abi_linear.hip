@@ -3,78 +3,11 @@
 //
 // As in abi.hip, validation looks at pointer values, dimensions and sizes
 // only, so a refused call is safe with any pointers.
-#include "qg_linear.h"
-#include "qg_rows.h"
+#include "qg_check.h"
 
 namespace {
 
-using qg::Rows;
-using qg::block;
-using qg::overlap;
-using qg::overlaps_any;
-using qg::rows_of;
-
-constexpr int MAX_DIM = 1 << 24;
-constexpr int MAX_EXPERTS = 1024;
-
-bool misaligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) != 0; }
-
-int launched(hipError_t e) { return e == hipSuccess ? QGEMV_OK : QGEMV_E_HIP; }
-
-bool bad_dtype(int dtype) { return dtype != QGEMV_F32 && dtype != QGEMV_BF16; }
-
-int element(int dtype) { return dtype == QGEMV_BF16 ? 2 : 4; }
-
-bool bad_sizes(int rows, int I, int O)
-{
-    return rows < 0 || rows > MAX_DIM || I < 1 || O < 1 || I > MAX_DIM || O > MAX_DIM;
-}
-
-// y against what a product reads (the residual may be y itself), and the
-// scratch against both.
-bool overlapping(const qg::LinearArgs &a, long long w_bytes, long long s_bytes,
-                 const void *workspace, size_t ws_bytes)
-{
-    const long long el = a.dtype == QGEMV_BF16 ? 2 : 4, oc = a.gated ? a.O / 2 : a.O;
-    const Rows y = rows_of(a.y, a.R, oc * el, a.ldy * el);
-    const Rows res = rows_of(a.residual, a.R, oc * el, a.ldr * el);
-    const Rows in[] = {rows_of(a.x, a.T, a.I * el, a.ldx * el),
-                       rows_of(a.w, a.E, w_bytes, a.offsets ? a.w_stride : w_bytes),
-                       rows_of(a.scales, a.E, s_bytes, a.offsets ? a.s_stride * 4 : s_bytes),
-                       block(a.bias, (long long)a.E * a.O * el),
-                       block(a.rows, (long long)a.R * 4),
-                       block(a.offsets, (long long)(a.E + 1) * 4)};
-    constexpr int N = sizeof(in) / sizeof(in[0]);
-    const Rows ws = block(workspace, (long long)ws_bytes);
-    const bool in_place = a.residual == a.y && (a.R == 1 || a.ldr == a.ldy);
-    return overlaps_any(y, in, N) || (!in_place && overlap(y, res)) || overlap(y, ws) ||
-           overlap(res, ws) || overlaps_any(ws, in, N);
-}
-
-// more products than any memory holds outputs for
-bool too_large(long long rows, int O) { return rows * O > 1LL << 39; }
-
-// Fills a's type, strides and epilogue from the arguments and checks them.
-int take(qg::LinearArgs &a, const qgemv_epilogue *e, bool with_residual)
-{
-    if (bad_dtype(a.dtype)) return QGEMV_E_ARG;
-    a.act = e ? e->act : QGEMV_ACT_NONE;
-    a.gated = e ? e->gated : 0;
-    a.bias = e ? e->bias : nullptr;
-    a.residual = e ? e->residual : nullptr;
-    a.ldr = a.residual ? e->ld_residual : 0;
-    if (a.act < QGEMV_ACT_NONE || a.act > QGEMV_ACT_GELU_TANH || (a.gated != 0 && a.gated != 1))
-        return QGEMV_E_ARG;
-    if (a.residual && !with_residual) return QGEMV_E_ARG;
-    if (a.gated && (a.O & 1)) return QGEMV_E_DIMS;
-    const int oc = a.gated ? a.O / 2 : a.O;
-    if (a.ldx < a.I || a.ldy < oc || (a.residual && a.ldr < oc)) return QGEMV_E_DIMS;
-    const uintptr_t el = element(a.dtype);
-    if (misaligned(a.scales, 4) || misaligned(a.x, el) || misaligned(a.y, el) ||
-        misaligned(a.bias, el) || misaligned(a.residual, el))
-        return QGEMV_E_ALIGN;
-    return QGEMV_OK;
-}
+using namespace qg;
 
 int dense(qg::WeightFormat fmt, const void *w, const float *scales, const void *x, long long ldx,
           void *y, long long ldy, int S, int I, int O, int gs, int dtype,
@@ -97,14 +30,14 @@ int dense(qg::WeightFormat fmt, const void *w, const float *scales, const void *
     a.gs = gs;
     a.ng = (I + gs - 1) / gs;
     a.dtype = dtype;
-    if (int e = take(a, epilogue, true)) return e;
+    if (int e = take(a, element(dtype), epilogue, true)) return e;
     if (S == 0) return QGEMV_OK;
     if (too_large(S, O)) return QGEMV_E_DIMS;
     const size_t need = qg::linear_workspace(S, S, 0, I, dtype);
     if (need > 0 && (!workspace || misaligned(workspace, 256) || ws_bytes < need))
         return QGEMV_E_WORKSPACE;
     const bool i4 = fmt == qg::FMT_I4G;
-    if (overlapping(a, (long long)O * (i4 ? (I + 1) / 2 : I),
+    if (overlapping(a, element(dtype), (long long)O * (i4 ? (I + 1) / 2 : I),
                     4LL * a.ng * (i4 ? O : (O + 127) / 128), workspace, need))
         return QGEMV_E_OVERLAP;
     return launched(qg::launch_linear(fmt, a, workspace, (hipStream_t)stream));
@@ -179,12 +112,12 @@ int qgemv_i4g_grouped(const void *w, const float *scales, long long w_stride, lo
     a.gs = gs;
     a.ng = (int)ng;
     a.dtype = dtype;
-    if (int e = take(a, epilogue, false)) return e;
+    if (int e = take(a, element(dtype), epilogue, false)) return e;
     if (R == 0) return QGEMV_OK;
     if (too_large(R, O) || !qg::linear_launchable(qg::FMT_I4G, a)) return QGEMV_E_DIMS;
     const size_t need = qg::linear_workspace(T, R, E, I, dtype);
     if (!workspace || misaligned(workspace, 256) || ws_bytes < need) return QGEMV_E_WORKSPACE;
-    if (overlapping(a, O * rb, 4 * O * ng, workspace, need)) return QGEMV_E_OVERLAP;
+    if (overlapping(a, element(dtype), O * rb, 4 * O * ng, workspace, need)) return QGEMV_E_OVERLAP;
     return launched(qg::launch_linear(qg::FMT_I4G, a, workspace, (hipStream_t)stream));
 }
 

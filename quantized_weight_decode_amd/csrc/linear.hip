@@ -353,12 +353,6 @@ __global__ __launch_bounds__(1024) void plan_tiles(const int32_t *__restrict__ o
     }
 }
 
-// tiles that R rows of E experts can need
-long long max_tiles(int R, int E, int bm)
-{
-    return (long long)R / bm + (E < R ? E : R);
-}
-
 // Tile of a product: the one whose busiest CU has the least to do, estimated
 // as workgroups per CU times the cost of one, relative to 128 x 256 (a fifth
 // more for a tile that has its CU to itself, one wave per SIMD); f32 counts two
@@ -444,6 +438,18 @@ void run_general(const LinearArgs &a, Shape shape, const RowTile *tiles, unsigne
 }
 
 }  // namespace
+
+long long max_tiles(int R, int E, int bm)
+{
+    return (long long)R / bm + (E < R ? E : R);
+}
+
+hipError_t launch_plan_tiles(const int32_t *offsets, int E, int R, int bm, RowTile *tiles,
+                             int ntiles, hipStream_t st)
+{
+    hipLaunchKernelGGL(plan_tiles, dim3(1), dim3(1024), 0, st, offsets, E, R, bm, tiles, ntiles);
+    return hipGetLastError();
+}
 
 size_t linear_workspace(int T, int R, int E, int I, int dtype)
 {
@@ -538,9 +544,7 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hip
     RowTile *tiles = nullptr;
     if (a.offsets) {
         tiles = static_cast<RowTile *>(ws);
-        hipLaunchKernelGGL(plan_tiles, dim3(1), dim3(1024), 0, st, a.offsets, a.E, a.R, bm, tiles,
-                           (int)mt);
-        hipError_t e = hipGetLastError();
+        const hipError_t e = launch_plan_tiles(a.offsets, a.E, a.R, bm, tiles, (int)mt, st);
         if (e != hipSuccess) return e;
         ws = static_cast<char *>(ws) + align256((size_t)max_tiles(a.R, a.E, 16) * sizeof(RowTile));
     }
