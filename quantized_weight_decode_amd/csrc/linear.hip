@@ -272,10 +272,10 @@ linear_general(LinearArgs a, const RowTile *__restrict__ tiles)
 
 // Row tiles of a grouped product, from the experts' offsets on the device:
 // first the whole blocks of bm rows, experts in ascending order, then the
-// experts' last, shorter blocks, the longest first (in sixteenths of rows), so
-// that the short ones fill the end of the launch; the rest of the list is
-// empty.  Offsets are clamped to 0..R and a negative count counts as none, so
-// that every tile lies within y.  One workgroup, a thread per expert.
+// experts' last, shorter blocks, the longest first (in classes of 16 rows, 32 of
+// a block of 256), so that the short ones fill the end of the launch; the rest of
+// the list is empty.  Offsets are clamped to 0..R and a negative count counts as
+// none, so that every tile lies within y.  One workgroup, a thread per expert.
 __global__ __launch_bounds__(1024) void plan_tiles(const int32_t *__restrict__ offsets, int E,
                                                    int R, int bm, RowTile *__restrict__ tiles,
                                                    int ntiles)
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(1024) void plan_tiles(const int32_t *__restrict__ o
     }
     if (lane == 63) wsum[wave] = incl;
     // length class of the short tile: 0 the longest, -1 none
-    const int cls = rest ? (bm - rest) / 16 : -1;
+    const int cls = rest ? (bm - rest) / (bm > 128 ? bm / 8 : 16) : -1;
     int rank = 0;
 #pragma unroll
     for (int c = 0; c < 8; c++) {

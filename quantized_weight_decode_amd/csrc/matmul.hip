@@ -9,6 +9,7 @@ namespace {
 
 // The kernel of a product, its row tiles and its launch's work items.
 struct Choice {
+    bool tile;
     int bm;
     long long mt, items;
 };
@@ -18,10 +19,18 @@ Choice choose(const MatmulArgs &p)
     Choice c{};
     const LinearArgs &a = p.a;
     const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
+    c.tile = rows > 64 && matmul_tile_fits(p);
     c.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    if (c.tile) c.bm = 128;
     c.mt = a.offsets ? max_tiles(a.R, a.E, c.bm) : (a.R + c.bm - 1) / c.bm;
-    c.items = matmul_stream_items(p, c.bm, c.mt);
+    c.items = c.tile ? matmul_tile_items(p, c.bm, c.mt) : matmul_stream_items(p, c.bm, c.mt);
     return c;
+}
+
+hipError_t run(const MatmulArgs &p, const Choice &c, const RowTile *tiles, hipStream_t st)
+{
+    return c.tile ? launch_matmul_tile(p, c.bm, tiles, (int)c.mt, st)
+                  : launch_matmul_stream(p, c.bm, tiles, (int)c.mt, st);
 }
 
 }  // namespace
@@ -46,7 +55,7 @@ hipError_t launch_matmul(const MatmulArgs &args, void *ws, hipStream_t st)
         RowTile *const tiles = static_cast<RowTile *>(ws);
         const hipError_t e = launch_plan_tiles(a.offsets, a.E, a.R, c.bm, tiles, (int)c.mt, st);
         if (e != hipSuccess) return e;
-        return launch_matmul_stream(p, c.bm, tiles, (int)c.mt, st);
+        return run(p, c, tiles, st);
     }
     // slices of rows whose work items fit a launch (64 rows of 2^24 outputs do)
     int slice = args.a.R;
@@ -64,7 +73,7 @@ hipError_t launch_matmul(const MatmulArgs &args, void *ws, hipStream_t st)
             a.residual = static_cast<const char *>(args.a.residual) + (long long)(r * a.ldr * el);
         const Choice c = choose(p);
         if (c.items > MAX_ITEMS) return hipErrorInvalidValue;
-        const hipError_t e = launch_matmul_stream(p, c.bm, nullptr, (int)c.mt, st);
+        const hipError_t e = run(p, c, nullptr, st);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

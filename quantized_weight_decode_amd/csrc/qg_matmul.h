@@ -24,6 +24,14 @@ long long matmul_stream_items(const MatmulArgs &p, int bm, long long ntm);
 hipError_t launch_matmul_stream(const MatmulArgs &p, int bm, const RowTile *tiles, int ntm,
                                 hipStream_t st);
 
+// The tile kernel (matmul_tile.hip): row tiles of 128 or 256 (256: bfloat16, both
+// operands' rows on 16 bytes).
+bool matmul_tile_fits(const MatmulArgs &p);
+bool matmul_tile_direct(const MatmulArgs &p);
+long long matmul_tile_items(const MatmulArgs &p, int bm, long long ntm);
+hipError_t launch_matmul_tile(const MatmulArgs &p, int bm, const RowTile *tiles, int ntm,
+                              hipStream_t st);
+
 hipError_t launch_fp8_quantize(const void *x, long long ldx, int S, int I, int dtype,
                                uint8_t *codes, long long ldc, float *scales, long long lds,
                                hipStream_t st);
