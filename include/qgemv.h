@@ -429,8 +429,9 @@ int qgemv_fp8_quantize(const void *x, long long ldx, int S, int I, int dtype, vo
  *   w, scale_inv  as qgemv_fp8b128;  x, x_scale  as qgemv_fp8_quantize's codes
  *   (rows ldx bytes apart) and scales (rows lds elements apart)
  *   dtype  of y, bias and residual;  any I >= 1, O >= 1, any alignment of w and x
- *   no workspace; y must not overlap what the call reads, but for the residual
- *   in place
+ *   y must not overlap what the call reads, but for the residual in place
+ *   workspace  qgemv_matmul_workspace bytes (may be 0: then it may be NULL), 256-byte
+ *              aligned, overwritten; calls that may overlap in time need one each
  * Products of two codes are exact, a block's sums and the sum over blocks are
  * f32 and y is rounded once.
  * The transpose of W's codes with the transpose of its scales is W^T in the same
@@ -439,9 +440,11 @@ int qgemv_fp8_quantize(const void *x, long long ldx, int S, int I, int dtype, vo
  * A NaN code or scale makes what it meets NaN.  The product of two scales that
  * meet must be in f32's range.
  */
+size_t qgemv_matmul_workspace(int S, int I, int O, int dtype, int gated);
 int qgemv_fp8b128_matmul(const void *w, const float *scale_inv, const void *x, long long ldx,
                          const float *x_scale, long long lds, void *y, long long ldy, int S, int I,
-                         int O, int dtype, const qgemv_epilogue *epilogue, void *stream);
+                         int O, int dtype, const qgemv_epilogue *epilogue, void *workspace,
+                         size_t ws_bytes, void *stream);
 
 /*
  * The same grouped by expert, as qgemv_i4g_grouped: rows offsets[e] ..

@@ -95,7 +95,9 @@ _SIGS = {
                                      C.c_void_p]),
     "qgemv_fp8b128_matmul": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_longlong,
                                        C.c_void_p, C.c_longlong, C.c_void_p, C.c_longlong, C.c_int,
-                                       C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p]),
+                                       C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
+                                       C.c_size_t, C.c_void_p]),
+    "qgemv_matmul_workspace": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int]),
     "qgemv_matmul_grouped_workspace": (C.c_size_t, [C.c_int, C.c_int]),
     "qgemv_fp8b128_matmul_grouped": (C.c_int, [C.c_void_p, C.c_void_p, C.c_longlong, C.c_longlong,
                                                C.c_int, C.c_void_p, C.c_void_p, C.c_void_p,
@@ -278,10 +280,14 @@ def qgemv_fp8_quantize(x, ldx, S, I, dtype, codes, ldc, scales, lds, stream):
     return lib().qgemv_fp8_quantize(x, ldx, S, I, dtype, codes, ldc, scales, lds, stream)
 
 
+def qgemv_matmul_workspace(S, I, O, dtype, gated):
+    return lib().qgemv_matmul_workspace(S, I, O, dtype, gated)
+
+
 def qgemv_fp8b128_matmul(w, scale_inv, x, ldx, x_scale, lds, y, ldy, S, I, O, dtype, epilogue,
-                         stream):
+                         workspace, ws_bytes, stream):
     return lib().qgemv_fp8b128_matmul(w, scale_inv, x, ldx, x_scale, lds, y, ldy, S, I, O, dtype,
-                                      epilogue, stream)
+                                      epilogue, workspace, ws_bytes, stream)
 
 
 def qgemv_matmul_grouped_workspace(R, E):
@@ -930,8 +936,16 @@ def _result(out, R, oc, dtype, device):
     return (out, *_rows(out, "out", dtype, (R, oc)))
 
 
+def matmul_workspace(S, I, O, dtype, device, gated=False):
+    """Scratch for one fp8b128_matmul call of these sizes."""
+    torch = _torch()
+    code = _dtype_code(torch.empty(0, dtype=dtype), "dtype")
+    return torch.empty(max(int(qgemv_matmul_workspace(S, I, O, code, int(bool(gated)))), 1),
+                       dtype=torch.uint8, device=device)
+
+
 def fp8b128_matmul(w, scale_inv, x, x_scale, bias=None, act=None, gated=False, residual=None,
-                   dtype=None, out=None):
+                   dtype=None, workspace=None, out=None):
     """fp8b128_linear's product with 8-bit activations: w codes [O][I], scale_inv
     f32 [ceil(O/128)][ceil(I/128)], x and x_scale as ``fp8_quantize`` gives them
     ([S][I], or [I]).  y [S][O] (gated: O/2 columns) of ``dtype``, float32 or
@@ -955,15 +969,17 @@ def fp8b128_matmul(w, scale_inv, x, x_scale, bias=None, act=None, gated=False, r
     _shape(scale_inv, "scale_inv", (-(-O // 128), -(-I // 128)))
     dtype, code = _result_type(dtype, out, residual, bias)
     _no_gradient(scale_inv, x_scale, bias, residual, out)
-    _one_device(w, scale_inv, x, x_scale, bias, residual, out)
+    _one_device(w, scale_inv, x, x_scale, bias, residual, workspace, out)
     xp, ldx = _rows(x, "x", torch.uint8)
     xsp, lds = _rows(x_scale, "x_scale", torch.float32, (S, -(-I // 128)))
     epi, oc = _epilogue(dtype, O, bias, act, gated, residual, S)
     y, yp, ldy = _result(out, S, oc, dtype, x.device)
     wp, sp = _dev(w, "w", torch.uint8), _dev(scale_inv, "scale_inv", torch.float32)
     with _on(x.device):
+        ws, wsp, nbytes = _scratch(
+            workspace, qgemv_matmul_workspace(S, I, O, code, int(bool(gated))), x.device)
         _call("qgemv_fp8b128_matmul", wp, sp, xp, ldx, xsp, lds, yp, ldy, S, I, O, code, _ref(epi),
-              _raw_stream(x.device))
+              wsp, nbytes, _raw_stream(x.device))
     return y[0] if one else y
 
 

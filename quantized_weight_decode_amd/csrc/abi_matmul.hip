@@ -70,9 +70,16 @@ int qgemv_fp8_quantize(const void *x, long long ldx, int S, int I, int dtype, vo
                                         scales, lds, (hipStream_t)stream));
 }
 
+size_t qgemv_matmul_workspace(int S, int I, int O, int dtype, int gated)
+{
+    if (bad_sizes(S, I, O) || S == 0 || bad_dtype(dtype) || (gated && (O & 1))) return 0;
+    return matmul_workspace(S, I, O, dtype, gated != 0);
+}
+
 int qgemv_fp8b128_matmul(const void *w, const float *scale_inv, const void *x, long long ldx,
                          const float *x_scale, long long lds, void *y, long long ldy, int S, int I,
-                         int O, int dtype, const qgemv_epilogue *epilogue, void *stream)
+                         int O, int dtype, const qgemv_epilogue *epilogue, void *workspace,
+                         size_t ws_bytes, void *stream)
 {
     if (bad_sizes(S, I, O)) return QGEMV_E_DIMS;
     if (S > 0 && (!w || !scale_inv || !x || !x_scale || !y)) return QGEMV_E_NULL;
@@ -83,14 +90,17 @@ int qgemv_fp8b128_matmul(const void *w, const float *scale_inv, const void *x, l
         return e;
     if (S == 0) return QGEMV_OK;
     if (too_large(S, O)) return QGEMV_E_DIMS;
-    if (overlapping(p, nullptr, 0)) return QGEMV_E_OVERLAP;
-    return launched(launch_matmul(p, nullptr, (hipStream_t)stream));
+    const size_t need = matmul_workspace(S, I, O, dtype, p.a.gated);
+    if (need > 0 && (!workspace || misaligned(workspace, 256) || ws_bytes < need))
+        return QGEMV_E_WORKSPACE;
+    if (overlapping(p, workspace, need)) return QGEMV_E_OVERLAP;
+    return launched(launch_matmul(p, workspace, (hipStream_t)stream));
 }
 
 size_t qgemv_matmul_grouped_workspace(int R, int E)
 {
     if (R < 0 || R > MAX_DIM || E < 1 || E > MAX_EXPERTS) return 0;
-    return matmul_workspace(R, E);
+    return matmul_grouped_workspace(R, E);
 }
 
 int qgemv_fp8b128_matmul_grouped(const void *w, const float *scale_inv, long long w_stride,
@@ -119,7 +129,7 @@ int qgemv_fp8b128_matmul_grouped(const void *w, const float *scale_inv, long lon
         return e;
     if (R == 0) return QGEMV_OK;
     if (too_large(R, O) || !matmul_launchable(p)) return QGEMV_E_DIMS;
-    const size_t need = matmul_workspace(R, E);
+    const size_t need = matmul_grouped_workspace(R, E);
     if (!workspace || misaligned(workspace, 256) || ws_bytes < need) return QGEMV_E_WORKSPACE;
     if (overlapping(p, workspace, need)) return QGEMV_E_OVERLAP;
     return launched(launch_matmul(p, workspace, (hipStream_t)stream));

@@ -272,10 +272,10 @@ linear_general(LinearArgs a, const RowTile *__restrict__ tiles)
 
 // Row tiles of a grouped product, from the experts' offsets on the device:
 // first the whole blocks of bm rows, experts in ascending order, then the
-// experts' last, shorter blocks, the longest first (in classes of 16 rows, 32 of
-// a block of 256), so that the short ones fill the end of the launch; the rest of
-// the list is empty.  Offsets are clamped to 0..R and a negative count counts as
-// none, so that every tile lies within y.  One workgroup, a thread per expert.
+// experts' last, shorter blocks, the longest first (in sixteenths of rows), so
+// that the short ones fill the end of the launch; the rest of the list is
+// empty.  Offsets are clamped to 0..R and a negative count counts as none, so
+// that every tile lies within y.  One workgroup, a thread per expert.
 __global__ __launch_bounds__(1024) void plan_tiles(const int32_t *__restrict__ offsets, int E,
                                                    int R, int bm, RowTile *__restrict__ tiles,
                                                    int ntiles)
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(1024) void plan_tiles(const int32_t *__restrict__ o
     }
     if (lane == 63) wsum[wave] = incl;
     // length class of the short tile: 0 the longest, -1 none
-    const int cls = rest ? (bm - rest) / (bm > 128 ? bm / 8 : 16) : -1;
+    const int cls = rest ? (bm - rest) / 16 : -1;
     int rank = 0;
 #pragma unroll
     for (int c = 0; c < 8; c++) {
@@ -351,6 +351,12 @@ __global__ __launch_bounds__(1024) void plan_tiles(const int32_t *__restrict__ o
         }
         tiles[i] = t;
     }
+}
+
+// tiles that R rows of E experts can need
+long long max_tiles(int R, int E, int bm)
+{
+    return (long long)R / bm + (E < R ? E : R);
 }
 
 // Tile of a product: the one whose busiest CU has the least to do, estimated
@@ -438,18 +444,6 @@ void run_general(const LinearArgs &a, Shape shape, const RowTile *tiles, unsigne
 }
 
 }  // namespace
-
-long long max_tiles(int R, int E, int bm)
-{
-    return (long long)R / bm + (E < R ? E : R);
-}
-
-hipError_t launch_plan_tiles(const int32_t *offsets, int E, int R, int bm, RowTile *tiles,
-                             int ntiles, hipStream_t st)
-{
-    hipLaunchKernelGGL(plan_tiles, dim3(1), dim3(1024), 0, st, offsets, E, R, bm, tiles, ntiles);
-    return hipGetLastError();
-}
 
 size_t linear_workspace(int T, int R, int E, int I, int dtype)
 {
@@ -544,7 +538,9 @@ hipError_t launch_linear(WeightFormat fmt, const LinearArgs &args, void *ws, hip
     RowTile *tiles = nullptr;
     if (a.offsets) {
         tiles = static_cast<RowTile *>(ws);
-        const hipError_t e = launch_plan_tiles(a.offsets, a.E, a.R, bm, tiles, (int)mt, st);
+        hipLaunchKernelGGL(plan_tiles, dim3(1), dim3(1024), 0, st, a.offsets, a.E, a.R, bm, tiles,
+                           (int)mt);
+        hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         ws = static_cast<char *>(ws) + align256((size_t)max_tiles(a.R, a.E, 16) * sizeof(RowTile));
     }

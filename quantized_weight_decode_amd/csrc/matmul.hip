@@ -1,5 +1,6 @@
 // matmul.hip -- products whose both operands are e4m3, dense or grouped by
 // expert: the choice among kernels, and slices of rows.
+#include <stdlib.h>
 #include "qg_launch.h"
 #include "qg_matmul.h"
 
@@ -7,37 +8,140 @@ namespace qg {
 
 namespace {
 
+// Row tiles of a grouped product, from the experts' offsets on the device: each
+// expert's rows in blocks of bm, experts in ascending order; the rest of the list
+// is empty.  Offsets are clamped to 0..R and a negative count counts as none, so
+// that every tile lies within y.  One workgroup, a thread per expert.
+__global__ __launch_bounds__(1024) void plan_experts(const int32_t *__restrict__ offsets, int E,
+                                                     int R, int bm,
+                                                     ExpertTile *__restrict__ tiles, int ntiles)
+{
+    __shared__ int base[1025];           // first tile of each expert
+    __shared__ int start[1024], rows[1024];
+    __shared__ int wsum[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int lo = 0, n = 0;
+    if (tid < E) {
+        lo = min(max(offsets[tid], 0), R);
+        n = max(min(max(offsets[tid + 1], 0), R) - lo, 0);
+    }
+    const int mine = (n + bm - 1) / bm;
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int v = __shfl_up(incl, d);
+        if (lane >= d) incl += v;
+    }
+    if (lane == 63) wsum[wave] = incl;
+    start[tid] = lo;
+    rows[tid] = n;
+    __syncthreads();
+    // overlapping offsets (not allowed) could name more tiles than the list
+    // holds; sums of up to 1024 counts of 2^24 / 16 tiles stay below 2^31
+    for (int w = 0; w < wave; w++) incl += wsum[w];
+    base[tid + 1] = incl;
+    if (tid == 0) base[0] = 0;
+    __syncthreads();
+    const int filled = min(base[1024], ntiles);
+    for (int i = tid; i < ntiles; i += 1024) {
+        ExpertTile t{};
+        t.filled = filled;
+        if (i < filled) {
+            int a = 0, b = 1024;                         // base[a] <= i < base[b]
+            while (b - a > 1) {
+                const int c = (a + b) / 2;
+                if (base[c] <= i) a = c;
+                else b = c;
+            }
+            t.expert = a;
+            t.first = base[a];
+            t.count = min(base[a + 1], ntiles) - base[a];
+            t.row0 = start[a] + (i - base[a]) * bm;
+            t.n = min(rows[a] - (i - base[a]) * bm, bm);
+        }
+        tiles[i] = t;
+    }
+}
+
+// tiles that R rows of E experts can need
+long long most_tiles(int R, int E, int bm)
+{
+    return (long long)R / bm + (E < R ? E : R);
+}
+
 // The kernel of a product, its row tiles and its launch's work items.
 struct Choice {
     bool tile;
-    int bm;
+    int kind, parts, bm;
     long long mt, items;
 };
 
-Choice choose(const MatmulArgs &p)
+// Up to 16 rows the stream kernel, up to 64 where it is estimated to be faster than the tile
+// kernel: 7 us and its weights at 4.2 TB/s, 1.2, 1.7 or 3 times for tiles of 16, 32
+// or 64 rows (whose products take the longer part).  us, stream and tile: 16 x 6144
+// x 12288 28 and 36, 64 x 6144 x 12288 64 and 37.
+Choice choose(const MatmulArgs &p, bool fits, bool direct)
 {
     Choice c{};
     const LinearArgs &a = p.a;
     const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
-    c.tile = rows > 64 && matmul_tile_fits(p);
+    c.parts = 1;
     c.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    if (c.tile) c.bm = 128;
-    c.mt = a.offsets ? max_tiles(a.R, a.E, c.bm) : (a.R + c.bm - 1) / c.bm;
-    c.items = c.tile ? matmul_tile_items(p, c.bm, c.mt) : matmul_stream_items(p, c.bm, c.mt);
+    if (fits && !a.offsets && rows > 16) {
+        const double tile = matmul_tile_kind(p, direct, c.kind, c.parts);
+        const double w = c.bm == 16 ? 1.2 : c.bm == 32 ? 1.7 : 3.0;
+        c.tile = rows > 64 || tile < 7.0 + w * a.O * (double)a.I / 4.2e6;
+    }
+    if (a.offsets && fits && a.R > 16) {
+        matmul_tile_kind(p, direct, c.kind, c.parts);
+        c.tile = true;
+    }
+    if (getenv("QG_TILE")) c.tile = atoi(getenv("QG_TILE"));
+    if (getenv("QG_KIND") && fits && direct && a.dtype == QGEMV_BF16) c.kind = atoi(getenv("QG_KIND"));
+    if (getenv("QG_PARTS") && !a.offsets) c.parts = atoi(getenv("QG_PARTS"));
+    if (c.tile) c.bm = matmul_tile_rows(c.kind);
+    else c.parts = 1;
+    c.mt = a.offsets ? most_tiles(a.R, a.E, c.bm) : (a.R + c.bm - 1) / c.bm;
+    c.items = c.tile ? matmul_tile_items(p, c.kind, c.parts, c.mt)
+                     : matmul_stream_items(p, c.bm, c.mt);
     return c;
 }
 
-hipError_t run(const MatmulArgs &p, const Choice &c, const RowTile *tiles, hipStream_t st)
+Choice choose(const MatmulArgs &p)
 {
-    return c.tile ? launch_matmul_tile(p, c.bm, tiles, (int)c.mt, st)
+    return choose(p, matmul_tile_fits(p), matmul_tile_direct(p));
+}
+
+hipError_t run(const MatmulArgs &p, const Choice &c, const ExpertTile *tiles, void *ws,
+               hipStream_t st)
+{
+    return c.tile ? launch_matmul_tile(p, c.kind, c.parts, tiles, (int)c.mt, ws, st)
                   : launch_matmul_stream(p, c.bm, tiles, (int)c.mt, st);
 }
 
 }  // namespace
 
-size_t matmul_workspace(int R, int E)
+size_t matmul_workspace(int S, int I, int O, int dtype, int gated)
 {
-    return align256((size_t)max_tiles(R, E, 16) * sizeof(RowTile));
+    MatmulArgs p{};
+    p.a.T = p.a.R = S;
+    p.a.E = 1;
+    p.a.I = I;
+    p.a.O = O;
+    p.a.ng = (I + 127) / 128;
+    p.a.dtype = dtype;
+    p.a.gated = gated;
+    size_t most = 0;
+    for (int direct = 0; direct < 2; direct++) {
+        const size_t n = matmul_part_bytes(p, choose(p, true, direct).parts);
+        most = n > most ? n : most;
+    }
+    return align256(most);
+}
+
+size_t matmul_grouped_workspace(int R, int E)
+{
+    return align256((size_t)most_tiles(R, E, 16) * sizeof(ExpertTile));
 }
 
 bool matmul_launchable(const MatmulArgs &p)
@@ -52,10 +156,12 @@ hipError_t launch_matmul(const MatmulArgs &args, void *ws, hipStream_t st)
     if (a.offsets) {
         const Choice c = choose(p);
         if (c.items > MAX_ITEMS) return hipErrorInvalidValue;
-        RowTile *const tiles = static_cast<RowTile *>(ws);
-        const hipError_t e = launch_plan_tiles(a.offsets, a.E, a.R, c.bm, tiles, (int)c.mt, st);
+        ExpertTile *const tiles = static_cast<ExpertTile *>(ws);
+        hipLaunchKernelGGL(plan_experts, dim3(1), dim3(1024), 0, st, a.offsets, a.E, a.R, c.bm,
+                           tiles, (int)c.mt);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        return run(p, c, tiles, st);
+        return run(p, c, tiles, nullptr, st);
     }
     // slices of rows whose work items fit a launch (64 rows of 2^24 outputs do)
     int slice = args.a.R;
@@ -71,9 +177,14 @@ hipError_t launch_matmul(const MatmulArgs &args, void *ws, hipStream_t st)
         a.y = static_cast<char *>(args.a.y) + (long long)(r * a.ldy * el);
         if (a.residual)
             a.residual = static_cast<const char *>(args.a.residual) + (long long)(r * a.ldr * el);
-        const Choice c = choose(p);
+        Choice c = choose(p);
+        // (the workspace is that of all rows together)
+        if (c.tile && slice < args.a.R) {
+            c.parts = 1;
+            c.items = matmul_tile_items(p, c.kind, 1, c.mt);
+        }
         if (c.items > MAX_ITEMS) return hipErrorInvalidValue;
-        const hipError_t e = run(p, c, nullptr, st);
+        const hipError_t e = run(p, c, nullptr, ws, st);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

@@ -68,7 +68,7 @@ struct Codes {
 // gained by them.
 template <typename XT, int MB, int NB, bool GATED>
 __global__ __launch_bounds__(SW * 64, 2) void matmul_stream(MatmulArgs p,
-                                                            const RowTile *__restrict__ tiles)
+                                                            const ExpertTile *__restrict__ tiles)
 {
     constexpr int YC = GATED ? NB * 8 : NB * 16;         // columns of y
     constexpr int LDR = NB * 16 + 4;
@@ -80,9 +80,9 @@ __global__ __launch_bounds__(SW * 64, 2) void matmul_stream(MatmulArgs p,
     const int oc = GATED ? a.O / 2 : a.O;
     const int ntn = (oc + YC - 1) / YC;
     const int o0 = (int)(blockIdx.x % ntn) * YC, mt = (int)(blockIdx.x / ntn);
-    RowTile t;
+    ExpertTile t;
     if (tiles) t = tiles[mt];
-    else t = RowTile{0, mt * (16 * MB), min(16 * MB, a.R - mt * (16 * MB)), 0};
+    else t = ExpertTile{0, mt * (16 * MB), min(16 * MB, a.R - mt * (16 * MB))};
     t.n = __builtin_amdgcn_readfirstlane(t.n);
     t.expert = __builtin_amdgcn_readfirstlane(t.expert);
     if (t.n <= 0) return;                                // uniform over the workgroup
@@ -214,7 +214,7 @@ int stream_blocks(const MatmulArgs &p, int bm)
 }
 
 template <typename XT, int MB, int NB>
-hipError_t run_stream(const MatmulArgs &p, const RowTile *tiles, unsigned grid, hipStream_t st)
+hipError_t run_stream(const MatmulArgs &p, const ExpertTile *tiles, unsigned grid, hipStream_t st)
 {
     if (p.a.gated)
         hipLaunchKernelGGL((matmul_stream<XT, MB, NB, true>), dim3(grid), dim3(SW * 64), 0, st, p,
@@ -238,7 +238,7 @@ long long matmul_stream_items(const MatmulArgs &p, int bm, long long ntm)
     return stream_grid(p, stream_blocks(p, bm), ntm) * (SW * 64);
 }
 
-hipError_t launch_matmul_stream(const MatmulArgs &p, int bm, const RowTile *tiles, int ntm,
+hipError_t launch_matmul_stream(const MatmulArgs &p, int bm, const ExpertTile *tiles, int ntm,
                                 hipStream_t st)
 {
     const int nb = stream_blocks(p, bm);

@@ -56,12 +56,6 @@ long long stream_items(WeightFormat fmt, const LinearArgs &a, int rows, int ntm)
 hipError_t launch_stream(WeightFormat fmt, const LinearArgs &a, int rows, const RowTile *tiles,
                          int ntm, hipStream_t st);
 
-// Row tiles of a grouped product (linear.hip): how many R rows of E experts can
-// need, and their list, made on the device from the experts' offsets.
-long long max_tiles(int R, int E, int bm);
-hipError_t launch_plan_tiles(const int32_t *offsets, int E, int R, int bm, RowTile *tiles,
-                             int ntiles, hipStream_t st);
-
 // A dimension of a launch holds fewer than 2^32 work items.
 constexpr long long MAX_ITEMS = 0xFFFFFFFFLL;
 

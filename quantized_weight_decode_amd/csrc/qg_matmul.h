@@ -15,22 +15,36 @@ struct MatmulArgs {
     long long ldxs;
 };
 
-size_t matmul_workspace(int R, int E);   // grouped only
+// One row tile of a grouped product: rows [row0, row0 + n) of y, of one expert,
+// whose `count` tiles start at tile `first` of the list.  The list is in the order
+// of the experts; its first `filled` tiles hold rows (n > 0).
+struct ExpertTile {
+    int expert, row0, n, first, count, filled, pad[2];
+};
+
+// Workspace bytes: of a dense product (a function of these sizes only), and of a
+// grouped one.
+size_t matmul_workspace(int S, int I, int O, int dtype, int gated);
+size_t matmul_grouped_workspace(int R, int E);
 bool matmul_launchable(const MatmulArgs &p);
 hipError_t launch_matmul(const MatmulArgs &p, void *ws, hipStream_t st);
 
 // The stream kernel (matmul_stream.hip): row tiles of 16, 32 or 64.
 long long matmul_stream_items(const MatmulArgs &p, int bm, long long ntm);
-hipError_t launch_matmul_stream(const MatmulArgs &p, int bm, const RowTile *tiles, int ntm,
+hipError_t launch_matmul_stream(const MatmulArgs &p, int bm, const ExpertTile *tiles, int ntm,
                                 hipStream_t st);
 
-// The tile kernel (matmul_tile.hip): row tiles of 128 or 256 (256: bfloat16, both
-// operands' rows on 16 bytes).
+// The tile kernel (matmul_tile.hip): whether it takes a product, and by
+// memory-to-LDS loads; the kind of its tiles, the parts of K and the time that they
+// are estimated to take (us); a tile's rows, and the bytes of the parts' sums.
 bool matmul_tile_fits(const MatmulArgs &p);
 bool matmul_tile_direct(const MatmulArgs &p);
-long long matmul_tile_items(const MatmulArgs &p, int bm, long long ntm);
-hipError_t launch_matmul_tile(const MatmulArgs &p, int bm, const RowTile *tiles, int ntm,
-                              hipStream_t st);
+double matmul_tile_kind(const MatmulArgs &p, bool direct, int &kind, int &parts);
+int matmul_tile_rows(int kind);
+size_t matmul_part_bytes(const MatmulArgs &p, int parts);
+long long matmul_tile_items(const MatmulArgs &p, int kind, int parts, long long ntm);
+hipError_t launch_matmul_tile(const MatmulArgs &p, int kind, int parts, const ExpertTile *tiles,
+                              int ntm, void *ws, hipStream_t st);
 
 hipError_t launch_fp8_quantize(const void *x, long long ldx, int S, int I, int dtype,
                                uint8_t *codes, long long ldc, float *scales, long long lds,

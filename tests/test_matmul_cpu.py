@@ -46,10 +46,11 @@ def test_quantize_refusals(q):
 
 def matmul(q, **k):
     a = dict(w=A, ws=2 * A, x=3 * A, ldx=200, xs=4 * A, lds=2, y=5 * A, ldy=8, S=3, I=200, O=8,
-             dtype=0, epi=None)
+             dtype=0, epi=None, wsp=7 * A, n=1 << 30)
     a.update(k)
     return q.qgemv_fp8b128_matmul(a["w"], a["ws"], a["x"], a["ldx"], a["xs"], a["lds"], a["y"],
-                                  a["ldy"], a["S"], a["I"], a["O"], a["dtype"], _epi(a["epi"]), 0)
+                                  a["ldy"], a["S"], a["I"], a["O"], a["dtype"], _epi(a["epi"]),
+                                  a["wsp"], a["n"], 0)
 
 
 def test_matmul_refusals(q):
@@ -71,8 +72,16 @@ def test_matmul_refusals(q):
         assert f(**{p: 5 * A + 16 - (16 if p in ("ws", "xs") else 3)}) == OVERLAP
     assert f(epi=E(0, 0, 5 * A + 8, None, 0)) == OVERLAP
     assert f(epi=E(0, 0, None, 5 * A + 8, 8)) == OVERLAP
-    assert f(S=0, w=0, ws=0, x=0, xs=0, y=0) == OK
+    assert f(S=0, w=0, ws=0, x=0, xs=0, y=0, wsp=0) == OK
     assert f(S=0, dtype=7) == ARG
+    # sizes that are cut along K need a workspace
+    big = dict(S=300, I=7168, ldx=7168, lds=56, O=7168, ldy=7168, dtype=1)
+    need = q.qgemv_matmul_workspace(300, 7168, 7168, 1, 0)
+    assert need > 0
+    assert f(wsp=0, **big) == WS and f(wsp=7 * A + 128, **big) == WS and f(n=need - 1, **big) == WS
+    assert f(wsp=5 * A, **big) == OVERLAP and f(wsp=A, **big) == OVERLAP
+    assert q.qgemv_matmul_workspace(0, 64, 64, 0, 0) == 0
+    assert q.qgemv_matmul_workspace(3, 64, 63, 0, 1) == 0
 
 
 def grouped(q, **k):
