@@ -1,6 +1,5 @@
 // matmul.hip -- products whose both operands are e4m3, dense or grouped by
 // expert: the choice among kernels, and slices of rows.
-#include <stdlib.h>
 #include "qg_launch.h"
 #include "qg_matmul.h"
 
@@ -76,29 +75,26 @@ struct Choice {
     long long mt, items;
 };
 
-// Up to 16 rows the stream kernel, up to 64 where it is estimated to be faster than the tile
-// kernel: 7 us and its weights at 4.2 TB/s, 1.2, 1.7 or 3 times for tiles of 16, 32
-// or 64 rows (whose products take the longer part).  us, stream and tile: 16 x 6144
-// x 12288 28 and 36, 64 x 6144 x 12288 64 and 37.
+// The tile kernel, or up to 64 rows the stream kernel where it is estimated to be
+// faster: 7 us and its weights at 5 TB/s, 1, 1.8 or 3.2 times for tiles of 16, 32 or
+// 64 rows (whose products take the longer part).  us, stream and tile: 5 x 16384 x
+// 7168 31.4 and 27.8, 5 x 4096 x 4096 13.7 and 26, 64 x 6144 x 12288 64 and 24.  (Up
+// to 16 rows of weights below 64 MB always, without estimating.)  Grouped by expert
+// the tile kernel from 17 rows on: 4 tokens of 8 of 256 experts, 7168 x 2048, 91 and
+// 81, 1 token 32 and 43.
 Choice choose(const MatmulArgs &p, bool fits, bool direct)
 {
     Choice c{};
     const LinearArgs &a = p.a;
     const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
+    const double bytes = a.O * (double)a.I;
     c.parts = 1;
     c.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    if (fits && !a.offsets && rows > 16) {
+    if (fits && (a.offsets ? a.R > 16 : rows > 16 || bytes > 64e6)) {
         const double tile = matmul_tile_kind(p, direct, c.kind, c.parts);
-        const double w = c.bm == 16 ? 1.2 : c.bm == 32 ? 1.7 : 3.0;
-        c.tile = rows > 64 || tile < 7.0 + w * a.O * (double)a.I / 4.2e6;
+        const double w = c.bm == 16 ? 1.0 : c.bm == 32 ? 1.8 : 3.2;
+        c.tile = a.offsets || rows > 64 || tile < 7.0 + w * bytes / 5e6;
     }
-    if (a.offsets && fits && a.R > 16) {
-        matmul_tile_kind(p, direct, c.kind, c.parts);
-        c.tile = true;
-    }
-    if (getenv("QG_TILE")) c.tile = atoi(getenv("QG_TILE"));
-    if (getenv("QG_KIND") && fits && direct && a.dtype == QGEMV_BF16) c.kind = atoi(getenv("QG_KIND"));
-    if (getenv("QG_PARTS") && !a.offsets) c.parts = atoi(getenv("QG_PARTS"));
     if (c.tile) c.bm = matmul_tile_rows(c.kind);
     else c.parts = 1;
     c.mt = a.offsets ? most_tiles(a.R, a.E, c.bm) : (a.R + c.bm - 1) / c.bm;

@@ -206,22 +206,27 @@ __global__ __launch_bounds__(SW * 64, 2) void matmul_stream(MatmulArgs p,
                   });
 }
 
-// Blocks of 16 rows of W per workgroup.
-int stream_blocks(const MatmulArgs &p, int bm)
+// Blocks of 16 rows of W per workgroup: one where two would leave a CU less than two
+// workgroups (gated: a gate and an up block at least).  us, 5 rows: 6144 x 12288 one
+// 22.2, two 25.1; 11008 x 4096 15.1 and 22.8; 16384 x 7168 34.4 and 31.4.
+int stream_blocks(const MatmulArgs &p, int bm, long long ntm)
 {
-    (void)bm;
-    return 2;
+    const long long wgs = ntm * ((p.a.O + 31) / 32);
+    return bm == 16 && !p.a.gated && wgs < 2 * cu_count() ? 1 : 2;
 }
 
 template <typename XT, int MB, int NB>
 hipError_t run_stream(const MatmulArgs &p, const ExpertTile *tiles, unsigned grid, hipStream_t st)
 {
-    if (p.a.gated)
-        hipLaunchKernelGGL((matmul_stream<XT, MB, NB, true>), dim3(grid), dim3(SW * 64), 0, st, p,
-                           tiles);
-    else
-        hipLaunchKernelGGL((matmul_stream<XT, MB, NB, false>), dim3(grid), dim3(SW * 64), 0, st, p,
-                           tiles);
+    if constexpr (NB > 1) {
+        if (p.a.gated) {
+            hipLaunchKernelGGL((matmul_stream<XT, MB, NB, true>), dim3(grid), dim3(SW * 64), 0, st,
+                               p, tiles);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((matmul_stream<XT, MB, NB, false>), dim3(grid), dim3(SW * 64), 0, st, p,
+                       tiles);
     return hipGetLastError();
 }
 
@@ -235,16 +240,17 @@ long long stream_grid(const MatmulArgs &p, int nb, long long ntm)
 
 long long matmul_stream_items(const MatmulArgs &p, int bm, long long ntm)
 {
-    return stream_grid(p, stream_blocks(p, bm), ntm) * (SW * 64);
+    return stream_grid(p, stream_blocks(p, bm, ntm), ntm) * (SW * 64);
 }
 
 hipError_t launch_matmul_stream(const MatmulArgs &p, int bm, const ExpertTile *tiles, int ntm,
                                 hipStream_t st)
 {
-    const int nb = stream_blocks(p, bm);
+    const int nb = stream_blocks(p, bm, ntm);
     const unsigned grid = (unsigned)stream_grid(p, nb, ntm);
 #define QG_STREAM(XT)                                                                       \
-    (bm == 16 ? run_stream<XT, 1, 2>(p, tiles, grid, st)                                    \
+    (bm == 16 ? nb == 1 ? run_stream<XT, 1, 1>(p, tiles, grid, st)                          \
+                        : run_stream<XT, 1, 2>(p, tiles, grid, st)                          \
      : bm == 32 ? run_stream<XT, 2, 2>(p, tiles, grid, st)                                  \
                 : run_stream<XT, 4, 2>(p, tiles, grid, st))
     return p.a.dtype == QGEMV_BF16 ? QG_STREAM(BF16) : QG_STREAM(F32);

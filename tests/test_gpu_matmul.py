@@ -80,6 +80,39 @@ def test_plain(q, S, I, O, dtype):
         assert rel_l2(y, ref) <= 2.0 ** -18
 
 
+# (S, I, O, gated) that reach each kind of tile, whole and ragged, and K in parts
+LARGE = [(2040, 384, 8192, False), (2040, 272, 8190, False), (2040, 256, 8192, True),
+         (2040, 400, 8180, True), (2100, 384, 8400, False), (2100, 384, 8200, True),
+         (1000, 384, 8200, False), (1000, 256, 7172, False), (1000, 256, 14336, True),
+         (300, 912, 2 * 392, True)]
+
+
+@pytest.mark.parametrize("S,I,O,gated", LARGE)
+def test_every_tile(q, S, I, O, gated):
+    check(q, S, I, O, torch.bfloat16, "silu" if gated else None, gated, bias=True, residual=True,
+          seed=S + O)
+    check(q, S, I, O, torch.bfloat16, None, gated, pad=16, seed=S + O + 1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S,I,O,gated", [(40, 16384, 264, False), (300, 7168, 520, False),
+                                         (257, 12048, 300, True), (70, 9001, 130, False),
+                                         (130, 9001, 132, True), (16, 12288, 7168, False)])
+def test_parts_of_k(q, S, I, O, gated, dtype):
+    """Products cut along K; the workspace is written up to its size only."""
+    need = q.qgemv_matmul_workspace(S, I, O, 1 if dtype == "bf16" else 0, int(gated))
+    assert need > 0 or S <= 64
+    check(q, S, I, O, DT[dtype], "gelu_tanh" if gated else None, gated, bias=True, residual=True,
+          seed=S)
+    w, s = weights((), O, I, S + 1)
+    c, cs = rows(S, I, S + 2)
+    ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    args = (cuda(w), cuda(s), cuda(c), cuda(cs))
+    y = q.fp8b128_matmul(*args, gated=gated, dtype=DT[dtype], workspace=ws[:need])
+    assert (ws[need:] == 0x5A).all()
+    assert torch.equal(y, q.fp8b128_matmul(*args, gated=gated, dtype=DT[dtype]))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("act", [None, "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("gated", [False, True])
@@ -213,7 +246,8 @@ def grouped_reference(w, s, c, cs, offsets, rowix, dtype, bias, act, gated):
 
 
 GROUPED = [(1, 1, 4, 128, 16), (4, 2, 8, 200, 48), (16, 4, 8, 384, 130), (70, 2, 5, 256, 270),
-           (300, 2, 4, 512, 300), (33, 8, 64, 640, 64), (600, 1, 3, 272, 528)]
+           (300, 2, 4, 512, 300), (33, 8, 64, 640, 64), (600, 1, 3, 272, 528),
+           (1100, 1, 2, 256, 528)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
