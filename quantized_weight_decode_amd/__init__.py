@@ -907,10 +907,14 @@ def fp8_quantize(x, out=None, scales=None):
     ng = -(-I // 128)
     if out is None:
         out = torch.empty((S, I), dtype=torch.uint8, device=x.device)
+        cp, ldc = out.data_ptr(), I
+    else:
+        cp, ldc = _rows(_codes(out, "out"), "out", torch.uint8, (S, I))
     if scales is None:
         scales = torch.empty((S, ng), dtype=torch.float32, device=x.device)
-    cp, ldc = _rows(_codes(out, "out"), "out", torch.uint8, (S, I))
-    sp, lds = _rows(scales, "scales", torch.float32, (S, ng))
+        sp, lds = scales.data_ptr(), ng
+    else:
+        sp, lds = _rows(scales, "scales", torch.float32, (S, ng))
     with _on(x.device):
         _call("qgemv_fp8_quantize", xp, ldx, S, I, code, cp, ldc, sp, lds, _raw_stream(x.device))
     return (out[0], scales[0]) if one else (out, scales)

@@ -161,21 +161,25 @@ hipError_t launch_matmul(const MatmulArgs &args, void *ws, hipStream_t st)
     }
     // slices of rows whose work items fit a launch (64 rows of 2^24 outputs do)
     int slice = args.a.R;
+    Choice c;
     for (;; slice = (slice / 2 + 63) / 64 * 64) {
         a.T = a.R = slice;
-        if (slice <= 64 || choose(p).items <= MAX_ITEMS) break;
+        c = choose(p);
+        if (slice <= 64 || c.items <= MAX_ITEMS) break;
     }
+    if (slice == args.a.R)
+        return c.items > MAX_ITEMS ? hipErrorInvalidValue : run(p, c, nullptr, ws, st);
     const size_t el = a.dtype == QGEMV_BF16 ? 2 : 4;
     for (int r = 0; r < args.a.R; r += slice) {
         a.T = a.R = args.a.R - r < slice ? args.a.R - r : slice;
         a.x = static_cast<const uint8_t *>(args.a.x) + r * a.ldx;
         p.xs = args.xs + r * p.ldxs;
         a.y = static_cast<char *>(args.a.y) + (long long)(r * a.ldy * el);
-        if (a.residual)
-            a.residual = static_cast<const char *>(args.a.residual) + (long long)(r * a.ldr * el);
-        Choice c = choose(p);
-        // (the workspace is that of all rows together)
-        if (c.tile && slice < args.a.R) {
+        if (args.a.residual)
+            a.residual =
+                static_cast<const char *>(args.a.residual) + (long long)(r * a.ldr * el);
+        c = choose(p);
+        if (c.parts > 1) {                               // (the workspace is that of all rows)
             c.parts = 1;
             c.items = matmul_tile_items(p, c.kind, 1, c.mt);
         }

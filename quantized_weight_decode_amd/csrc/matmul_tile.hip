@@ -65,8 +65,9 @@ size_t matmul_part_bytes(const MatmulArgs &p, int parts)
 }
 
 // The kind of tile, and of a dense product the parts of K, for which the busiest CU
-// ends first, one workgroup (of the square kind two) per CU at a time; joining
-// parts costs a launch and their sums' way to memory and back.  Grouped by expert
+// ends first, one workgroup (of the square kind two) per CU at a time; parts where
+// they find CUs without work, for joining them costs a launch and their sums' way to
+// memory and back (1501 x 16384 x 7168, 168 tiles: 236 us, in three parts 259).  Grouped by expert
 // 128 x 256, whose three stages suit experts of few rows, bound by their weights'
 // bytes, up to 512 rows per expert.
 double matmul_tile_kind(const MatmulArgs &p, bool direct, int &kind, int &parts)
@@ -88,8 +89,9 @@ double matmul_tile_kind(const MatmulArgs &p, bool direct, int &kind, int &parts)
         const double c = a.dtype == QGEMV_F32 ? 2 * k.step : k.step;
         for (const int f : {1, 2, 3, 4, 6, 8, 12, 16}) {
             const int per = ((a.ng + f - 1) / f + SG - 1) / SG * SG, n = (a.ng + per - 1) / per;
-            if (n != f || (f > 1 && a.R > 4096)) continue;
             const long long slots = i == SQUARE ? 2 * ncu : ncu;
+            if (f > 1 && (tiles * f > slots || a.R > 4096)) break;
+            if (n != f) continue;
             double us = (double)((tiles * f + slots - 1) / slots) * (per * c + k.fixed);
             if (f > 1) us += 5.0 + 8e-6 * f * a.R * (double)a.O / 5.0;
             if (least < 0.0 || us < least) {

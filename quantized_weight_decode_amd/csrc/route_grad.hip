@@ -35,12 +35,25 @@ struct Piece {
                 if (j < left) p[j] = v[j];
         }
     }
+    // past the caches
+    __device__ __forceinline__ void store_past(raw *p, int left) const
+    {
+        if (left >= VEC) {
+            __builtin_nontemporal_store(v, reinterpret_cast<vec *>(p));
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; j++)
+                if (j < left) p[j] = v[j];
+        }
+    }
 };
 
 // ---------------------------------------------------------------------------
-// y[r] = x[tokens[r]].  A wave has one row, so its index is scalar; rows of
-// index -1 are left as they were.  Bound by HBM: R rows written, T read (each
-// token's row again for every expert of it, from the caches).
+// y[r] = x[tokens[r]].  A wave has one row, so its index is scalar; rows of index
+// -1 are left as they were.  Bound by HBM: R rows written, T read (each token's
+// row again for every expert of it, from the caches, which the stores therefore
+// pass by: 4096 tokens of 8, 7168 bf16, 150 us with ordinary stores and a piece per
+// thread).  A thread has four pieces of the row in flight.
 // ---------------------------------------------------------------------------
 template <typename XT, int VEC>
 __global__ __launch_bounds__(256) void dispatch(const typename XT::raw *__restrict__ x,
@@ -49,20 +62,25 @@ __global__ __launch_bounds__(256) void dispatch(const typename XT::raw *__restri
                                                 typename XT::raw *__restrict__ y, long long ldy,
                                                 int ncb)
 {
+    constexpr int U = 4;
     const int rb = (int)(blockIdx.x / ncb), cb = (int)(blockIdx.x % ncb);
     const int r = __builtin_amdgcn_readfirstlane(rb * (int)blockDim.y + (int)threadIdx.y);
-    const int c = (cb * (int)blockDim.x + (int)threadIdx.x) * VEC;
-    if (r >= R || c >= I) return;
+    const int step = (int)blockDim.x * VEC, c = cb * U * step + (int)threadIdx.x * VEC;
+    if (r >= R) return;
     const int t = tokens[r];
     if (t == -1) return;
-    Piece<XT, VEC> p;
-    if (t < 0 || t >= T) {
+    const bool bad = t < 0 || t >= T;
+    Piece<XT, VEC> p[U];
 #pragma unroll
-        for (int j = 0; j < VEC; j++) p.v[j] = XT::put(__builtin_nanf(""));
-    } else {
-        p.load(x + (long long)t * ldx + c, I - c);
+    for (int i = 0; i < U; i++)
+        p[i].load(x + (long long)(bad ? 0 : t) * ldx + c + i * step, bad ? 0 : I - c - i * step);
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+        if (bad)
+#pragma unroll
+            for (int j = 0; j < VEC; j++) p[i].v[j] = XT::put(__builtin_nanf(""));
+        p[i].store_past(y + (long long)r * ldy + c + i * step, I - c - i * step);
     }
-    p.store(y + (long long)r * ldy + c, I - c);
 }
 
 // ---------------------------------------------------------------------------
@@ -183,14 +201,15 @@ __global__ __launch_bounds__(256) void combine_grad(
     }
 }
 
-// Threads across a row of nch pieces, rows per workgroup, workgroups per row.
+// Threads across a row of nch pieces, `each` of them per thread, rows per workgroup,
+// workgroups per row.
 struct Shape {
     int bx, by, ncb;
 };
-Shape shape_of(int nch)
+Shape shape_of(int nch, int each = 1)
 {
-    const int bx = nch > 192 ? 256 : nch > 64 ? 128 : 64;
-    return {bx, 256 / bx, (nch + bx - 1) / bx};
+    const int bx = nch > 192 * each ? 256 : nch > 64 * each ? 128 : 64;
+    return {bx, 256 / bx, (nch + bx * each - 1) / (bx * each)};
 }
 
 // Slices of n rows whose launches of `items` work items per row hold fewer than
@@ -214,7 +233,7 @@ hipError_t run_dispatch(const void *x, long long ldx, int T, const int32_t *toke
                         void *y, long long ldy, hipStream_t st)
 {
     typedef typename XT::raw raw;
-    const Shape s = shape_of((I + VEC - 1) / VEC);
+    const Shape s = shape_of((I + VEC - 1) / VEC, 4);
     return sliced(R, (long long)s.bx * s.ncb, s.by, [&](long long r, int n) {
         hipLaunchKernelGGL((dispatch<XT, VEC>), dim3((unsigned)((n + s.by - 1) / s.by * s.ncb)),
                            dim3(s.bx, s.by), 0, st, static_cast<const raw *>(x), ldx, T,
