@@ -7,9 +7,11 @@ a sum of total magnitude m is off by at most (I + 16) 2^-24 m.
 
 The e4m3 matrix instructions, which many rows of a bfloat16 product take, add a
 rounding of their own: of eight consecutive columns' products each is cut to a
-multiple of 2^(e - 13), e the largest exponent among them (a product's exponent
-being the sum of its factors').  The largest product is at least 2^e and, with its
-8 bits, not touched; the other seven lose less than 2^-13 of it each.
+multiple of 2^(e - 13), e the largest exponent among them, a product's exponent
+being the sum of its codes' (-6 for subnormal codes and zero).  So each loses less
+than 2^-13 of (largest |x|, or 2^-6) times (largest |w|, or 2^-6) of the eight, in
+codes; the largest itself keeps its 8 bits.  The codes of the tests' blocks reach 1
+at least, so 2^-6 of a block's largest value stands for 2^-6 times its scale.
 """
 import numpy as np
 import torch
@@ -53,16 +55,22 @@ def rows(S, I, seed, outliers=True):
 
 
 def quantize(x):
-    """The definition on the CPU: f32 scales and quotients, e4m3 to nearest even
-    (by the type's own conversion, which is exact at these magnitudes)."""
+    """The definition: f32 scales, and the e4m3 values nearest to the exact quotients
+    448 x / max|x|.  In 64 bits 448 x is exact, and the division's rounding cannot
+    reach the middle of two codes, from which any other quotient of f32 numbers is
+    2^-32 away at least; dividing by a power of two and rint are exact."""
     x = x.float()
     S, I = x.shape
     n = -(-I // 128)
     wide = torch.zeros(S, n * 128)
     wide[:, :I] = x
     b = wide.reshape(S, n, 128)
-    s = (b.abs().amax(2) / 448.0).clamp_min(2.0 ** -126)
-    q = (b / s[:, :, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    m = b.abs().amax(2)
+    s = (m / 448.0).clamp_min(2.0 ** -126)
+    q = b.double() * 448.0 / m.double().clamp_min(448.0 * 2.0 ** -126)[:, :, None]
+    step = torch.exp2(torch.frexp(q)[1].clamp_min(-5).double() - 4)
+    q = torch.where(torch.isfinite(q), torch.round(q / step) * step, q)
+    q = q.float().to(torch.float8_e4m3fn).view(torch.uint8)
     bad = ~torch.isfinite(b).all(2)             # an infinity or NaN in the block
     s[bad] = float("nan")
     q[bad] = 0x7F
@@ -71,17 +79,17 @@ def quantize(x):
 
 def sum_bound(W, x, dtype):
     """How far the sums x W^T of a product with results of this type may be off
-    (torch f64).  The largest product of eight columns is at most the product of
-    their largest factors, and at most the sum of the eight."""
+    (torch f64)."""
     W = torch.from_numpy(np.ascontiguousarray(W))
-    mag = x.abs() @ W.abs().t()
-    bound = (W.shape[1] + 16) * U * mag
+    bound = (W.shape[1] + 16) * U * (x.abs() @ W.abs().t())
     if dtype == torch.bfloat16:
         def largest(t):
-            wide = torch.zeros(t.shape[0], -(-t.shape[1] // 8) * 8, dtype=t.dtype)
+            n = t.shape[0], -(-t.shape[1] // 128)
+            wide = torch.zeros(n[0], n[1] * 128, dtype=t.dtype)
             wide[:, :t.shape[1]] = t.abs()
-            return wide.reshape(t.shape[0], wide.shape[1] // 8, 8).amax(2)
-        bound = bound + 7 * 2.0 ** -13 * torch.minimum(mag, largest(x) @ largest(W).t())
+            block = wide.reshape(*n, 128).amax(2) * 2.0 ** -6
+            return torch.maximum(wide.reshape(*n, 16, 8).amax(3), block[:, :, None]).flatten(1)
+        bound = bound + 7 * 2.0 ** -13 * largest(x) @ largest(W).t()
     return bound
 
 

@@ -152,6 +152,32 @@ def test_every_code(q):
             assert torch.equal(y.cpu(), (v[:S, None] * v[None, :]).bfloat16())
 
 
+@pytest.mark.parametrize("S", [3, 90, 260])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_codes_of_every_size_together(q, S, dtype):
+    """Subnormal codes, zeros and the largest ones side by side, in both operands."""
+    I, O = 640, 260
+    w, s = weights((), O, I, 40)
+    r = np.random.default_rng(41)
+    c = weights((), S, I, 42)[0]
+    small = (r.integers(0, 8, (S, I)) | r.integers(0, 2, (S, I)) << 7).astype(np.uint8)
+    c = np.where(r.random((S, I)) < 0.5, small, c)
+    w = np.where(r.random((O, I)) < 0.3, r.integers(0, 8, (O, I)).astype(np.uint8), w)
+    c[:, ::128] = w[:, ::128] = 0x38                 # 1 in every block
+    cs = np.exp(r.uniform(-3, 3, (S, 5))).astype(np.float32)
+    ref, bound = reference(decode_weights(w, s), decode_rows(c, cs), DT[dtype])
+    y = q.fp8b128_matmul(cuda(w), cuda(s), cuda(c), cuda(cs), dtype=DT[dtype])
+    assert_within(y, ref, bound)
+    # groups of eight where only subnormal codes meet large ones
+    c[:, 8:] = 1
+    w[:, 8:] = 0x7E
+    w[:, 9::8] = 0x01
+    c[:, ::128] = w[:, ::128] = 0x38
+    ref, bound = reference(decode_weights(w, s), decode_rows(c, cs), DT[dtype])
+    y = q.fp8b128_matmul(cuda(w), cuda(s), cuda(c), cuda(cs), dtype=DT[dtype])
+    assert_within(y, ref, bound)
+
+
 @pytest.mark.parametrize("S", [2, 60, 260])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_nan_stays_in_its_row_and_column(q, S, dtype):
@@ -349,3 +375,32 @@ def test_two_calls_at_once_and_replays(q):
             assert torch.equal(u, v)
         for u, v in zip(eager, alone[3]):
             assert torch.equal(u, v)
+
+
+def test_weights_and_rows_beyond_4_gb(q):
+    """Offsets that pass 32 bits: the last rows of W, and the last rows of x through
+    an index, against the same rows alone."""
+    I, O = 65536, 65664                                  # 4.3 GB of codes
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(50)
+    w = torch.randint(0, 126, (O, I), dtype=torch.uint8, generator=g, device="cuda")
+    s = torch.rand((O // 128, I // 128), generator=g, device="cuda") * 1e-3
+    x, xs = q.fp8_quantize(torch.randn((70, I), generator=g, device="cuda"))
+    last = slice(O - 256, O)
+    xd = decode_rows(x, xs)
+    ref, bound = reference(decode_weights(w[last].cpu().numpy(), s[-2:].cpu().numpy()), xd,
+                           torch.bfloat16)
+    for S in (3, 70):
+        y = q.fp8b128_matmul(w, s, x[:S], xs[:S])
+        assert_within(y[:, last], ref[:S], bound[:S], f"{S} rows")
+    # W's rows as activations: T rows of x of 4.3 GB, read through an index
+    ws = torch.rand((O, I // 128), generator=g, device="cuda")
+    pick = torch.tensor([O - 1, 5, O - 3, 65535, 32768] * 8, dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    wx, sx = x[:64].contiguous(), torch.rand((1, I // 128), generator=g, device="cuda") * 1e-3
+    y = q.fp8b128_matmul_grouped(wx[None], sx[None], w, ws, offsets, rows=pick)
+    ref, bound = reference(decode_weights(wx.cpu().numpy(), sx.cpu().numpy()),
+                           decode_rows(w[pick.long()], ws[pick.long()]), torch.bfloat16)
+    assert_within(y, ref, bound)

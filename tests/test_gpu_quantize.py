@@ -55,6 +55,26 @@ def test_borders(q, dtype):
         same(q.fp8_quantize(xe.cuda()), quantize(xe))
 
 
+def test_quotients_next_to_the_middle_of_two_codes(q):
+    """x as near to middle * max / 448 as f32 gets, and its neighbours: an f32 quotient
+    of an f32 scale would put some of them on the wrong side."""
+    r = np.random.default_rng(7)
+    v = np.unique(np.abs(torch.from_numpy(FINITE).view(torch.float8_e4m3fn).double().numpy()))
+    mid = np.resize((v[1:] + v[:-1]) / 2, 127)
+    top = (r.uniform(1, 2, (600, 1)) * np.exp2(r.integers(-60, 60, (600, 1)))).astype(np.float32)
+    x = (mid * top.astype(np.float64) / 448).astype(np.float32)
+    for k in (0, -1, 1):
+        near = x if k == 0 else np.nextafter(x, np.float32(k) * np.inf, dtype=np.float32)
+        t = torch.from_numpy(np.concatenate([top, near * np.where(r.random(near.shape) < 0.5, -1, 1)
+                                             .astype(np.float32)], 1))
+        same(q.fp8_quantize(t.cuda()), quantize(t))
+    # bfloat16, whose quotients hit middles exactly: 0.75 of the largest and its like
+    top = torch.from_numpy(r.uniform(1, 2, (2000, 1))).bfloat16()
+    t = torch.cat([top, (top.float() * torch.from_numpy(np.resize(mid, (1, 127))).float() / 448)
+                   .bfloat16()], 1)
+    same(q.fp8_quantize(t.cuda()), quantize(t))
+
+
 def test_smallest_and_largest(q):
     rows = [np.zeros(256), np.full(256, 2.0 ** -149), np.full(256, -2.0 ** -126),
             np.linspace(-1, 1, 256) * 2.0 ** -118, np.linspace(-1, 1, 256) * 2.0 ** -117.3,
