@@ -147,25 +147,33 @@ __global__ __launch_bounds__(256) void combine_grad(
     __shared__ float part[4][KB];
     const int t = (int)(blockIdx.x / nkb), k0 = (int)(blockIdx.x % nkb) * KB;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // lane k has slot k of the token (K <= 64): its row, whether that is the token's
+    // own, its gate
     const int32_t *const pt = pos + (long long)t * K;
-    const float *const gt = gates + (long long)t * K;
+    const int pk = lane < K ? pt[lane] : -1;
+    const bool range = pk >= 0 && pk < R;
+    const float gk = lane < K ? gates[(long long)t * K + lane] : 0.0f;
+    const bool mine = range && tokens[pk] == first + t;
+    const unsigned long long valid = __ballot(range), owned = __ballot(mine);
     int r[KB];
     bool in[KB], own[KB];
     float g[KB], dot[KB];
 #pragma unroll
     for (int i = 0; i < KB; i++) {
-        const int p = k0 + i < K ? pt[k0 + i] : -1;
-        in[i] = p >= 0 && p < R;
-        r[i] = in[i] ? p : 0;
-        own[i] = in[i] && tokens[r[i]] == first + t;
+        const int k = k0 + i < K ? k0 + i : 0;
+        in[i] = k0 + i < K && (valid >> k & 1);
+        own[i] = in[i] && (owned >> k & 1);
+        r[i] = in[i] ? __builtin_amdgcn_readlane(pk, k) : 0;
         dot[i] = 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < KB; i++) {
         // a row that several of the token's slots name has all their gates
         g[i] = 0.0f;
-        if (own[i])
-            for (int k = 0; k < K; k++) g[i] += pt[k] == r[i] ? gt[k] : 0.0f;
+        unsigned long long same = __ballot(lane < K && pk == r[i]);
+        while (same) {                                   // uniform over the wave
+            const int at = __builtin_ctzll(same);
+            g[i] += __builtin_bit_cast(
+                float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, gk), at));
+            same &= same - 1;
+        }
     }
     const typename XT::raw *const dyt = dy + (long long)t * lddy;
     for (int c = tid * VEC; c < O; c += 256 * VEC) {
@@ -194,8 +202,7 @@ __global__ __launch_bounds__(256) void combine_grad(
     }
     __syncthreads();
     if (tid < KB && k0 + tid < K) {
-        const int p = pt[k0 + tid];
-        const bool ok = p >= 0 && p < R && tokens[p] == first + t;
+        const bool ok = owned >> (k0 + tid) & 1;
         const float sum = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
         dgates[(long long)t * K + k0 + tid] = ok ? sum : __builtin_nanf("");
     }
@@ -293,9 +300,16 @@ hipError_t launch_moe_combine_grad(const void *dy, long long lddy, const void *h
     const bool wide = aligned16((uintptr_t)dy | (uintptr_t)h | (uintptr_t)dh |
                                 (uintptr_t)(lddy * el) | (uintptr_t)(ldh * el) |
                                 (uintptr_t)(lddh * el));
-    constexpr int KB = 8;
-    const int nkb = (K + KB - 1) / KB;
+    // eight slots per workgroup, two where eight would leave CUs without work (33
+    // tokens of 8, 2048 f32: 12.7 us in eights)
+    const bool few = (long long)T * ((K + 7) / 8) < 256;
+    const int nkb = few ? (K + 1) / 2 : (K + 7) / 8;
 #define QG_GRAD(XT, VEC)                                                                    \
+    do {                                                                                    \
+        if (few) QG_GRAD1(XT, VEC, 2);                                                      \
+        else QG_GRAD1(XT, VEC, 8);                                                          \
+    } while (0)
+#define QG_GRAD1(XT, VEC, KB)                                                               \
     hipLaunchKernelGGL((combine_grad<XT, VEC, KB>), dim3((unsigned)(n * nkb)), dim3(256), 0, st, \
                        static_cast<const XT::raw *>(dy) + t * lddy, lddy,                   \
                        static_cast<const XT::raw *>(h), ldh, R, tokens, pos + t * K,        \
@@ -311,6 +325,7 @@ hipError_t launch_moe_combine_grad(const void *dy, long long lddy, const void *h
         }
     });
 #undef QG_GRAD
+#undef QG_GRAD1
 }
 
 }  // namespace qg
