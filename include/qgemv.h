@@ -439,7 +439,8 @@ int qgemv_fp8_quantize(const void *x, long long ldx, int S, int I, int dtype, vo
  * formed on the e4m3 matrix cores, which cut each product to a multiple of 2^(e - 13)
  * before they sum eight consecutive columns' to f32: e is the largest of the eight
  * products' exponents, a product's being the sum of its codes' (-6 for subnormal
- * codes and zero).  That is below 2^-8 of the step to which e4m3 has rounded x.
+ * codes and zero).  That is at most 2^-9 of what rounding one of its factors to e4m3
+ * may have moved the product with that exponent.
  * The transpose of W's codes with the transpose of its scales is W^T in the same
  * format, so the gradient of x is the same call on those and on the quantized
  * gradient of y.

@@ -9,10 +9,13 @@ Two layers:
   (ints), sizes and a stream handle, returning the status code;
 * ``i4g``, ``fp8b128``, ``mq4v2``, ``fwht256``, ``moe_topk``, ``dequant_*``,
   ``i4g_linear``, ``fp8b128_linear``, ``moe_group``, ``i4g_grouped``,
-  ``moe_combine`` -- take torch tensors on the current CUDA (HIP) device, allocate the output
+  ``moe_combine``, ``fp8_quantize``, ``fp8b128_matmul``,
+  ``fp8b128_matmul_grouped``, ``moe_dispatch`` and the gradients
+  ``moe_dispatch_grad``, ``moe_combine_grad`` -- take torch tensors on the current CUDA (HIP) device, allocate the output
   with ``torch.empty``, launch on ``torch.cuda.current_stream()`` and raise
-  ``QgemvError`` on a refusal.  No call records a gradient; the products with
-  an epilogue and ``moe_combine`` refuse arguments that ask for one.
+  ``QgemvError`` on a refusal.  No call records a gradient (the gradients are
+  calls of their own); the products with an epilogue and of 8-bit operands,
+  ``moe_combine`` and what belongs to it refuse arguments that ask for one.
 """
 from __future__ import annotations
 
