@@ -71,7 +71,8 @@ long long most_tiles(int R, int E, int bm)
 // The kernel of a product, its row tiles and its launch's work items.
 struct Choice {
     bool tile;
-    int kind, parts, bm;
+    TilePlan plan;
+    int bm;
     long long mt, items;
 };
 
@@ -88,17 +89,16 @@ Choice choose(const MatmulArgs &p, bool fits, bool direct)
     const LinearArgs &a = p.a;
     const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
     const double bytes = a.O * (double)a.I;
-    c.parts = 1;
     c.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     if (fits && (a.offsets ? a.R > 16 : rows > 16 || bytes > 64e6)) {
-        const double tile = matmul_tile_kind(p, direct, c.kind, c.parts);
+        c.plan = matmul_tile_plan(p, direct);
         const double w = c.bm == 16 ? 1.0 : c.bm == 32 ? 1.8 : 3.2;
-        c.tile = a.offsets || rows > 64 || tile < 7.0 + w * bytes / 5e6;
+        c.tile = a.offsets || rows > 64 || c.plan.us < 7.0 + w * bytes / 5e6;
     }
-    if (c.tile) c.bm = matmul_tile_rows(c.kind);
-    else c.parts = 1;
+    if (c.tile) c.bm = matmul_tile_rows(c.plan.kind);
+    else c.plan.parts = 1;
     c.mt = a.offsets ? most_tiles(a.R, a.E, c.bm) : (a.R + c.bm - 1) / c.bm;
-    c.items = c.tile ? matmul_tile_items(p, c.kind, c.parts, c.mt)
+    c.items = c.tile ? matmul_tile_items(p, c.plan, c.mt)
                      : matmul_stream_items(p, c.bm, c.mt);
     return c;
 }
@@ -111,7 +111,7 @@ Choice choose(const MatmulArgs &p)
 hipError_t run(const MatmulArgs &p, const Choice &c, const ExpertTile *tiles, void *ws,
                hipStream_t st)
 {
-    return c.tile ? launch_matmul_tile(p, c.kind, c.parts, tiles, (int)c.mt, ws, st)
+    return c.tile ? launch_matmul_tile(p, c.plan, tiles, (int)c.mt, ws, st)
                   : launch_matmul_stream(p, c.bm, tiles, (int)c.mt, st);
 }
 
@@ -129,7 +129,7 @@ size_t matmul_workspace(int S, int I, int O, int dtype, int gated)
     p.a.gated = gated;
     size_t most = 0;
     for (int direct = 0; direct < 2; direct++) {
-        const size_t n = matmul_part_bytes(p, choose(p, true, direct).parts);
+        const size_t n = matmul_part_bytes(p, choose(p, true, direct).plan.parts);
         most = n > most ? n : most;
     }
     return align256(most);
@@ -179,9 +179,9 @@ hipError_t launch_matmul(const MatmulArgs &args, void *ws, hipStream_t st)
             a.residual =
                 static_cast<const char *>(args.a.residual) + (long long)(r * a.ldr * el);
         c = choose(p);
-        if (c.parts > 1) {                               // (the workspace is that of all rows)
-            c.parts = 1;
-            c.items = matmul_tile_items(p, c.kind, 1, c.mt);
+        if (c.plan.parts > 1) {                          // (the workspace is that of all rows)
+            c.plan.parts = 1;
+            c.items = matmul_tile_items(p, c.plan, c.mt);
         }
         if (c.items > MAX_ITEMS) return hipErrorInvalidValue;
         const hipError_t e = run(p, c, nullptr, ws, st);

@@ -15,7 +15,7 @@ namespace qg {
 struct TileParams {
     MatmulArgs m;
     const ExpertTile *tiles;             // grouped, else nullptr
-    int ntm, ntn;
+    int ntm, ntn, col0;                  // tiles of the launch; its first column of y
     int parts, per;                      // parts of K, of `per` steps (dense)
     float *partial;                      // their sums [parts][halves of W][R][ldp], parts > 1
     int ldp;
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(WW * WT * 64, WW * WT <= 4 ? 2 : 2) void matmul_til
     // repeat one that exists, a bad row index reads row 0 and is marked in the end.
     const int row_l = tid >> 3;
     const uint32_t ch = ((tid & 7) ^ swizzle(row_l)) * 16;
-    const int c0 = nt * YC;
+    const int c0 = p.col0 + nt * YC;
     const int first_step = RAGGED ? 0 : part * p.per;
     const uint8_t *const wexp =
         a.w + (long long)t.expert * a.w_stride + (long long)first_step * TK;

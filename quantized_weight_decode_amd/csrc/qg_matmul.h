@@ -34,16 +34,23 @@ long long matmul_stream_items(const MatmulArgs &p, int bm, long long ntm);
 hipError_t launch_matmul_stream(const MatmulArgs &p, int bm, const ExpertTile *tiles, int ntm,
                                 hipStream_t st);
 
+// How the tile kernel takes a product: tiles of `kind`, K in `parts` (dense); the
+// first `head` columns of y, if any, by a launch of their own, of `head_kind`.
+struct TilePlan {
+    int kind, parts, head, head_kind;
+    double us;                           // estimated (dense)
+};
+
 // The tile kernel (matmul_tile.hip): whether it takes a product, and by
-// memory-to-LDS loads; the kind of its tiles, the parts of K and the time that they
-// are estimated to take (us); a tile's rows, and the bytes of the parts' sums.
+// memory-to-LDS loads; its plan; the rows of a kind's tiles, the bytes of the parts'
+// sums, the work items of the larger launch.
 bool matmul_tile_fits(const MatmulArgs &p);
 bool matmul_tile_direct(const MatmulArgs &p);
-double matmul_tile_kind(const MatmulArgs &p, bool direct, int &kind, int &parts);
+TilePlan matmul_tile_plan(const MatmulArgs &p, bool direct);
 int matmul_tile_rows(int kind);
 size_t matmul_part_bytes(const MatmulArgs &p, int parts);
-long long matmul_tile_items(const MatmulArgs &p, int kind, int parts, long long ntm);
-hipError_t launch_matmul_tile(const MatmulArgs &p, int kind, int parts, const ExpertTile *tiles,
+long long matmul_tile_items(const MatmulArgs &p, const TilePlan &plan, long long ntm);
+hipError_t launch_matmul_tile(const MatmulArgs &p, const TilePlan &plan, const ExpertTile *tiles,
                               int ntm, void *ws, hipStream_t st);
 
 hipError_t launch_fp8_quantize(const void *x, long long ldx, int S, int I, int dtype,

@@ -94,6 +94,13 @@ def test_every_tile(q, S, I, O, gated):
     check(q, S, I, O, torch.bfloat16, None, gated, pad=16, seed=S + O + 1)
 
 
+@pytest.mark.parametrize("S,I,O,gated", [(2040, 2048, 12290, False), (2040, 2048, 12288, True)])
+def test_two_launches(q, S, I, O, gated):
+    """More tiles than one round of the CUs: the last columns by a launch of their own."""
+    check(q, S, I, O, torch.bfloat16, "relu" if gated else None, gated, bias=True, residual=True,
+          seed=O)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("S,I,O,gated", [(40, 16384, 264, False), (300, 7168, 520, False),
                                          (257, 12048, 300, True), (70, 9001, 130, False),
