@@ -11,16 +11,18 @@ Two layers:
   ``i4g_linear``, ``fp8b128_linear``, ``moe_group``, ``i4g_grouped``,
   ``moe_combine``, ``fp8_quantize``, ``fp8b128_matmul``,
   ``fp8b128_matmul_grouped``, ``moe_dispatch`` and the gradients
-  ``moe_dispatch_grad``, ``moe_combine_grad`` -- take torch tensors on the current CUDA (HIP) device, allocate the output
-  with ``torch.empty``, launch on ``torch.cuda.current_stream()`` and raise
-  ``QgemvError`` on a refusal.  No call records a gradient (the gradients are
-  calls of their own); the products with an epilogue and of 8-bit operands,
-  ``moe_combine`` and what belongs to it refuse arguments that ask for one.
+  ``moe_dispatch_grad``, ``moe_combine_grad`` -- take torch tensors on the
+  current CUDA (HIP) device, allocate the output with ``torch.empty``, launch on
+  ``torch.cuda.current_stream()`` and raise ``QgemvError`` on a refusal.  No call
+  records a gradient (the gradients are calls of their own); the products with
+  an epilogue and of 8-bit operands, ``moe_combine`` and what belongs to it
+  refuse arguments that ask for one.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import functools
 import operator
 import os
 
@@ -936,6 +938,12 @@ def _result_type(dtype, *ts):
     raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
 
 
+@functools.lru_cache(maxsize=1024)
+def _matmul_need(S, I, O, code, gated, device):
+    """Bytes of scratch of a product on the current device (by its index)."""
+    return qgemv_matmul_workspace(S, I, O, code, gated)
+
+
 def _result(out, R, oc, dtype, device):
     if out is None:
         out = _torch().empty((R, oc), dtype=dtype, device=device)
@@ -984,7 +992,7 @@ def fp8b128_matmul(w, scale_inv, x, x_scale, bias=None, act=None, gated=False, r
     wp, sp = _dev(w, "w", torch.uint8), _dev(scale_inv, "scale_inv", torch.float32)
     with _on(x.device):
         ws, wsp, nbytes = _scratch(
-            workspace, qgemv_matmul_workspace(S, I, O, code, int(bool(gated))), x.device)
+            workspace, _matmul_need(S, I, O, code, int(bool(gated)), x.device.index), x.device)
         _call("qgemv_fp8b128_matmul", wp, sp, xp, ldx, xsp, lds, yp, ldy, S, I, O, code, _ref(epi),
               wsp, nbytes, _raw_stream(x.device))
     return y[0] if one else y
@@ -1028,9 +1036,9 @@ def fp8b128_matmul_grouped(w, scale_inv, x, x_scale, offsets, rows=None, bias=No
     rp = _dev(rows, "rows", torch.int32) if rows is not None else None
     with _on(x.device):
         ws, wsp, nbytes = _scratch(workspace, qgemv_matmul_grouped_workspace(R, E), x.device)
-        _call("qgemv_fp8b128_matmul_grouped", wp, sp, O * I, scale_inv.shape[1] * scale_inv.shape[2], E, op,
-              rp, xp, ldx, xsp, lds, T, yp, ldy, R, I, O, code, _ref(epi), wsp, nbytes,
-              _raw_stream(x.device))
+        _call("qgemv_fp8b128_matmul_grouped", wp, sp, O * I,
+              scale_inv.shape[1] * scale_inv.shape[2], E, op, rp, xp, ldx, xsp, lds, T, yp, ldy, R,
+              I, O, code, _ref(epi), wsp, nbytes, _raw_stream(x.device))
     return y
 
 

@@ -92,7 +92,7 @@ __global__ __launch_bounds__(SW * 64, 2) void matmul_stream(MatmulArgs p,
     // reads row 0 and is marked in the epilogue.
     const uint8_t *xrow[MB], *wrow[NB];
     const float *xsrow[MB], *wsrow[NB];
-    int second[NB];                      // of the lane's four rows of W, the first of the next block
+    int second[NB];                      // of the lane's rows of W, the first of the next block
 #pragma unroll
     for (int m = 0; m < MB; m++) {
         long long r = t.row0 + (m * 16 + li < t.n ? m * 16 + li : 0);

@@ -167,12 +167,14 @@ __device__ __forceinline__ void finish_rows(const LinearArgs &a, int expert, con
 // neither waits; the ends by 16-byte pieces (33 -> 16 us for a tile of two K steps).
 template <typename XT, int WF, int TF, int WW, int WT, bool EXACT, bool GATED, bool ROWS,
           bool DIRECT, bool RAGGED>
-__global__ __launch_bounds__(WW * WT * 64, WW * WT <= 4 ? 2 : 2) void matmul_tile(TileParams p)
+__global__ __launch_bounds__(WW * WT * 64, 2) void matmul_tile(TileParams p)
 {
     constexpr int NT = WW * WT * 64, BW = WW * WF * 16, BT = WT * TF * 16;
     constexpr int PW = BW * 8 / NT, PX = BT * 8 / NT;    // 16-byte chunks per thread
     constexpr int RL = NT / 8;                           // rows of one load of all threads
-    constexpr int STAGES = !DIRECT ? 1 : !EXACT && 3 * (BW + BT) * TK + 10240 <= LDS_BUDGET && BW > 128 ? 3 : 2;
+    // (three where they fit beside the scales; 128 x 128 has two workgroups per CU)
+    constexpr bool THREE = !EXACT && BW > 128 && 3 * (BW + BT) * TK + 10240 <= LDS_BUDGET;
+    constexpr int STAGES = !DIRECT ? 1 : THREE ? 3 : 2;
     constexpr uint32_t XB = BT * TK, WB = BW * TK, SB = XB + WB;
     constexpr int NX = (BT * SG + NT - 1) / NT;          // scale loads per thread
     constexpr uint32_t XS = NX * NT * 4, SS = XS + WW * WT * 256;
@@ -277,7 +279,8 @@ __global__ __launch_bounds__(WW * WT * 64, WW * WT <= 4 ? 2 : 2) void matmul_til
                          min(up0 / 128 + 1, blocks - 1)};
     const float *const sexp = a.scales + (long long)t.expert * a.s_stride + first_step;
     const int seg = min(lane / SG, 2);
-    const float *const wsrc = sexp + (long long)(seg == 0 ? sblk[0] : seg == 1 ? sblk[1] : sblk[2]) * a.ng;
+    const float *const wsrc =
+        sexp + (long long)(seg == 0 ? sblk[0] : seg == 1 ? sblk[1] : sblk[2]) * a.ng;
 
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem);
@@ -404,8 +407,8 @@ __global__ __launch_bounds__(WW * WT * 64, WW * WT <= 4 ? 2 : 2) void matmul_til
                         for (int h = 0; h < 4; h++)
                             z = __builtin_amdgcn_mfma_f32_16x16x32_f16(wh[h], xh[n][h], z, 0, 0, 0);
                     } else {
-                        z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[m & 1], xf[n], z, 0, 0,
-                                                                             0, 0, 0, 0);
+                        z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            wf[m & 1], xf[n], z, 0, 0, 0, 0, 0, 0);
                     }
                     g[m & 1][n] = z;
                 }
@@ -440,7 +443,8 @@ __global__ __launch_bounds__(WW * WT * 64, WW * WT <= 4 ? 2 : 2) void matmul_til
             auto read_scales = [&](int s) {
                 const char *const sc = smem + STAGES * SB + ((s / SG) & 1) * SS;
                 const float *const sl = reinterpret_cast<const float *>(sc) + s % SG;
-                const float *const wl = reinterpret_cast<const float *>(sc + XS + wave * 256) + s % SG;
+                const float *const wl =
+                    reinterpret_cast<const float *>(sc + XS + wave * 256) + s % SG;
 #pragma unroll
                 for (int n = 0; n < TA; n++) sx[n] = sl[((n * WT + wt) * 16 + li) * SG];
                 sw[0] = wl[0];
@@ -467,7 +471,7 @@ __global__ __launch_bounds__(WW * WT * 64, WW * WT <= 4 ? 2 : 2) void matmul_til
                 if (GATED) s1[GATED ? n : 0] = sx[n] * sw[1];
                 if (ROWS) s2[ROWS ? n : 0] = sx[n] * sw[2];
             };
-            static_assert(WF % WB2 == 0 && WF * TA % (LAG + 1) == 0, "buffers alternate over steps");
+            static_assert(WF % WB2 == 0 && WF * TA % (LAG + 1) == 0, "buffers alternate");
             __syncthreads();                                 // (earlier loads are done)
             load_scales(0);
             load_direct(0);
@@ -512,7 +516,8 @@ __global__ __launch_bounds__(WW * WT * 64, WW * WT <= 4 ? 2 : 2) void matmul_til
                                                             : 0;
                             wait_some(later);
                         }
-                        if (s + STAGES < steps && (s + STAGES) % SG == 0) load_scales((s + STAGES) / SG);
+                        if (s + STAGES < steps && (s + STAGES) % SG == 0)
+                            load_scales((s + STAGES) / SG);
                         char *const next = smem + (STAGES == 2 ? (s + 1) & 1 : (s + 1) % 3) * SB;
                         if (s + 2 == steps && rem < TK) {    // uniform over the workgroup
                             clear_tail(next);
@@ -584,7 +589,8 @@ __global__ __launch_bounds__(WW * WT * 64, WW * WT <= 4 ? 2 : 2) void matmul_til
                             uint32_t w = 0;
 #pragma unroll
                             for (int b = 0; b < 4; b++)
-                                if ((int)ch + 4 * j + b < rem) w |= (uint32_t)src[4 * j + b] << (8 * b);
+                                if ((int)ch + 4 * j + b < rem)
+                                    w |= (uint32_t)src[4 * j + b] << (8 * b);
                             v[j] = w;
                         }
                         return v;
@@ -600,7 +606,7 @@ __global__ __launch_bounds__(WW * WT * 64, WW * WT <= 4 ? 2 : 2) void matmul_til
             load_scales(0);
             fetch(0);
             for (int s = 0; s < steps; s++) {
-                wait_loads<0>();                             // scales; the last step's reads are done
+                wait_loads<0>();                         // scales; the last step's reads
 #pragma unroll
                 for (int i = 0; i < PX; i++)
                     *reinterpret_cast<u32x4 *>(smem + (tid + NT * i) * 16) = xv[i];

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void join_parts(TileParams p)
     const int row_ = blockIdx.y, c0 = p.col0 + blockIdx.x * 1024;
     const long long plane = (long long)a.R * p.ldp;
     const float *const at = p.partial + (long long)row_ * p.ldp;
-    finish<XT, 4>(a, 0, threadIdx.x, 256, 1024, [&](int i, int &row, int &col, float &v, float &up) {
+    auto sums = [&](int i, int &row, int &col, float &v, float &up) {
         row = row_;
         col = c0 + i;
         v = up = 0.0f;
@@ -51,7 +51,8 @@ __global__ __launch_bounds__(256) void join_parts(TileParams p)
             v += at[k * (GATED ? 2 : 1) * plane + col];
             if (GATED) up += at[(2 * k + 1) * plane + col];
         }
-    });
+    };
+    finish<XT, 4>(a, 0, threadIdx.x, 256, 1024, sums);
 }
 
 }  // namespace

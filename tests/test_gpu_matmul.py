@@ -411,3 +411,40 @@ def test_weights_and_rows_beyond_4_gb(q):
     ref, bound = reference(decode_weights(wx.cpu().numpy(), sx.cpu().numpy()),
                            decode_rows(w[pick.long()], ws[pick.long()]), torch.bfloat16)
     assert_within(y, ref, bound)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_parts_on_two_streams_and_replayed(q, dtype):
+    """Products cut along K, whose parts lie in a workspace: two at once, and captured,
+    against the same calls alone."""
+    S, I, O = 200, 7168, 520
+    w, s = weights((), O, I, 60)
+    wd, sd = cuda(w), cuda(s)
+    assert q.qgemv_matmul_workspace(S, I, O, 1 if dtype == "bf16" else 0, 0) > 0
+    sets = [tuple(cuda(t) for t in rows(S, I, 61 + i)) for i in range(3)]
+
+    def call(x, xs):
+        return q.fp8b128_matmul(wd, sd, x, xs, act="relu", dtype=DT[dtype])
+    alone = [call(*v).clone() for v in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append(call(*sets[i]))
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(got[i], alone[i])
+    fixed = [t.clone() for t in sets[0]]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = call(*fixed)
+    for i in (1, 2, 0, 1):
+        for t, v in zip(fixed, sets[i]):
+            t.copy_(v)
+        g.replay()
+        eager = call(*sets[2])
+        torch.cuda.synchronize()
+        assert torch.equal(y, alone[i]) and torch.equal(eager, alone[2])
