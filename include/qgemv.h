@@ -445,7 +445,7 @@ int qgemv_fp8_quantize(const void *x, long long ldx, int S, int I, int dtype, vo
  * format, so the gradient of x is the same call on those and on the quantized
  * gradient of y.
  * A NaN code or scale makes what it meets NaN.  The product of two scales that
- * meet must be in f32's range.
+ * meet must be in f32's normal range (where codes other than zero meet).
  */
 size_t qgemv_matmul_workspace(int S, int I, int O, int dtype, int gated);
 int qgemv_fp8b128_matmul(const void *w, const float *scale_inv, const void *x, long long ldx,
