@@ -884,9 +884,10 @@ def moe_combine(h, pos, gates, residual=None, out=None):
 # Codes are uint8 (or float8_e4m3fn, whose bytes they are).  x and its scales, and
 # the rows of routed tensors, may be row-strided views.
 def _codes(t, name):
-    """t's bytes, uint8."""
+    """t's bytes, uint8 (a view of those forgets that t asks for a gradient)."""
     torch = _torch()
     if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
+        _no_gradient(t)
         return t.view(torch.uint8)
     return t
 
@@ -906,7 +907,7 @@ def fp8_quantize(x, out=None, scales=None):
         scales = scales.unsqueeze(0) if scales is not None and scales.dim() == 1 else scales
     S, I = x.shape
     _sizes("qgemv_fp8_quantize", S, I)
-    _no_gradient(x, scales)
+    _no_gradient(x, out, scales)
     _one_device(x, out, scales)
     xp, ldx = _rows(x, "x", x.dtype)
     ng = -(-I // 128)
