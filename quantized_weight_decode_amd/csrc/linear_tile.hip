@@ -32,7 +32,7 @@ __device__ __forceinline__ void load8(const typename XT::raw *src, bool vec, flo
 {
     typedef typename XT::raw raw;
     if (vec) {
-        typedef raw rawx8 __attribute__((ext_vector_type(8)));
+        typedef typename Eight<raw>::type rawx8;
         const rawx8 t = *reinterpret_cast<const rawx8 *>(src);
 #pragma unroll
         for (int j = 0; j < 8; j++) v[j] = XT::get(t[j]);

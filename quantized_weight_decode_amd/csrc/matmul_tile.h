@@ -63,7 +63,7 @@ __device__ __forceinline__ void finish_rows_act(const LinearArgs &a, int expert,
                                                 int lane, int n, int col0, Row row_of)
 {
     typedef typename XT::raw raw;
-    typedef raw piece __attribute__((ext_vector_type(8)));
+    typedef typename Eight<raw>::type piece;
     constexpr int LPR = WC / 8;
     const int oc = GATED ? a.O / 2 : a.O, c = lane % LPR * 8, col = col0 + c;
     if (col >= oc) return;

@@ -13,6 +13,15 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+// Eight consecutive elements of a row on 16 bytes.  (A vector of eight floats would
+// promise the compiler 32, which no caller checks.)
+template <typename R>
+struct Eight {
+    typedef R type __attribute__((ext_vector_type(8), aligned(16)));
+};
+static_assert(alignof(Eight<float>::type) == 16 && alignof(Eight<uint16_t>::type) == 16,
+              "loads and stores of eight need 16 bytes");
+
 constexpr int WAVE = 64;
 
 // s_waitcnt operands (gfx9 encoding: vmcnt in bits 3:0 and 15:14, expcnt in

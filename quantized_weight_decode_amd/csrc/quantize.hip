@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void quantize(const typename XT::raw *__restri
     const bool whole = c + 8 <= I;
     float v[8];
     if (VEC && whole) {
-        typedef raw rawx8 __attribute__((ext_vector_type(8)));
+        typedef typename Eight<raw>::type rawx8;
         const rawx8 t = *reinterpret_cast<const rawx8 *>(src);
 #pragma unroll
         for (int j = 0; j < 8; j++) v[j] = XT::get(t[j]);
