@@ -69,34 +69,14 @@ long long most_tiles(int R, int E, int bm)
 }
 
 // The kernel of a product, its row tiles and its launch's work items.
-struct Choice {
-    bool tile;
-    TilePlan plan;
-    int bm;
+struct Choice : MatmulPlan {
     long long mt, items;
 };
 
-// The tile kernel, or up to 64 rows the stream kernel where it is estimated to be
-// faster: 7 us and its weights at 5 TB/s, 1, 1.8 or 3.2 times for tiles of 16, 32 or
-// 64 rows (whose products take the longer part).  us, stream and tile: 5 x 16384 x
-// 7168 31.4 and 27.8, 5 x 4096 x 4096 13.7 and 26, 64 x 6144 x 12288 64 and 24.  (Up
-// to 16 rows of weights below 64 MB always, without estimating.)  Grouped by expert
-// the tile kernel from 17 rows on: 4 tokens of 8 of 256 experts, 7168 x 2048, 91 and
-// 81, 1 token 32 and 43.
 Choice choose(const MatmulArgs &p, bool fits, bool direct)
 {
-    Choice c{};
     const LinearArgs &a = p.a;
-    const int rows = a.offsets ? (a.R + a.E - 1) / a.E : a.R;
-    const double bytes = a.O * (double)a.I;
-    c.bm = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    if (fits && (a.offsets ? a.R > 16 : rows > 16 || bytes > 64e6)) {
-        c.plan = matmul_tile_plan(p, direct);
-        const double w = c.bm == 16 ? 1.0 : c.bm == 32 ? 1.8 : 3.2;
-        c.tile = a.offsets || rows > 64 || c.plan.us < 7.0 + w * bytes / 5e6;
-    }
-    if (c.tile) c.bm = matmul_tile_rows(c.plan.kind);
-    else c.plan.parts = 1;
+    Choice c{plan_matmul(sizes_of(p), fits, direct, cu_count()), 0, 0};
     c.mt = a.offsets ? most_tiles(a.R, a.E, c.bm) : (a.R + c.bm - 1) / c.bm;
     c.items = c.tile ? matmul_tile_items(p, c.plan, c.mt)
                      : matmul_stream_items(p, c.bm, c.mt);

@@ -34,7 +34,7 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int TK = 128;                  // columns per K step: one scale block
-constexpr int SG = 4;                    // K steps whose scales are fetched together
+constexpr int SG = SCALE_STEPS;          // K steps whose scales are fetched together
 
 // All but the wave's last n loads have arrived, and its LDS reads are done, for every
 // wave of the workgroup (n uniform; more than 9: as if 0).

@@ -1,5 +1,5 @@
-// matmul_tile.hip -- the tile kernel of 8-bit products (matmul_tile.h): which kind of
-// tile and how many parts of K a product takes, the launch, and the parts joined.
+// matmul_tile.hip -- the tile kernel of 8-bit products (matmul_tile.h): its launches by
+// a plan (qg_matmul_plan.h), and the parts of K joined.
 #include "matmul_tile.h"
 
 namespace qg {
@@ -20,17 +20,6 @@ bool matmul_tile_fits(const MatmulArgs &p)
 }
 
 namespace {
-
-struct Kind {
-    int bt, bw, waves;                   // rows of x, rows of W, waves
-    double step, fixed;                  // us per K step and per tile
-};
-const Kind KINDS[] = {{256, 256, 8, 1.5, 14.0},
-                      {192, 256, 8, 1.27, 13.0},
-                      {128, 256, 8, 0.97, 12.0},
-                      {64, 256, 8, 0.64, 10.0},
-                      {128, 128, 4, 1.0, 10.0}};
-constexpr int SQUARE = 4;                // the only one for f32, or rows that are not on 16 bytes
 
 // The sums of K's parts joined, in their order, and the ends: a thread has four
 // outputs of a row in flight.
@@ -57,92 +46,24 @@ __global__ __launch_bounds__(256) void join_parts(TileParams p)
 
 }  // namespace
 
-int matmul_tile_rows(int kind) { return KINDS[kind].bt; }
-
 size_t matmul_part_bytes(const MatmulArgs &p, int parts)
 {
     const int oc = p.a.gated ? p.a.O / 2 : p.a.O;
     return parts > 1 ? (size_t)parts * (p.a.gated ? 2 : 1) * p.a.R * ((oc + 3) / 4 * 4) * 4 : 0;
 }
 
-// Tiles of n columns of y by R rows, and the time of `parts` parts of each, one
-// workgroup (of the square kind two) per CU at a time; joining parts costs a launch
-// and their sums' way to memory and back.
-static long long tiles_of(const MatmulArgs &p, int kind, int n)
-{
-    const Kind &k = KINDS[kind];
-    const int cols = k.bw / (p.a.gated ? 2 : 1);
-    return (long long)((p.a.R + k.bt - 1) / k.bt) * ((n + cols - 1) / cols);
-}
-
-// The plan of n columns in one launch: the kind, and the parts of K where tiles leave
-// CUs without work, for which the busiest CU ends first (1501 x 16384 x 7168, 168
-// tiles: 236 us, in three parts 259).
-static TilePlan plan_columns(const MatmulArgs &p, bool any, int n, long long ncu)
-{
-    const LinearArgs &a = p.a;
-    TilePlan best{};
-    best.us = -1.0;
-    for (int i = any ? 0 : SQUARE; i <= SQUARE; i++) {
-        const Kind &k = KINDS[i];
-        const long long tiles = tiles_of(p, i, n), slots = i == SQUARE ? 2 * ncu : ncu;
-        const double c = a.dtype == QGEMV_F32 ? 2 * k.step : k.step;
-        for (const int f : {1, 2, 3, 4, 6, 8, 12, 16}) {
-            if (f > 1 && (tiles * f > slots || a.R > 4096)) break;
-            const int per = ((a.ng + f - 1) / f + SG - 1) / SG * SG;
-            if ((a.ng + per - 1) / per != f) continue;
-            double us = (double)((tiles * f + slots - 1) / slots) *
-                        ((f > 1 ? per : a.ng) * c + k.fixed);
-            if (f > 1) us += 5.0 + 8e-6 * f * a.R * (double)a.O / 5.0;
-            if (best.us < 0.0 || us < best.us) best = TilePlan{i, f, 0, 0, us};
-        }
-    }
-    return best;
-}
-
-// Dense: the faster of one launch and of two, the first with as many columns as give
-// every CU the same number of one kind's tiles, the second with the rest, by what suits
-// that.  us: 2048 x 6144 x 12288, 384 tiles of 256 x 256 at once 157 (gated 170), 256 of
-// them and the rest in tiles of 128 x 256 152 (160).
-// Grouped by expert 128 x 256, whose three stages suit experts of few rows, bound by
-// their weights' bytes, up to 512 rows per expert.
-TilePlan matmul_tile_plan(const MatmulArgs &p, bool direct)
-{
-    const LinearArgs &a = p.a;
-    const bool any = a.dtype == QGEMV_BF16 && direct;
-    if (a.offsets) return TilePlan{!any ? SQUARE : a.R / a.E < 512 ? 2 : 0, 1, 0, 0, 0.0};
-    const int oc = a.gated ? a.O / 2 : a.O;
-    const long long ncu = cu_count();
-    TilePlan best = plan_columns(p, any, oc, ncu);
-    for (int i = 0; any && i < SQUARE; i++) {
-        const Kind &k = KINDS[i];
-        const int cols = k.bw / (a.gated ? 2 : 1);
-        const long long ntm = (a.R + k.bt - 1) / k.bt, rounds = tiles_of(p, i, oc) / ncu;
-        const long long head = rounds * ncu / ntm * cols;
-        if (rounds < 1 || head < cols || head >= oc) continue;
-        const double us = rounds * (a.ng * k.step + k.fixed) + 7.0;
-        if (us >= best.us) continue;
-        TilePlan rest = plan_columns(p, any, oc - (int)head, ncu);
-        rest.us += us;
-        rest.head = (int)head;
-        rest.head_kind = i;
-        if (rest.us < best.us) best = rest;
-    }
-    return best;
-}
-
 // Workgroups of a launch of n columns, and tiles across them.  Grouped: any number of
 // tiles up to ntm may hold rows, and they are dealt to the XCDs in runs of up to 32.
 static long long tile_grid(const MatmulArgs &p, int kind, int parts, int n, long long ntm, int &ntn)
 {
-    const int cols = KINDS[kind].bw / (p.a.gated ? 2 : 1);
+    const int cols = TILE_KINDS[kind].bw / (p.a.gated ? 2 : 1);
     ntn = (n + cols - 1) / cols;
     return p.a.offsets ? (ntm * ntn / 8 + 32) * 8 : ntm * ntn * parts;
 }
 
 static long long row_tiles(const MatmulArgs &p, int kind)
 {
-    return (p.a.R + KINDS[kind].bt - 1) / KINDS[kind].bt;
+    return (p.a.R + TILE_KINDS[kind].bt - 1) / TILE_KINDS[kind].bt;
 }
 
 long long matmul_tile_items(const MatmulArgs &p, const TilePlan &plan, long long ntm)
@@ -150,11 +71,11 @@ long long matmul_tile_items(const MatmulArgs &p, const TilePlan &plan, long long
     const int oc = p.a.gated ? p.a.O / 2 : p.a.O;
     int ntn;
     const long long n = tile_grid(p, plan.kind, plan.parts, oc - plan.head, ntm, ntn) *
-                        KINDS[plan.kind].waves * 64;
+                        TILE_KINDS[plan.kind].waves * 64;
     if (!plan.head) return n;
     const long long m =
         tile_grid(p, plan.head_kind, 1, plan.head, row_tiles(p, plan.head_kind), ntn) *
-        KINDS[plan.head_kind].waves * 64;
+        TILE_KINDS[plan.head_kind].waves * 64;
     return n > m ? n : m;
 }
 
@@ -171,7 +92,7 @@ static hipError_t launch_columns(const MatmulArgs &m, int kind, int parts, int c
     const unsigned grid = (unsigned)tile_grid(m, kind, parts, n, ntm, p.ntn);
     const int oc = a.gated ? a.O / 2 : a.O;
     p.parts = parts;
-    p.per = parts > 1 ? ((a.ng + parts - 1) / parts + SG - 1) / SG * SG : a.ng;
+    p.per = parts > 1 ? steps_per_part(a.ng, parts) : a.ng;
     // every part has steps, and a place for its sums
     if ((parts - 1) * (long long)p.per >= a.ng || (parts > 1 && !ws)) return hipErrorInvalidValue;
     p.partial = static_cast<float *>(ws);

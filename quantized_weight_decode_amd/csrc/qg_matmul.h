@@ -4,6 +4,7 @@
 #pragma once
 
 #include "qg_linear.h"
+#include "qg_matmul_plan.h"
 
 namespace qg {
 
@@ -14,6 +15,12 @@ struct MatmulArgs {
     const float *xs;                     // [T][ldxs], a scale per 128 columns
     long long ldxs;
 };
+
+inline MatmulSizes sizes_of(const MatmulArgs &p)
+{
+    const LinearArgs &a = p.a;
+    return {a.R, a.offsets ? a.E : 0, a.I, a.O, a.dtype == QGEMV_BF16, a.gated != 0};
+}
 
 // One row tile of a grouped product: rows [row0, row0 + n) of y, of one expert,
 // whose `count` tiles start at tile `first` of the list.  The list is in the order
@@ -34,20 +41,11 @@ long long matmul_stream_items(const MatmulArgs &p, int bm, long long ntm);
 hipError_t launch_matmul_stream(const MatmulArgs &p, int bm, const ExpertTile *tiles, int ntm,
                                 hipStream_t st);
 
-// How the tile kernel takes a product: tiles of `kind`, K in `parts` (dense); the
-// first `head` columns of y, if any, by a launch of their own, of `head_kind`.
-struct TilePlan {
-    int kind, parts, head, head_kind;
-    double us;                           // estimated (dense)
-};
-
 // The tile kernel (matmul_tile.hip): whether it takes a product, and by
-// memory-to-LDS loads; its plan; the rows of a kind's tiles, the bytes of the parts'
-// sums, the work items of the larger launch.
+// memory-to-LDS loads; the bytes of the parts' sums, the work items of the larger
+// launch of a plan.
 bool matmul_tile_fits(const MatmulArgs &p);
 bool matmul_tile_direct(const MatmulArgs &p);
-TilePlan matmul_tile_plan(const MatmulArgs &p, bool direct);
-int matmul_tile_rows(int kind);
 size_t matmul_part_bytes(const MatmulArgs &p, int parts);
 long long matmul_tile_items(const MatmulArgs &p, const TilePlan &plan, long long ntm);
 hipError_t launch_matmul_tile(const MatmulArgs &p, const TilePlan &plan, const ExpertTile *tiles,
