@@ -695,18 +695,24 @@ __global__ __launch_bounds__(WW * WT * 64, 2) void matmul_tile(TileParams p)
     }
 }
 
-template <typename XT, int WF, int TF, int WW, int WT, bool EXACT, bool DIRECT>
+// GROUPED: plan_tiles gives grouped products this kind, too.
+template <typename XT, int WF, int TF, int WW, int WT, bool EXACT, bool DIRECT, bool GROUPED>
 hipError_t run_tile(const TileParams &p, unsigned grid, hipStream_t st)
 {
     const LinearArgs &a = p.m.a;
     constexpr int NT = WW * WT * 64, WC = WF * 8;        // gated: columns of y per wave
+    if (p.tiles && !GROUPED) return hipErrorInvalidValue;
 #define QG_RUN1(G, R, N)                                                                    \
     hipLaunchKernelGGL((matmul_tile<XT, WF, TF, WW, WT, EXACT, G, R, DIRECT, N>), dim3(grid), \
                        dim3(NT), 0, st, p)
 #define QG_RUN(G, R)                                                                        \
     do {                                                                                    \
-        if (p.tiles) QG_RUN1(G, R, true);                                                   \
-        else QG_RUN1(G, R, false);                                                          \
+        if constexpr (GROUPED)                                                              \
+            if (p.tiles) {                                                                  \
+                QG_RUN1(G, R, true);                                                        \
+                break;                                                                      \
+            }                                                                               \
+        QG_RUN1(G, R, false);                                                               \
     } while (0)
     if (!a.gated) QG_RUN(false, false);
     else if (a.O / 2 % WC == 0) QG_RUN(true, false);     // a wave's up rows share a scale block

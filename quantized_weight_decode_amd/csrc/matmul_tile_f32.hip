@@ -5,8 +5,8 @@ namespace qg {
 
 hipError_t run_tile_f32(const TileParams &p, bool direct, unsigned grid, hipStream_t st)
 {
-    return direct ? run_tile<F32, 4, 4, 2, 2, true, true>(p, grid, st)
-                  : run_tile<F32, 4, 4, 2, 2, true, false>(p, grid, st);
+    return direct ? run_tile<F32, 4, 4, 2, 2, true, true, true>(p, grid, st)
+                  : run_tile<F32, 4, 4, 2, 2, true, false, true>(p, grid, st);
 }
 
 }  // namespace qg

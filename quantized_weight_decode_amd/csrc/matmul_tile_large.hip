@@ -5,8 +5,8 @@ namespace qg {
 
 hipError_t run_tile_large(const TileParams &p, int kind, unsigned grid, hipStream_t st)
 {
-    return kind == 0 ? run_tile<BF16, 8, 4, 2, 4, false, true>(p, grid, st)
-                     : run_tile<BF16, 8, 3, 2, 4, false, true>(p, grid, st);
+    return kind == 0 ? run_tile<BF16, 8, 4, 2, 4, false, true, true>(p, grid, st)
+                     : run_tile<BF16, 8, 3, 2, 4, false, true, false>(p, grid, st);
 }
 
 }  // namespace qg

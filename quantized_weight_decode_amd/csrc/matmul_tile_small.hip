@@ -5,8 +5,8 @@ namespace qg {
 
 hipError_t run_tile_small(const TileParams &p, int kind, unsigned grid, hipStream_t st)
 {
-    return kind == 2 ? run_tile<BF16, 8, 2, 2, 4, false, true>(p, grid, st)
-                     : run_tile<BF16, 8, 1, 2, 4, false, true>(p, grid, st);
+    return kind == 2 ? run_tile<BF16, 8, 2, 2, 4, false, true, true>(p, grid, st)
+                     : run_tile<BF16, 8, 1, 2, 4, false, true, false>(p, grid, st);
 }
 
 }  // namespace qg

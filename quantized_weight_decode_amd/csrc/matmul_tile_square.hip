@@ -5,8 +5,8 @@ namespace qg {
 
 hipError_t run_tile_square(const TileParams &p, bool direct, unsigned grid, hipStream_t st)
 {
-    return direct ? run_tile<BF16, 4, 4, 2, 2, false, true>(p, grid, st)
-                  : run_tile<BF16, 4, 4, 2, 2, false, false>(p, grid, st);
+    return direct ? run_tile<BF16, 4, 4, 2, 2, false, true, false>(p, grid, st)
+                  : run_tile<BF16, 4, 4, 2, 2, false, false, true>(p, grid, st);
 }
 
 }  // namespace qg
