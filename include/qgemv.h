@@ -431,7 +431,11 @@ int qgemv_fp8_quantize(const void *x, long long ldx, int S, int I, int dtype, vo
  *   dtype  of y, bias and residual;  any I >= 1, O >= 1, any alignment of w and x
  *   y must not overlap what the call reads, but for the residual in place
  *   workspace  qgemv_matmul_workspace bytes (may be 0: then it may be NULL), 256-byte
- *              aligned, overwritten; calls that may overlap in time need one each
+ *              aligned, overwritten; calls that may overlap in time need one each.
+ *              It holds sums of parts of K, into which products of few tiles are cut:
+ *              fewer rows may need more of it (bf16, 7168 x 7168 on 256 CUs: 512 rows
+ *              29 MB, 1024 rows none), so ask for every S, and reserve the largest
+ *              answer for calls of several S; it goes by the current device's CUs
  * Products of two codes are exact, the sum over blocks is f32 and y is rounded once.
  * A block's products are summed in f32 for f32 results and for few rows (up to 16 of
  * weights below 64 MB; up to 64, and of larger weights, by size).  Those of more

@@ -953,7 +953,8 @@ def _result(out, R, oc, dtype, device):
 
 
 def matmul_workspace(S, I, O, dtype, device, gated=False):
-    """Scratch for one fp8b128_matmul call of these sizes."""
+    """Scratch for one fp8b128_matmul call of these sizes, on ``device``.  Fewer rows
+    may need more: for calls of several S, the largest of theirs."""
     torch = _torch()
     code = _dtype_code(torch.empty(0, dtype=dtype), "dtype")
     return torch.empty(max(int(qgemv_matmul_workspace(S, I, O, code, int(bool(gated)))), 1),

@@ -29,8 +29,8 @@ struct ExpertTile {
     int expert, row0, n, first, count, filled, pad[2];
 };
 
-// Workspace bytes: of a dense product (a function of these sizes only), and of a
-// grouped one.
+// Workspace bytes: of a dense product (by these sizes and the device's CUs; not
+// monotone in S), and of a grouped one (by its sizes only).
 size_t matmul_workspace(int S, int I, int O, int dtype, int gated);
 size_t matmul_grouped_workspace(int R, int E);
 bool matmul_launchable(const MatmulArgs &p);
