@@ -956,9 +956,12 @@ def matmul_workspace(S, I, O, dtype, device, gated=False):
     """Scratch for one fp8b128_matmul call of these sizes, on ``device``.  Fewer rows
     may need more: for calls of several S, the largest of theirs."""
     torch = _torch()
+    _sizes("qgemv_matmul_workspace", S, I, O)
     code = _dtype_code(torch.empty(0, dtype=dtype), "dtype")
-    return torch.empty(max(int(qgemv_matmul_workspace(S, I, O, code, int(bool(gated)))), 1),
-                       dtype=torch.uint8, device=device)
+    device = torch.device(device)
+    with _on(device) if device.index is not None else _NO_GUARD:
+        need = int(qgemv_matmul_workspace(S, I, O, code, int(bool(gated))))
+    return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
 
 
 def fp8b128_matmul(w, scale_inv, x, x_scale, bias=None, act=None, gated=False, residual=None,
@@ -1002,6 +1005,7 @@ def fp8b128_matmul(w, scale_inv, x, x_scale, bias=None, act=None, gated=False, r
 
 def matmul_grouped_workspace(R, E, device):
     """Scratch for one fp8b128_matmul_grouped call of these sizes."""
+    _sizes("qgemv_matmul_grouped_workspace", R, E)
     return _torch().empty(max(int(qgemv_matmul_grouped_workspace(R, E)), 1),
                           dtype=_torch().uint8, device=device)
 

@@ -65,3 +65,38 @@ def test_codes_that_ask_for_none(q, name, call):
             return asks(*shape)
     with torch.no_grad(), pytest.raises((TypeError, ValueError), match="CUDA|devices"):
         call(q, made)
+
+
+def test_scratch_sizes(q):
+    """Sizes that a C int would wrap are refused, and a product's scratch is asked for
+    with its device current, by whose CUs it goes."""
+    for f in (lambda n: q.matmul_workspace(n, 7168, 7168, torch.bfloat16, "cpu"),
+              lambda n: q.matmul_workspace(300, n, 7168, torch.bfloat16, "cpu"),
+              lambda n: q.matmul_workspace(300, 7168, n, torch.bfloat16, "cpu"),
+              lambda n: q.matmul_grouped_workspace(n, 8, "cpu"),
+              lambda n: q.matmul_grouped_workspace(300, n, "cpu")):
+        for n in ((1 << 32) + 300, -1):
+            with pytest.raises(q.QgemvError) as e:
+                f(n)
+            assert e.value.status == 2
+    ws = q.matmul_workspace(300, 7168, 7168, torch.bfloat16, "cpu")
+    assert ws.numel() == q.qgemv_matmul_workspace(300, 7168, 7168, 1, 0)
+
+
+def test_scratch_goes_by_its_device(q, monkeypatch):
+    current, asked = [0], []
+
+    class Guard:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+    monkeypatch.setattr(q, "_on", Guard)
+    monkeypatch.setattr(q, "qgemv_matmul_workspace",
+                        lambda *_: asked.append(current[0]) or 4096)
+    q.matmul_workspace(300, 7168, 7168, torch.bfloat16, torch.device("meta", 3))
+    assert asked == [3] and current == [0]
