@@ -1,6 +1,7 @@
 // route_grad.hip -- token rows put in expert order, the gradient of that, and
 // the gradient of the experts' gate-weighted return.
 #include "qg_device.h"
+#include "qg_launch.h"
 #include "qg_matmul.h"
 
 namespace qg {
@@ -300,9 +301,10 @@ hipError_t launch_moe_combine_grad(const void *dy, long long lddy, const void *h
     const bool wide = aligned16((uintptr_t)dy | (uintptr_t)h | (uintptr_t)dh |
                                 (uintptr_t)(lddy * el) | (uintptr_t)(ldh * el) |
                                 (uintptr_t)(lddh * el));
-    // eight slots per workgroup, two where eight would leave CUs without work (33
-    // tokens of 8, 2048 f32: 12.7 us in eights)
-    const bool few = (long long)T * ((K + 7) / 8) < 256;
+    // eight slots per workgroup, two where eight would leave CUs without work.  Twos and
+    // eights, us: kernel of 33 tokens of 8, 2048 f32 4.8 and 12.7; calls of 7168 bf16, 200
+    // tokens 14.2 and 14.6, 300 17.1 and 20.7, 512 26.5 and 25.6, 1024 47.1 and 44.9
+    const bool few = (long long)T * ((K + 7) / 8) < cu_count();
     const int nkb = few ? (K + 1) / 2 : (K + 7) / 8;
 #define QG_GRAD(XT, VEC)                                                                    \
     do {                                                                                    \
