@@ -970,8 +970,11 @@ def fp8b128_matmul(w, scale_inv, x, x_scale, bias=None, act=None, gated=False, r
     f32 [ceil(O/128)][ceil(I/128)], x and x_scale as ``fp8_quantize`` gives them
     ([S][I], or [I]).  y [S][O] (gated: O/2 columns) of ``dtype``, float32 or
     bfloat16: by default the type of out, residual or bias, else bfloat16.
-    The gradient of x is the product with w.t().contiguous() and
-    scale_inv.t().contiguous(), which are W^T in the same format."""
+    The gradient of x through the product alone (no act, no gate) is the product
+    with w.t().contiguous() and scale_inv.t().contiguous(), which are W^T in the same
+    format.  bfloat16 results of many rows carry some 5e-5 of their sums' norm beside
+    their rounding, float32 ones do not.  Up to some 32 rows that are not quantized
+    anyway, ``fp8b128_linear`` is faster."""
     torch = _torch()
     w, x = _codes(w, "w"), _codes(x, "x")
     one = x.dim() == 1
@@ -1051,7 +1054,8 @@ def fp8b128_matmul_grouped(w, scale_inv, x, x_scale, offsets, rows=None, bias=No
 def moe_dispatch(x, tokens, out=None):
     """Token rows in expert order: y[r] = x[tokens[r]], x [T][I] f32 or bf16, tokens
     int32 [R] as ``moe_group`` gives; rows of index -1 are left as they are in
-    ``out``."""
+    ``out`` (a new y's are not set).  The grouped products read x through ``rows``
+    without this copy."""
     torch = _torch()
     code = _dtype_code(x, "x")
     if x.dim() != 2 or tokens.dim() != 1:

@@ -65,8 +65,8 @@ struct Codes {
 // scale block's products are summed from zero and added as acc += (xs ws) sum.
 // f16's matrix cores sum to f32's precision; those of e4m3 do not (matmul_tile.h),
 // and where the weights' bytes bound the product nothing is gained by them.
-// Bound by the bytes in flight: 5 x 6144 x 12288 22 us a call (75 MB, 3.4 TB/s), 3 x 512
-// x 256 5.2 us of kernel, its latency.
+// Bound by the bytes in flight: 5 x 6144 x 12288 22 us a call for f32 (75 MB, 3.4 TB/s),
+// 25 for bf16; 3 x 512 x 256 4.9 us of kernel, its latency.
 template <typename XT, int MB, int NB, bool GATED>
 __global__ __launch_bounds__(SW * 64, 2) void matmul_stream(MatmulArgs p,
                                                             const ExpertTile *__restrict__ tiles)

@@ -158,8 +158,8 @@ __device__ __forceinline__ void finish_rows(const LinearArgs &a, int expert, con
 //
 // 256 x 256 x 8 waves: a wave reads 12 fragments (24 KB) of LDS for 32 matrix
 // instructions of 32 cycles; 128 x 128 of 4 waves, two workgroups per CU, reads 16 KB
-// for 16.  4096 x 8192 x 8192 takes 249 us (2200 TFLOP/s) in tiles of 256, 285 of 192,
-// 312 of 128 and 320 of 128 x 128; the library's e4m3 product of the size, without
+// for 16.  4096 x 8192 x 8192 takes 240 us (2290 TFLOP/s) in tiles of 256, 293 of 192,
+// 297 of 128 and 317 of 128 x 128; the library's e4m3 product of the size, without
 // block scales, 189.  Bound by the matrix cores, LDS reads and the card's power
 // together: matrix cores busy 61 % of the cycles at 1.76 GHz (without the LDS loads 66 %
 // at 1.96, without the reads either 203 -> 180 us), a tile's start and end 13 us.

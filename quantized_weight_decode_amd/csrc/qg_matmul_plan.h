@@ -49,9 +49,10 @@ inline long long tiles_of(const MatmulSizes &p, int kind, int n)
 }
 
 // The plan of n columns in one launch: the kind, and the parts of K where tiles leave
-// CUs without work, for which the busiest CU ends first (1501 x 16384 x 7168, 168
-// tiles: 236 us, in three parts 259).  One workgroup (of the square kind two) per CU at
-// a time; joining parts costs a launch and their sums' way to memory and back.
+// CUs without work, for which the busiest CU ends first (1501 x 16384 x 7168: 224 tiles
+// of 192 rows 196 us, 168 of 256 rows 219, those in three parts 236).  One workgroup (of
+// the square kind two) per CU at a time; joining parts costs a launch and their sums'
+// way to memory and back.
 inline TilePlan plan_columns(const MatmulSizes &p, bool any, int n, long long ncu)
 {
     const int steps = p.steps();
@@ -77,10 +78,16 @@ inline TilePlan plan_columns(const MatmulSizes &p, bool any, int n, long long nc
 // The tile kernel's plan; direct: rows of both operands on 16 bytes.
 // Dense: the faster of one launch and of two, the first with as many columns as give
 // every CU the same number of one kind's tiles, the second with the rest, by what suits
-// that.  us: 2048 x 6144 x 12288, 384 tiles of 256 x 256 at once 157 (gated 170), 256 of
-// them and the rest in tiles of 128 x 256 152 (160).
+// that.  us: 2048 x 6144 x 12288, 384 tiles of 256 x 256 at once 177 (gated 179); 256 of
+// them, then the rest in 512 of 128 x 128 159 (161), in 256 of 128 x 256, whose estimate
+// is 0.6 higher, 157 (159); 2040 x 6144 x 12290 at once 206 (211), the rest in tiles of
+// 192 rows 197 (201).
 // Grouped by expert 128 x 256, whose three stages suit experts of few rows, bound by
-// their weights' bytes, up to 512 rows per expert.
+// their weights' bytes, up to 512 rows per expert on average.  us, 128 and 256 rows per
+// tile, unevenly routed: 64 experts of 7168 x 2048 with 128 rows each 275 and 294, 256
+// rows 428 and 387, 512 rows 704 and 590, 1024 rows 1223 and 1023; 8 experts with 128
+// rows 66 and 88, 384 rows 79 and 106, 512 rows 130 and 105.  (Between 256 and 512 rows
+// many experts would gain from 256, few would lose.)
 inline TilePlan plan_tiles(const MatmulSizes &p, bool direct, long long ncu)
 {
     const bool any = p.bf16 && direct;
@@ -113,11 +120,14 @@ struct MatmulPlan {
 
 // The tile kernel, or up to 64 rows the stream kernel where it is estimated to be
 // faster: 7 us and its weights at 5 TB/s, 1, 1.8 or 3.2 times for tiles of 16, 32 or
-// 64 rows (whose products take the longer part).  us, stream and tile: 5 x 16384 x
-// 7168 31.4 and 27.8, 5 x 4096 x 4096 13.7 and 26, 64 x 6144 x 12288 64 and 24.  (Up
-// to 16 rows of weights below 64 MB always, without estimating.)  Grouped by expert
-// the tile kernel from 17 rows on: 4 tokens of 8 of 256 experts, 7168 x 2048, 91 and
-// 81, 1 token 32 and 43.
+// 64 rows (whose products take the longer part).  us of a call by stream and tile, bf16
+// results (f32): 5 x 16384 x 7168 34 and 31 (34 and 40), 16 rows 43 and 32 (43 and 41),
+// 5 x 4096 x 4096 15 and 19 (15 and 19), 64 x 6144 x 12288 66 and 30 (65 and 35).  (Up
+// to 16 rows of weights below 64 MB always, without estimating: 16 x 4096 x 4096.)
+// Grouped by expert the tile kernel from 17 rows on: of 256 experts, 7168 x 2048, 16
+// rows 62 and 65 (61 and 67), 32 rows 107 and 94 (107 and 95), 128 rows 261 and 235 (262
+// and 248).  Where experts are few that is too early: of 8, 32 rows 33 and 51 (33 and
+// 55), 64 rows 42 and 53 (42 and 56).
 // fits: the tile kernel's offsets are within 32 bits.
 inline MatmulPlan plan_matmul(const MatmulSizes &p, bool fits, bool direct, long long ncu)
 {
