@@ -21,7 +21,8 @@ def test_every_way_but_the_rarest_is_among_them():
     """All kinds in one launch, whole and in parts, plain and gated; and behind a first
     launch all but 256 rows, which come there only in parts of very long K."""
     def some(kind, cut, head):
-        return {g for k, c, h, *_, g in REACHED if k == kind and c == cut and (h is not None) == head}
+        return {g for k, c, h, *_, g in REACHED
+                if (k, c, h is not None) == (kind, cut, head)}
     for kind in range(5):
         assert some(kind, False, False) == some(kind, True, False) == {False, True}
     for kind in range(1, 5):
